@@ -216,7 +216,6 @@ def _block_values(codes, scales):
 def _plain_layer(st):
     c = st["case"]
     T, d, E, k, E_local, F = (c[n] for n in ("T", "d", "E", "k", "E_local", "F"))
-    out = {}
     if c["route"]:
         # 64 bits: an expert next to the k-th place must not change sides
         logits = st["x"].double() @ st["w_router"].double()
@@ -226,7 +225,6 @@ def _plain_layer(st):
         p = torch.exp(logits - logits.amax(dim=1, keepdim=True))
         gates = (p.gather(1, order) / p.sum(dim=1, keepdim=True)).float()
         ids = order.to(torch.int32)
-        out["topk_ids"], out["topk_w"] = ids, gates
     else:
         ids, gates = st["ids"], st["gates"]
     # gate of every (token, local expert) pair, 0 where the token did not choose it
@@ -244,8 +242,7 @@ def _plain_layer(st):
     gate, up = gu[:, :, :F], gu[:, :, F:]
     h = gate / (1.0 + torch.exp(-gate)) * up * dense[:, :, None]
     y = torch.bmm(h.transpose(0, 1).contiguous(), down.transpose(1, 2).contiguous()).sum(dim=0)
-    out["out"] = y.to(torch.bfloat16)
-    return out
+    return {"out": y.to(torch.bfloat16)}
 
 
 # ------------------------------------------------------------------------------------------------ the library's calls
@@ -268,7 +265,7 @@ def _own_layer(st):
             routing["x"] = st["x"]
         o = mk.mk_moe_layer_q8(st["x_q8"], st["x_scale"], st["gate_up"], st["gate_up_scale"], st["down"],
                                st["down_scale"], c["k"], workspace=st["workspace"], **routing)
-    return {n: o[n] for n in ("topk_ids", "topk_w", "out")} if c["route"] else {"out": o["out"]}
+    return {"out": o["out"]}
 
 
 def run(state):
@@ -304,7 +301,7 @@ def work(case):
         b = hit * 2 * w + 2 * T * d
     else:
         b = hit * (w + 4 * w // GROUP ** 2) + T * d + 4 * T * d // GROUP + (2 * T * d if case["route"] else 0)
-    b += 2 * T * d + 8 * T * k
+    b += 2 * T * d + (0 if case["route"] else 8 * T * k)
     fl = 2 * rows * w
     if case["route"]:
         b += 4 * d * E
@@ -332,13 +329,11 @@ def exact(case, seed):
             out["q8_scale"] = s
         return out
     T, d, k, F = case["T"], case["d"], case["k"], case["F"]
-    out = {}
     if case["route"]:
         z = torch.matmul(st["x"].to(torch.float64), st["w_router"].to(torch.float64))
         z = z if st["bias"] is None else z + st["bias"].to(torch.float64)
         top = z.topk(k, dim=1)
         ids, gates = top.indices, torch.exp(top.values - torch.logsumexp(z, dim=1, keepdim=True))
-        out["topk_ids"], out["topk_w"] = ids.to(torch.int32), gates
     else:
         ids, gates = st["ids"].long(), st["gates"].to(torch.float64)
 
@@ -363,5 +358,4 @@ def exact(case, seed):
         a = torch.matmul(x[t], gu.T)
         h = a[:, :F] * torch.sigmoid(a[:, :F]) * a[:, F:]
         y.index_add_(0, t, gates[t, j].unsqueeze(1) * torch.matmul(h, dn.T))
-    out["out"] = y
-    return out
+    return {"out": y}
