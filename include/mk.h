@@ -332,6 +332,32 @@ mk_status mk_grouped_gemm(const void *a, const int32_t *expert_offsets, int32_t 
 mk_status mk_grouped_gemm_swiglu(const void *a, const int32_t *expert_offsets, int32_t E_local, const void *w_gate_up,
                                  int32_t K, int32_t F, void *h, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Residual addition and root-mean-square norm, the step in front of the router
+ * and the experts, in one pass:
+ *   h[t, i] = x[t, i] + residual[t, i]                     (h = x without residual)
+ *   y[t, i] = h[t, i] * gamma[i] / sqrt( mean over i of h[t, i]^2  +  eps )
+ * and, for an 8-bit output, per row and group g of 128 columns
+ *   y_scale[t, g] = max( max over the group of |y|, 2^-40 ) / 448,
+ *   y_q8[t, i]    = e4m3_rne( y[t, i] / y_scale[t, i / 128] ).
+ * fp32 arithmetic; every output is rounded once, from the fp32 values (the sum
+ * of squares from the unrounded h, y_q8 from the unrounded y).  Sums of squares
+ * past the fp32 range give y = 0; a NaN or an infinity in a row of x or the
+ * residual gives that row the values the formula has (a NaN is left out of the
+ * maximum, so it reaches its own column's code and not the group's scale).
+ * The pages (zubnet.ai, paragraph 2) start at the routing of token rows; the
+ * norm that makes these rows is this library's reading.
+ *   x [T, d] bf16    residual [T, d] bf16 or NULL    gamma [d] bf16
+ *   residual_out     NULL or [T, d] bf16: h (out)    y   NULL or [T, d] bf16 (out)
+ *   y_q8, y_scale    both NULL, or [T, d] e4m3 (OCP, no infinities) and
+ *                    [T, d / 128] fp32 (out)
+ * residual_out and y may each be x or residual itself; outputs must not overlap
+ * one another or gamma, nor x or the residual in any other way.
+ * Requires T >= 0, d > 0, d % 8 == 0 (d % 128 == 0 with y_q8), eps >= 0, at
+ * least one output, and d <= 32768 (else MK_EUNSUPPORTED).  T == 0 is a no-op
+ * returning MK_OK.  No workspace. */
+mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma, int32_t T, int32_t d, float eps,
+                         void *residual_out, void *y, void *y_q8, float *y_scale, void *stream);
+
 /* Synchronous: reads the device error word of a dispatch workspace (the caller
  * must have synchronised the stream).  Returns MK_OK, MK_ETIMEOUT or MK_EINVAL;
  * *detail (if non-NULL) receives which wait or id failed.  Clears the word. */

@@ -106,6 +106,8 @@ def load() -> ctypes.CDLL:
     lib.mk_grouped_gemm.restype = _c_i32
     lib.mk_grouped_gemm_swiglu.argtypes = [_vp, _vp, _c_i32, _vp, _c_i32, _c_i32, _vp, _vp, ctypes.c_size_t, _vp]
     lib.mk_grouped_gemm_swiglu.restype = _c_i32
+    lib.mk_add_rmsnorm.argtypes = [_vp, _vp, _vp, _c_i32, _c_i32, ctypes.c_float, _vp, _vp, _vp, _vp, _vp]
+    lib.mk_add_rmsnorm.restype = _c_i32
     _lib = lib
     return lib
 
@@ -385,3 +387,68 @@ def mk_grouped_gemm_swiglu(a: torch.Tensor, expert_offsets: torch.Tensor, w_gate
 
 def mk_grouped_gemm_workspace_bytes(E_local: int) -> int:
     return int(load().mk_grouped_gemm_workspace_bytes(E_local))
+
+
+_FP8 = torch.float8_e4m3fn
+
+
+def _on(dev: torch.device, what: str, **tensors) -> None:
+    """Checks name=(tensor, dtype, shape) against the call's device and the library's layout; a tensor may be None."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.device != dev or not t.is_cuda:
+            raise ValueError(f"{what}: {name} is on {t.device}, expected a device tensor on {dev}")
+        if t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{what}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _call_on(dev: torch.device, stream, fn, what: str, *args) -> None:
+    """Runs fn(*args, stream) with `dev` current, on the caller's stream or dev's current one."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call_on(dev, stream, fn, what, *args)
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    _check(fn(*args, s.cuda_stream), what)
+
+
+def mk_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
+                   eps: float = 1e-6, bf16: bool = True, q8: bool = False, out: Optional[dict] = None,
+                   stream=None) -> dict:
+    """Residual addition and RMS norm (mk_add_rmsnorm) of x [T, d] bf16.
+
+    Returns a dict of the outputs: "residual" (h = x + residual, if a residual is given), "y" (with bf16=True) and
+    "q8", "q8_scale" (with q8=True: e4m3 [T, d] and fp32 [T, d / 128]).  Tensors given in `out` under these names
+    receive them (residual and y may be x or residual itself); the others are allocated."""
+    T, d = x.shape
+    dev = x.device
+    o = {}
+    given = out or {}
+    if residual is not None:
+        o["residual"] = given.get("residual")
+        if o["residual"] is None:
+            o["residual"] = torch.empty_like(x)
+    if bf16:
+        o["y"] = given.get("y")
+        if o["y"] is None:
+            o["y"] = torch.empty_like(x)
+    if q8:
+        o["q8"], o["q8_scale"] = given.get("q8"), given.get("q8_scale")
+        if o["q8"] is None:
+            o["q8"] = torch.empty(T, d, dtype=_FP8, device=dev)
+        if o["q8_scale"] is None:
+            o["q8_scale"] = torch.empty(T, d // 128, dtype=torch.float32, device=dev)
+    res_out, y, q, qs = o.get("residual"), o.get("y"), o.get("q8"), o.get("q8_scale")
+    bf = torch.bfloat16
+    _on(dev, "mk_add_rmsnorm", x=(x, bf, x.shape), gamma=(gamma, bf, (d,)), residual=(residual, bf, x.shape),
+        residual_out=(res_out, bf, x.shape), y=(y, bf, x.shape), q8=(q, _FP8, x.shape),
+        q8_scale=(qs, torch.float32, (T, d // 128)))
+    _call_on(dev, stream, load().mk_add_rmsnorm, "mk_add_rmsnorm", x.data_ptr(), _addr(residual), gamma.data_ptr(),
+             T, d, eps, _addr(res_out), _addr(y), _addr(q), _addr(qs))
+    return o

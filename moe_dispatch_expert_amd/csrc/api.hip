@@ -13,6 +13,7 @@
 #include "layout_dev.h"
 #include "mk_args.h"
 #include "mk_launch.h"
+#include "norm_args.h"
 #include "route_dev.h"
 
 static __device__ __align__(256) char scratch[MK_STATIC_SCRATCH_BYTES];
@@ -720,6 +721,42 @@ mk_status mk_grouped_gemm_swiglu(const void *a, const int32_t *expert_offsets, i
     if (grid < 8) grid = 8;
     if (launch_gemm_swiglu(ga, grid, hs) != hipSuccess) return MK_EHIP;
     return MK_OK;
+}
+
+mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma, int32_t T, int32_t d, float eps,
+                         void *residual_out, void *y, void *y_q8, float *y_scale, void *stream)
+{
+    if (T < 0 || d <= 0 || d % 8 != 0 || !(eps >= 0.0f)) return MK_EINVAL;
+    if (y_q8 && d % 128 != 0) return MK_EINVAL;
+    if (d > kNormMaxD) return MK_EUNSUPPORTED;
+    if (T == 0) return MK_OK;   // before the outputs: an empty tensor has no address
+    if ((!residual_out && !y && !y_q8) || (y_q8 != nullptr) != (y_scale != nullptr)) return MK_EINVAL;
+    if (!x || !gamma) return MK_EINVAL;
+    const void *ptrs[] = {x, residual, gamma, residual_out, y, y_q8, y_scale};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MK_EINVAL;
+    // the inputs are read whole before a row is written, so an output may replace x or the residual; two
+    // outputs in one place, or one over gamma, would destroy each other
+    const void *outs[] = {residual_out, y, y_q8, y_scale};
+    for (int i = 0; i < 4; ++i) {
+        if (outs[i] && outs[i] == gamma) return MK_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (outs[i] && outs[i] == outs[j]) return MK_EINVAL;
+    }
+    if ((y_q8 && (y_q8 == x || y_q8 == residual)) || (y_scale && (y_scale == x || y_scale == residual)))
+        return MK_EINVAL;   // narrower rows would land in other rows' inputs
+    NormArgs a{};
+    a.x = (const uint16_t *)x;
+    a.res = (const uint16_t *)residual;
+    a.gamma = (const uint16_t *)gamma;
+    a.res_out = (uint16_t *)residual_out;
+    a.y = (uint16_t *)y;
+    a.q = (uint8_t *)y_q8;
+    a.qs = y_scale;
+    a.T = T;
+    a.d = d;
+    a.eps = eps;
+    return launch_add_rmsnorm(a, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
 }
 
 mk_status mk_poll_error(void *workspace, int32_t *detail)

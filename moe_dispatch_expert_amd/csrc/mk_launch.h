@@ -15,6 +15,7 @@ struct SlotArgs;
 struct GemmArgs;
 struct FusedArgs;
 struct WsHeader;
+struct NormArgs;
 
 // Router partial sums, one wave task per wave (router_tasks).
 hipError_t launch_router(const RouterArgs &a, hipStream_t s);
@@ -50,5 +51,7 @@ int fused4_per_cu();
 // A staged call's status into status[2], then the error words cleared; a zero fill of bytes (% 16 == 0).
 hipError_t launch_status(WsHeader *hdr, int32_t *status, hipStream_t s);
 hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);
+// Residual addition + RMS norm (d <= kNormMaxD).
+hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t s);
 
 }  // namespace mk
