@@ -358,6 +358,64 @@ mk_status mk_grouped_gemm_swiglu(const void *a, const int32_t *expert_offsets, i
 mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma, int32_t T, int32_t d, float eps,
                          void *residual_out, void *y, void *y_q8, float *y_scale, void *stream);
 
+/* A whole MoE layer for a few tokens (a decode step): router, gated expert FFN
+ * and combine, without the dispatch's row buffers.  The pages name the dispatch
+ * and GEMM of an MoE layer (zubnet.ai, paragraph 2); the layer around them is
+ * this library's reading, as for mk_swiglu and mk_combine:
+ *   out[t] = bf16_rne( sum over t's local choices e of
+ *              w[t, e] * W_down[e] . ( silu(W_gate[e] . x[t]) * (W_up[e] . x[t]) ) )
+ * fp32 sums and activation.  One intermediate is rounded: w * silu(g) * u, to
+ * bf16 (g and u themselves are not, unlike mk_dispatch_gemm followed by
+ * mk_swiglu, and the gate is folded in before that rounding).
+ *   s           the shape, with N = 2F as for mk_dispatch_gemm_swiglu; T <= 128
+ *   w_router, bias   routing inside the call, ids and gates bit for bit those of
+ *               mk_route_topk; or
+ *   topk_ids_in, topk_w_in   [T, k] ids and gates routed by the caller (both or
+ *               neither; w_router is then not read).  An id outside
+ *               [e_begin, e_begin + E_local), a negative one too, adds nothing
+ *               (padding rows: all -1); an id given twice for a token counts
+ *               with the sum of its gates.  A token without a local choice gets
+ *               a zero row.
+ *   w_gate_up   [E_local, 2F, d] bf16 (F gate rows, then F up rows; d contiguous)
+ *   w_down      [E_local, d, F] bf16 (F contiguous)
+ *   t_valid     NULL, or a device int32: only the first min(T, max(0, *t_valid))
+ *               tokens are computed, and the other rows of every output are left
+ *               as they were (a captured call at its largest batch)
+ *   out         [T, d] bf16 (out; may be x)
+ *   topk_ids_out, topk_w_out   NULL or [T, k]: the choices, as used
+ *   workspace   mk_moe_layer_workspace_bytes(s) bytes, any contents; two calls
+ *               in flight must not share one.
+ * Results do not depend on the device's load: every sum has a fixed order.
+ * Requires the shape of mk_dispatch_gemm, F % 8 == 0 (else MK_EINVAL), T <= 128,
+ * d <= 32768, k <= 32, 2F * d * 2 < 2^31 (else MK_EUNSUPPORTED).  T == 0 is a
+ * no-op returning MK_OK.  The call allocates nothing and may be captured. */
+size_t mk_moe_layer_workspace_bytes(const mk_shape *s);
+mk_status mk_moe_layer(const mk_shape *s, const void *x, const float *w_router, const float *bias,
+                       const int32_t *topk_ids_in, const float *topk_w_in, const void *w_gate_up, const void *w_down,
+                       const int32_t *t_valid, void *out, int32_t *topk_ids_out, float *topk_w_out, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* mk_moe_layer with 8-bit activations and weights, the activations as
+ * mk_add_rmsnorm leaves them: everything as there, with
+ *   x[t, i]        = x_q8[t, i] * x_scale[t, i / 128]
+ *   W_gate[e][f,i] = w_gate_up_q8[e, f, i]     * gate_up_scale[e, f / 128, i / 128]
+ *   W_up[e][f, i]  = w_gate_up_q8[e, F + f, i] * gate_up_scale[e, nf + f / 128, i / 128],  nf = ceil(F / 128)
+ *   W_down[e][n,f] = w_down_q8[e, n, f]        * down_scale[e, n / 128, f / 128]
+ * The products are of the 8-bit values (of bf16 w * silu(g) * u with the 8-bit
+ * W_down), summed in fp32 over 128 columns, scaled, and summed in fp32.
+ *   x             [T, d] bf16, the router's input (NULL with topk_ids_in)
+ *   x_q8, x_scale [T, d] e4m3 (OCP), [T, d / 128] fp32
+ *   w_gate_up_q8, gate_up_scale   [E_local, 2F, d] e4m3, [E_local, 2 nf, d / 128] fp32
+ *   w_down_q8, down_scale         [E_local, d, F] e4m3,  [E_local, d / 128, nf] fp32
+ * Requires F % 16 == 0 (else MK_EINVAL) and 2F * d < 2^31 (else
+ * MK_EUNSUPPORTED); the workspace is mk_moe_layer's. */
+mk_status mk_moe_layer_q8(const mk_shape *s, const void *x, const void *x_q8, const float *x_scale,
+                          const float *w_router, const float *bias, const int32_t *topk_ids_in,
+                          const float *topk_w_in, const void *w_gate_up_q8, const float *gate_up_scale,
+                          const void *w_down_q8, const float *down_scale, const int32_t *t_valid, void *out,
+                          int32_t *topk_ids_out, float *topk_w_out, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
 /* Synchronous: reads the device error word of a dispatch workspace (the caller
  * must have synchronised the stream).  Returns MK_OK, MK_ETIMEOUT or MK_EINVAL;
  * *detail (if non-NULL) receives which wait or id failed.  Clears the word. */

@@ -108,6 +108,12 @@ def load() -> ctypes.CDLL:
     lib.mk_grouped_gemm_swiglu.restype = _c_i32
     lib.mk_add_rmsnorm.argtypes = [_vp, _vp, _vp, _c_i32, _c_i32, ctypes.c_float, _vp, _vp, _vp, _vp, _vp]
     lib.mk_add_rmsnorm.restype = _c_i32
+    lib.mk_moe_layer_workspace_bytes.argtypes = [P(MkShape)]
+    lib.mk_moe_layer_workspace_bytes.restype = ctypes.c_size_t
+    lib.mk_moe_layer.argtypes = [P(MkShape)] + [_vp] * 12 + [ctypes.c_size_t, _vp]
+    lib.mk_moe_layer.restype = _c_i32
+    lib.mk_moe_layer_q8.argtypes = [P(MkShape)] + [_vp] * 16 + [ctypes.c_size_t, _vp]
+    lib.mk_moe_layer_q8.restype = _c_i32
     _lib = lib
     return lib
 
@@ -452,3 +458,83 @@ def mk_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torc
     _call_on(dev, stream, load().mk_add_rmsnorm, "mk_add_rmsnorm", x.data_ptr(), _addr(residual), gamma.data_ptr(),
              T, d, eps, _addr(res_out), _addr(y), _addr(q), _addr(qs))
     return o
+
+
+def mk_moe_layer_workspace_bytes(T, d, E, k, e_begin, E_local, F) -> int:
+    """Workspace bytes of mk_moe_layer and mk_moe_layer_q8 (F features per expert); 0 for a shape they refuse."""
+    shape = _shape(T, d, E, k, e_begin, E_local, 2 * F)
+    return int(load().mk_moe_layer_workspace_bytes(ctypes.byref(shape)))
+
+
+def _moe_layer(what, x, x_q8, x_scale, w_gate_up, gate_up_scale, w_down, down_scale, k, w_router, bias, topk_ids_in,
+               topk_w_in, E, e_begin, t_valid, workspace, out, stream) -> dict:
+    q8 = x_q8 is not None
+    act = x_q8 if q8 else x
+    T, d = act.shape
+    dev = act.device
+    E_local, two_f, _ = w_gate_up.shape
+    F = two_f // 2
+    if E is None:
+        E = w_router.shape[1] if w_router is not None else E_local
+    given = out or {}
+    o = {"out": given.get("out"), "topk_ids": given.get("topk_ids"), "topk_w": given.get("topk_w")}
+    if o["out"] is None:
+        o["out"] = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
+    shape = _shape(T, d, E, k, e_begin, E_local, two_f)
+    lib = load()
+    if workspace is None:
+        nbytes = int(lib.mk_moe_layer_workspace_bytes(ctypes.byref(shape)))
+        if nbytes == 0:   # the call itself names the reason
+            nbytes = 256
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    wt, f32 = (_FP8 if q8 else torch.bfloat16), torch.float32
+    nf = -(-F // 128)
+    _on(dev, what, x=(x, torch.bfloat16, (T, d)), x_q8=(x_q8, _FP8, (T, d)), x_scale=(x_scale, f32, (T, d // 128)),
+        w_router=(w_router, f32, (d, E)), bias=(bias, f32, (E,)), topk_ids_in=(topk_ids_in, torch.int32, (T, k)),
+        topk_w_in=(topk_w_in, f32, (T, k)), w_gate_up=(w_gate_up, wt, (E_local, two_f, d)),
+        gate_up_scale=(gate_up_scale, f32, (E_local, 2 * nf, d // 128)), w_down=(w_down, wt, (E_local, d, F)),
+        down_scale=(down_scale, f32, (E_local, d // 128, nf)), t_valid=(t_valid, torch.int32, (1,)),
+        out=(o["out"], torch.bfloat16, (T, d)), topk_ids=(o["topk_ids"], torch.int32, (T, k)),
+        topk_w=(o["topk_w"], f32, (T, k)), workspace=(workspace, torch.uint8, workspace.shape))
+    routing = (_addr(w_router), _addr(bias), _addr(topk_ids_in), _addr(topk_w_in))
+    outs = (_addr(t_valid), o["out"].data_ptr(), _addr(o["topk_ids"]), _addr(o["topk_w"]), workspace.data_ptr(),
+            workspace.numel())
+    if q8:
+        _call_on(dev, stream, lib.mk_moe_layer_q8, what, ctypes.byref(shape), _addr(x), x_q8.data_ptr(),
+                 _addr(x_scale), *routing, w_gate_up.data_ptr(), _addr(gate_up_scale), w_down.data_ptr(),
+                 _addr(down_scale), *outs)
+    else:
+        _call_on(dev, stream, lib.mk_moe_layer, what, ctypes.byref(shape), x.data_ptr(), *routing,
+                 w_gate_up.data_ptr(), w_down.data_ptr(), *outs)
+    o["workspace"] = workspace
+    return o
+
+
+def mk_moe_layer(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, k: int, *,
+                 w_router: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                 topk_ids_in: Optional[torch.Tensor] = None, topk_w_in: Optional[torch.Tensor] = None,
+                 E: Optional[int] = None, e_begin: int = 0, t_valid: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None, stream=None) -> dict:
+    """The whole MoE layer of at most 128 tokens x [T, d] (mk_moe_layer): routed here with w_router [d, E] (and bias),
+    or by topk_ids_in and topk_w_in [T, k]; w_gate_up [E_local, 2F, d], w_down [E_local, d, F] bf16.
+
+    t_valid: int32 tensor of one element, the tokens to compute (the other rows stay as they are).
+    workspace: a uint8 tensor of mk_moe_layer_workspace_bytes bytes, reused across calls (allocated here if None).
+    Returns dict(out [T, d] bf16, topk_ids, topk_w, workspace); `out` and, to have the choices written,
+    "topk_ids" (int32) and "topk_w" (fp32) [T, k] may be given in the dict `out`."""
+    return _moe_layer("mk_moe_layer", x, None, None, w_gate_up, None, w_down, None, k, w_router, bias, topk_ids_in,
+                      topk_w_in, E, e_begin, t_valid, workspace, out, stream)
+
+
+def mk_moe_layer_q8(x_q8: torch.Tensor, x_scale: torch.Tensor, w_gate_up: torch.Tensor, gate_up_scale: torch.Tensor,
+                    w_down: torch.Tensor, down_scale: torch.Tensor, k: int, *, x: Optional[torch.Tensor] = None,
+                    w_router: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                    topk_ids_in: Optional[torch.Tensor] = None, topk_w_in: Optional[torch.Tensor] = None,
+                    E: Optional[int] = None, e_begin: int = 0, t_valid: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None, stream=None) -> dict:
+    """mk_moe_layer with e4m3 activations (x_q8 [T, d], x_scale [T, d / 128], as mk_add_rmsnorm's q8 outputs) and e4m3
+    weights with one fp32 scale per 128 x 128 block of the gate, the up and the down matrix: gate_up_scale
+    [E_local, 2 ceil(F / 128), d / 128] (gate blocks, then up blocks), down_scale [E_local, d / 128, ceil(F / 128)].
+    x [T, d] bf16 is the router's input, needed with w_router."""
+    return _moe_layer("mk_moe_layer_q8", x, x_q8, x_scale, w_gate_up, gate_up_scale, w_down, down_scale, k, w_router,
+                      bias, topk_ids_in, topk_w_in, E, e_begin, t_valid, workspace, out, stream)

@@ -10,6 +10,7 @@
 #include "../../include/mk.h"
 #include "fused_dev.h"
 #include "gemm_dev.h"
+#include "layer_args.h"
 #include "layout_dev.h"
 #include "mk_args.h"
 #include "mk_launch.h"
@@ -479,6 +480,114 @@ constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
 void *g_scratch_dev[kMaxDevices];
 
+// ---------------------------------------------------------------- the few-token MoE layer
+
+// Workspace: router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] bf16.
+struct LayerWs {
+    size_t ids, w, h, total;
+};
+
+LayerWs layer_ws(const mk_shape *s)
+{
+    LayerWs L;
+    L.ids = align256((size_t)kRouterSegments * s->T * s->E * 4);
+    L.w = L.ids + align256((size_t)s->T * s->k * 4);
+    L.h = L.w + align256((size_t)s->T * s->k * 4);
+    L.total = L.h + align256((size_t)s->T * std::min(s->k, s->E_local) * (s->N / 2) * 2) + 256;
+    return L;
+}
+
+mk_status check_layer_shape(const mk_shape *s, bool q8)
+{
+    const mk_status st = check_shape(s);
+    if (st != MK_OK) return st;
+    if (s->N % (q8 ? 32 : 16) != 0) return MK_EINVAL;
+    // the kernels' offsets inside one expert's matrix and inside the token rows are 32-bit
+    if (s->T > kLayerMaxT || s->d > kNormMaxD || (int64_t)s->N * s->d * (q8 ? 1 : 2) >= ((int64_t)1 << 31))
+        return MK_EUNSUPPORTED;
+    return MK_OK;
+}
+
+mk_status layer_impl(const mk_shape *s, bool q8, const void *x, const void *x_q8, const float *x_scale,
+                     const float *w_router, const float *bias, const int32_t *topk_ids_in, const float *topk_w_in,
+                     const void *w_gate_up, const float *gate_up_scale, const void *w_down, const float *down_scale,
+                     const int32_t *t_valid, void *out, int32_t *topk_ids_out, float *topk_w_out, void *workspace,
+                     size_t workspace_bytes, void *stream)
+{
+    const mk_status st = check_layer_shape(s, q8);
+    if (st != MK_OK) return st;
+    if (s->T == 0) return MK_OK;
+    const bool given = topk_ids_in != nullptr;
+    if (given != (topk_w_in != nullptr) || (!given && !w_router)) return MK_EINVAL;
+    if ((!q8 || !given) && !x) return MK_EINVAL;
+    if (q8 && (!x_q8 || !x_scale || !gate_up_scale || !down_scale)) return MK_EINVAL;
+    if (!w_gate_up || !w_down || !out || !workspace) return MK_EINVAL;
+    const void *ptrs[] = {x, x_q8, x_scale, w_router, bias, topk_ids_in, topk_w_in, w_gate_up, gate_up_scale, w_down,
+                          down_scale, t_valid, out, topk_ids_out, topk_w_out, workspace};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return MK_EINVAL;
+    const LayerWs L = layer_ws(s);
+    if (workspace_bytes < L.total) return MK_EWORKSPACE;
+    hipStream_t hs = (hipStream_t)stream;
+    char *ws = (char *)workspace;
+    LayerArgs a{};
+    a.x = (const uint16_t *)x;
+    a.xq = (const uint8_t *)x_q8;
+    a.xs = x_scale;
+    a.w_gu = w_gate_up;
+    a.w_dn = w_down;
+    a.s_gu = gate_up_scale;
+    a.s_dn = down_scale;
+    a.ids_ws = (int32_t *)(ws + L.ids);
+    a.ids = given ? topk_ids_in : a.ids_ws;
+    a.gates = given ? topk_w_in : (const float *)(ws + L.w);
+    a.ids_user = topk_ids_out;
+    a.w_user = topk_w_out;
+    a.part = (float *)ws;
+    a.wr = w_router;
+    a.bias = bias;
+    a.h = (uint16_t *)(ws + L.h);
+    a.out = (uint16_t *)out;
+    a.t_valid = t_valid;
+    a.T = s->T;
+    a.d = s->d;
+    a.E = s->E;
+    a.k = s->k;
+    a.e_begin = s->e_begin;
+    a.E_local = s->E_local;
+    a.F = s->N / 2;
+    a.given = given ? 1 : 0;
+    const bool self = !given && s->T <= kLayerSelfT && s->E <= kLayerSelfE;
+    if (!given) {
+        if (s->T <= kLayerSelfT) {
+            if (launch_layer_router(a, hs) != hipSuccess) return MK_EHIP;
+        } else {
+            RouterArgs ra{};
+            ra.src.p[0] = a.x;
+            ra.src.S = 1;
+            ra.src.rows_per_src = s->T;
+            ra.wr = w_router;
+            ra.part = a.part;
+            ra.T = s->T;
+            ra.d = s->d;
+            ra.E = s->E;
+            if (launch_router(ra, hs) != hipSuccess) return MK_EHIP;
+        }
+        if (!self) {
+            TopkArgs ta{};
+            ta.part = a.part;
+            ta.bias = bias;
+            ta.ids = a.ids_ws;
+            ta.w_user = (float *)(ws + L.w);
+            ta.T = s->T;
+            ta.E = s->E;
+            ta.k = s->k;
+            if (launch_topk(ta, CountArgs{}, false, hs) != hipSuccess) return MK_EHIP;
+        }
+    }
+    return launch_layer(a, q8, self, hs) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -757,6 +866,35 @@ mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma,
     a.d = d;
     a.eps = eps;
     return launch_add_rmsnorm(a, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
+size_t mk_moe_layer_workspace_bytes(const mk_shape *s)
+{
+    // the 8-bit form takes a subset of the bf16 form's feature counts and needs no more workspace, but its weight
+    // matrices may be twice as large
+    if (check_layer_shape(s, false) != MK_OK && check_layer_shape(s, true) != MK_OK) return 0;
+    return layer_ws(s).total;
+}
+
+mk_status mk_moe_layer(const mk_shape *s, const void *x, const float *w_router, const float *bias,
+                       const int32_t *topk_ids_in, const float *topk_w_in, const void *w_gate_up, const void *w_down,
+                       const int32_t *t_valid, void *out, int32_t *topk_ids_out, float *topk_w_out, void *workspace,
+                       size_t workspace_bytes, void *stream)
+{
+    return layer_impl(s, false, x, nullptr, nullptr, w_router, bias, topk_ids_in, topk_w_in, w_gate_up, nullptr,
+                      w_down, nullptr, t_valid, out, topk_ids_out, topk_w_out, workspace, workspace_bytes, stream);
+}
+
+mk_status mk_moe_layer_q8(const mk_shape *s, const void *x, const void *x_q8, const float *x_scale,
+                          const float *w_router, const float *bias, const int32_t *topk_ids_in,
+                          const float *topk_w_in, const void *w_gate_up_q8, const float *gate_up_scale,
+                          const void *w_down_q8, const float *down_scale, const int32_t *t_valid, void *out,
+                          int32_t *topk_ids_out, float *topk_w_out, void *workspace, size_t workspace_bytes,
+                          void *stream)
+{
+    return layer_impl(s, true, x, x_q8, x_scale, w_router, bias, topk_ids_in, topk_w_in, w_gate_up_q8, gate_up_scale,
+                      w_down_q8, down_scale, t_valid, out, topk_ids_out, topk_w_out, workspace, workspace_bytes,
+                      stream);
 }
 
 mk_status mk_poll_error(void *workspace, int32_t *detail)

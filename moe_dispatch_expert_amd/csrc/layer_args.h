@@ -1,0 +1,36 @@
+// layer_args.h -- arguments and workspace of the few-token MoE layer.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "mk_args.h"
+
+namespace mk {
+
+constexpr int kLayerMaxT = 128;      // tokens per call (two 64-bit token masks per expert)
+constexpr int kLayerSelfT = 8;       // tokens up to which the vector router runs and the up kernel selects by itself
+constexpr int kLayerSelfE = 256;     // ... and experts, for the selection
+constexpr int kQ8Group = 128;        // columns (and rows of weights) per scale
+
+struct LayerArgs {
+    const uint16_t *x;               // [T, d] bf16: router input, and the experts' in the bf16 form
+    const uint8_t *xq;               // [T, d] e4m3 (8-bit form)
+    const float *xs;                 // [T, d / 128]
+    const void *w_gu, *w_dn;         // [E_local, 2F, d], [E_local, d, F]: bf16 or e4m3
+    const float *s_gu, *s_dn;        // [E_local, 2 ceil(F / 128), d / 128], [E_local, d / 128, ceil(F / 128)]
+    const int32_t *ids;              // [T, k] given or selected ids (what the up kernel reads unless it selects)
+    const float *gates;              // [T, k]
+    int32_t *ids_ws;                 // [T, k] ids the down kernel reads, written by the up kernel when it selects
+    int32_t *ids_user;               // NULL or [T, k]: copies for the caller
+    float *w_user;
+    float *part;                     // [8, T, E] router partial sums
+    const float *wr, *bias;          // router
+    uint16_t *h;                     // [T min(k, E_local), F] bf16: gate * silu(g) * u, rows in expert order
+    uint16_t *out;                   // [T, d] bf16
+    const int32_t *t_valid;          // NULL or the number of tokens to compute (device)
+    int32_t T, d, E, k, e_begin, E_local, F;
+    int32_t given;                   // ids came from the caller: they may repeat
+};
+
+}  // namespace mk

@@ -16,6 +16,7 @@ struct GemmArgs;
 struct FusedArgs;
 struct WsHeader;
 struct NormArgs;
+struct LayerArgs;
 
 // Router partial sums, one wave task per wave (router_tasks).
 hipError_t launch_router(const RouterArgs &a, hipStream_t s);
@@ -53,5 +54,9 @@ hipError_t launch_status(WsHeader *hdr, int32_t *status, hipStream_t s);
 hipError_t launch_zero(void *p, size_t bytes, hipStream_t s);
 // Residual addition + RMS norm (d <= kNormMaxD).
 hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t s);
+// Few-token MoE layer: the vector router (T <= kLayerSelfT), and the up and down kernels (self: the up kernel selects
+// the experts from the router's partial sums).
+hipError_t launch_layer_router(const LayerArgs &a, hipStream_t s);
+hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s);
 
 }  // namespace mk

@@ -277,8 +277,16 @@ __device__ __forceinline__ void topk_load(const TopkArgs &a, int t, TopkPartials
     }
 }
 
+// What the lanes of a wave hold after the selection: lane j < k the j-th choice, every lane the largest logit and
+// the softmax's denominator.
+struct TopkPick {
+    int id;
+    float logit, top, zsum;
+    __device__ __forceinline__ float gate() const { return expf(logit - top) / zsum; }
+};
+
 template <int NV>
-__device__ __forceinline__ void topk_select(const TopkArgs &a, int t, const TopkPartials<NV> &r)
+__device__ __forceinline__ TopkPick topk_pick(const TopkArgs &a, int t, const TopkPartials<NV> &r)
 {
 #pragma clang fp contract(off)
     const int l = threadIdx.x % kWave;
@@ -295,8 +303,7 @@ __device__ __forceinline__ void topk_select(const TopkArgs &a, int t, const Topk
         key[v] = e < a.E ? topk_key(x, e) : 0ull;
         if (a.logits_user && e < a.E) a.logits_user[(size_t)t * a.E + e] = x;
     }
-    float top_logit = 0.0f, sel_logit = 0.0f;
-    int sel_id = 0;
+    TopkPick p{0, 0.0f, 0.0f, 0.0f};
     for (int j = 0; j < a.k; ++j) {
         uint64_t best = 0;
 #pragma unroll
@@ -308,24 +315,31 @@ __device__ __forceinline__ void topk_select(const TopkArgs &a, int t, const Topk
             if (key[v] == best) key[v] = 0ull;
         const uint32_t ok = (uint32_t)(best >> 32);
         const float logit = __uint_as_float((ok & 0x80000000u) ? (ok & 0x7FFFFFFFu) : ~ok);
-        if (j == 0) top_logit = logit;
+        if (j == 0) p.top = logit;
         if (l == j) {
-            sel_logit = logit;
-            sel_id = e;
+            p.logit = logit;
+            p.id = e;
         }
     }
-    float zsum = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
-        if (l + v * kWave < a.E) zsum += expf(lv[v] - top_logit);
-    zsum = wave_sum_f32(zsum);
+        if (l + v * kWave < a.E) p.zsum += expf(lv[v] - p.top);
+    p.zsum = wave_sum_f32(p.zsum);
+    return p;
+}
+
+template <int NV>
+__device__ __forceinline__ void topk_select(const TopkArgs &a, int t, const TopkPartials<NV> &r)
+{
+    const int l = threadIdx.x % kWave;
+    const TopkPick p = topk_pick<NV>(a, t, r);
     if (l < a.k) {
         const size_t o = (size_t)t * a.k + l;
-        store_through(a.ids + o, sel_id);   // read by other workgroups after the next grid barrier
-        if (a.ids_user) a.ids_user[o] = sel_id;
-        if (a.w_user) a.w_user[o] = expf(sel_logit - top_logit) / zsum;
+        store_through(a.ids + o, p.id);   // read by other workgroups after the next grid barrier
+        if (a.ids_user) a.ids_user[o] = p.id;
+        if (a.w_user) a.w_user[o] = p.gate();
         // the token's bit in its block's mask of every local expert it chose
-        const int le = sel_id - a.e_begin;
+        const int le = p.id - a.e_begin;
         if (a.blkmask && le >= 0 && le < a.E_local)
             __hip_atomic_fetch_or(a.blkmask + (size_t)(t / kTokBlock) * a.E_local + le, 1ull << (t % kTokBlock),
                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
