@@ -6,8 +6,8 @@
 // A few tokens make this a matter of streaming the chosen experts' weights once:
 // 3 F d weights against 6 F d flops per row of an expert, i.e. 1 to 16 rows
 // leave the matrix cores idle most of the time.  So
-//   - the weights are the matrix core's A operand (16 weight rows x 32 K per
-//     instruction, one 16-byte load per lane straight into registers, no LDS),
+//   - the weights are the matrix core's A operand (16 weight rows), loaded
+//     straight into registers (no LDS), 8 rows x 128 bytes per instruction, and
 //     the tokens of the expert its B operand (16 columns), loaded from the L2;
 //   - K is split over the waves of a workgroup, so that a workgroup's unit of
 //     work is a thin slab of weights and a few experts already fill the device;
@@ -156,6 +156,22 @@ __device__ __forceinline__ u32x4_t load_w(const char *base, uint32_t off)
 }
 __device__ __forceinline__ u32x4_t load_x(const char *base, uint32_t off) { return *(const u32x4_t *)(base + off); }
 
+// Sixteen weight rows x 128 bytes come in as two loads of 8 rows x 128 bytes, so that each load reads whole cache lines:
+// non-temporal loads of 16 rows x 64 bytes, which the operand layout below would give, fetch every line twice (measured
+// over 2 GiB, rows 14336 bytes apart: 5.5 against 7.1 TB/s).  Lane i + 16 g of load a (rows 0 - 7) and of load b (rows
+// 8 - 15) takes row i % 8, 16-byte piece g + 4 (i / 8).  Exchanging a's lanes i >= 8 with b's lanes i < 8 inside each 16
+// lanes leaves the matrix core's layout, lane i + 16 g = row i: piece g in a, piece 4 + g in b.
+__device__ __forceinline__ void swap_halves(u32x4_t &a, u32x4_t &b)
+{
+    constexpr int kRor8 = 0x128;   // DPP row_ror:8
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int x = (int)a[j], y = (int)b[j];
+        a[j] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, kRor8, 0xF, 0xC, false);
+        b[j] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, kRor8, 0xF, 0x3, false);
+    }
+}
+
 __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, u32x4_t b, f32x4_t c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
@@ -184,34 +200,47 @@ __device__ __forceinline__ u32x4_t fp8_to_bf16(uint32_t lo, uint32_t hi)
 
 // ---------------------------------------------------------------- gate|up
 
-// acc[r][n] += W tile r (16 rows) x token tile n over K steps s0 .. s1 - 1 of 32; wo, xo: the lane's byte offsets from w
-// and x at K = 0.  U steps are in flight at a time: as many as R U + NT U loads leave room for beside the sums in 128
-// registers.
+// acc[r][n] += W tile r (16 rows) x token tile n over K steps s0 .. s1 - 1 of 64.  wo[r][0], wo[r][1]: the lane's byte
+// offsets from w of the tile's rows 0 - 7 and 8 - 15 (swap_halves) at K = 0; xo[n]: of its token from x, with 16 g.  U
+// steps are in flight at a time.
 template <int R, int NT>
-__device__ __forceinline__ void up_bf16(const char *w, const uint32_t (&wo)[R], const char *x,
+__device__ __forceinline__ void up_bf16(const char *w, const uint32_t (&wo)[R][2], const char *x,
                                         const uint32_t (&xo)[NT], int s0, int s1, f32x4_t (&acc)[R][NT])
 {
     int s = s0;
     auto run = [&](auto uc) {
         constexpr int U = decltype(uc)::value;
-        u32x4_t wv[R][U];
+        u32x4_t wv[R][U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int r = 0; r < R; ++r) wv[r][u] = load_w(w, wo[r] + (uint32_t)(s + u) * 64);
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) wv[r][u][i] = load_w(w, wo[r][i] + (uint32_t)(s + u) * 128);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            u32x4_t xv[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) xv[u] = load_x(x, xo[n] + (uint32_t)(s + u) * 64);
+            u32x4_t xv[U][2];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int r = 0; r < R; ++r) acc[r][n] = mfma_bf16(wv[r][u], xv[u], acc[r][n]);
+                for (int i = 0; i < 2; ++i) xv[u][i] = load_x(x, xo[n] + (uint32_t)(s + u) * 128 + 64 * i);
+            if (n == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) swap_halves(wv[r][u][0], wv[r][u][1]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[r][n] = mfma_bf16(wv[r][u][i], xv[u][i], acc[r][n]);
+            if (NT >= 4) __builtin_amdgcn_sched_barrier(0);   // keeps later tiles' loads out of the registers
         }
         s += U;
     };
-    constexpr int U = R == 1 ? 8 : NT <= 2 ? 4 : NT == 4 ? 2 : 1;
+    constexpr int U = R == 1 ? 4 : NT <= 2 ? 2 : 1;
     while (s + U <= s1) run(IntC<U>());
     while (s < s1) run(IntC<1>());
 }
@@ -219,40 +248,46 @@ __device__ __forceinline__ void up_bf16(const char *w, const uint32_t (&wo)[R], 
 // The same for e4m3 operands over 128-wide blocks b0 .. b1 - 1: a block's product, times the token's and the weights'
 // scales of the block, joins the sum in fp32.  sw[r]: the tile's scales (this lane's rows), sx + so[n]: the lane's token's.
 template <int R, int NT>
-__device__ __forceinline__ void up_q8(const char *w, const uint32_t (&wo)[R], const char *x, const uint32_t (&xo)[NT],
-                                      const float *const (&sw)[R], const float *sx, const uint32_t (&so)[NT], int b0, int b1,
-                                      f32x4_t (&acc)[R][NT])
+__device__ __forceinline__ void up_q8(const char *w, const uint32_t (&wo)[R][2], const char *x,
+                                      const uint32_t (&xo)[NT], const float *const (&sw)[R], const float *sx,
+                                      const uint32_t (&so)[NT], int b0, int b1, f32x4_t (&acc)[R][NT])
 {
     int b = b0;
     auto run = [&](auto uc) {
         constexpr int U = decltype(uc)::value;
-        u32x4_t wv[R][2 * U];
+        u32x4_t wv[R][U][2];
         float fw[R][U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                wv[r][2 * u] = load_w(w, wo[r] + (uint32_t)(b + u) * kQ8Group);
-                wv[r][2 * u + 1] = load_w(w, wo[r] + (uint32_t)(b + u) * kQ8Group + 64);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) wv[r][u][i] = load_w(w, wo[r][i] + (uint32_t)(b + u) * kQ8Group);
                 fw[r][u] = sw[r][b + u];
             }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            u32x4_t xv[2 * U];
+            u32x4_t xv[U][2];
             float fx[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                xv[2 * u] = load_x(x, xo[n] + (uint32_t)(b + u) * kQ8Group);
-                xv[2 * u + 1] = load_x(x, xo[n] + (uint32_t)(b + u) * kQ8Group + 64);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) xv[u][i] = load_x(x, xo[n] + (uint32_t)(b + u) * kQ8Group + 64 * i);
                 fx[u] = sx[so[n] + b + u];
+            }
+            if (n == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) swap_halves(wv[r][u][0], wv[r][u][1]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
-                    p = mfma_fp8_64(wv[r][2 * u], xv[2 * u], p);
-                    p = mfma_fp8_64(wv[r][2 * u + 1], xv[2 * u + 1], p);
+                    p = mfma_fp8_64(wv[r][u][0], xv[u][0], p);
+                    p = mfma_fp8_64(wv[r][u][1], xv[u][1], p);
                     const float f = fw[r][u] * fx[u];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) acc[r][n][q] = __builtin_fmaf(p[q], f, acc[r][n][q]);
@@ -282,21 +317,32 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[r][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    // the lane's weight row of the expert in each tile (features past F repeat the last; never stored)
-    uint32_t wo[R], xo[NT];
+    // the lane's weight rows of the expert in each tile (features past F repeat the last; never stored)
+    uint32_t wo[R][2], xo[NT];
     if (R == 1) {
-        wo[0] = c < 8 ? f0 + c : a.F + f0 + c - 8;
+        wo[0][0] = f0 + (c & 7);
+        wo[0][1] = a.F + wo[0][0];
     } else {
-        wo[0] = min(f0 + c, a.F - 1);
-        wo[R - 1] = a.F + wo[0];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            wo[0][i] = min(f0 + 8 * i + (c & 7), a.F - 1);
+            wo[R - 1][i] = a.F + wo[0][i];
+        }
     }
     // the lane's token in each tile (columns past cnt repeat the last; never stored)
+    uint32_t tok[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xo[n] = s.tok[row0 + min(16 * n + c, cnt - 1)];
+    for (int n = 0; n < NT; ++n) tok[n] = s.tok[row0 + min(16 * n + c, cnt - 1)];
     const size_t we = (size_t)e * 2 * a.F * a.d;
     constexpr int kBytes = Q8 ? 1 : 2;
     const char *w = (const char *)a.w_gu + we * kBytes, *x = Q8 ? (const char *)a.xq : (const char *)a.x;
     const uint32_t pitch = (uint32_t)a.d * kBytes;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wo[r][i] = wo[r][i] * pitch + 16 * (g + 4 * (c >> 3));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xo[n] = tok[n] * pitch + 16 * g;
     if constexpr (Q8) {
         const int nb = a.d / kQ8Group, nf = (a.F + kQ8Group - 1) / kQ8Group;
         const float *sw[R];
@@ -310,18 +356,10 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
             sw[R - 1] = se + (size_t)nf * nb;
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) so[n] = xo[n] * (uint32_t)nb;
-#pragma unroll
-        for (int r = 0; r < R; ++r) wo[r] = wo[r] * pitch + 16 * g;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) xo[n] = xo[n] * pitch + 16 * g;
+        for (int n = 0; n < NT; ++n) so[n] = tok[n] * (uint32_t)nb;
         up_q8<R, NT>(w, wo, x, xo, sw, a.xs, so, nb * wave / kUpWaves, nb * (wave + 1) / kUpWaves, acc);
     } else {
-#pragma unroll
-        for (int r = 0; r < R; ++r) wo[r] = wo[r] * pitch + 16 * g;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) xo[n] = xo[n] * pitch + 16 * g;
-        const int ns = a.d / 32;
+        const int ns = a.d / 64;
         up_bf16<R, NT>(w, wo, x, xo, ns * wave / kUpWaves, ns * (wave + 1) / kUpWaves, acc);
     }
     // The waves' parts of a token tile meet in LDS ([column][row], so a lane's four rows are one 16-byte word), are
@@ -415,84 +453,102 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_layer_up(LayerArgs a)
 constexpr int kDownWaves = 4;
 
 // One expert's part of 16 output columns: acc[n] = sum over K of W_down rows x h rows of token tile n, for this wave's
-// share of K.  wo, ho[n]: the lane's byte offsets from w and h at K = 0.
+// share of K.  wo: the lane's byte offsets from w of the rows 0 - 7 and 8 - 15 (swap_halves), ho[n]: of its h row from h
+// with 16 g, all at K = 0.  kp: the lane's piece of a weight row, in elements.
 template <int NT>
-__device__ __forceinline__ void down_bf16(const char *w, uint32_t wo, const char *h, const uint32_t (&ho)[NT], int F,
-                                          int wave, f32x4_t (&acc)[NT])
+__device__ __forceinline__ void down_bf16(const char *w, const uint32_t (&wo)[2], int kp, const char *h,
+                                          const uint32_t (&ho)[NT], int F, int wave, f32x4_t (&acc)[NT])
 {
-    const int ns = F / 32;
+    const int ns = F / 64;
     int s = ns * wave / kDownWaves;
     const int s1 = ns * (wave + 1) / kDownWaves;
-    auto run = [&](auto uc) {
+    const int kh = 8 * (int)(threadIdx.x % kWave >> 4);
+    auto run = [&](auto uc, auto partial) {
         constexpr int U = decltype(uc)::value;
-        u32x4_t wv[U];
+        // PARTIAL: the last step, with F % 64 of K left; pieces past F are zeros on both sides
+        constexpr bool PARTIAL = decltype(partial)::value != 0;
+        const int left = PARTIAL ? F % 64 : 64;
+        const u32x4_t z = {0u, 0u, 0u, 0u};
+        u32x4_t wv[U][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) wv[u] = load_w(w, wo + (uint32_t)(s + u) * 64);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                wv[u][i] = !PARTIAL || kp < left ? load_w(w, wo[i] + (uint32_t)(s + u) * 128) : z;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            u32x4_t hv[U];
+            u32x4_t hv[U][2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) hv[u] = load_x(h, ho[n] + (uint32_t)(s + u) * 64);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < U; ++u) acc[n] = mfma_bf16(wv[u], hv[u], acc[n]);
+                for (int i = 0; i < 2; ++i)
+                    hv[u][i] = !PARTIAL || kh + 32 * i < left ? load_x(h, ho[n] + (uint32_t)(s + u) * 128 + 64 * i) : z;
+            if (n == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) swap_halves(wv[u][0], wv[u][1]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) acc[n] = mfma_bf16(wv[u][i], hv[u][i], acc[n]);
+            if (NT >= 4) __builtin_amdgcn_sched_barrier(0);   // keeps later tiles' loads out of the registers
         }
         s += U;
     };
-    constexpr int U = NT == 1 ? 8 : NT <= 4 ? 4 : 2;
-    while (s + U <= s1) run(IntC<U>());
-    while (s < s1) run(IntC<1>());
-    if (F % 32 != 0 && wave == kDownWaves - 1) {   // the last, partial step: lane groups past F take zeros
-        const bool in = ns * 32 + 8 * (int)(threadIdx.x % kWave >> 4) < F;
-        const u32x4_t z = {0u, 0u, 0u, 0u};
-        const u32x4_t wv = in ? load_w(w, wo + (uint32_t)ns * 64) : z;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = mfma_bf16(wv, in ? load_x(h, ho[n] + (uint32_t)ns * 64) : z, acc[n]);
-    }
+    constexpr int U = NT == 1 ? 4 : 2;
+    while (s + U <= s1) run(IntC<U>(), IntC<0>());
+    while (s < s1) run(IntC<1>(), IntC<0>());
+    if (F % 64 != 0 && wave == kDownWaves - 1) run(IntC<1>(), IntC<1>());
 }
 
 // The same with e4m3 weights, converted to bf16 (exact) in front of the matrix core; sw: the column tile's scales, one
-// per 128 of K.  Lane group g holds K elements 16 g .. 16 g + 15 of a 64-wide step in both operands.
+// per 128 of K.  Lane group g holds K elements 16 g .. 16 g + 15 of a 64-wide half block in both operands.
 template <int NT>
-__device__ __forceinline__ void down_q8(const char *w, uint32_t wo, const char *h, const uint32_t (&ho)[NT],
-                                        const float *sw, int F, int wave, f32x4_t (&acc)[NT])
+__device__ __forceinline__ void down_q8(const char *w, const uint32_t (&wo)[2], int kp, const char *h,
+                                        const uint32_t (&ho)[NT], const float *sw, int F, int wave,
+                                        f32x4_t (&acc)[NT])
 {
     const int nb = F / kQ8Group;
     int b = nb * wave / kDownWaves;
     const int b1 = nb * (wave + 1) / kDownWaves;
-    const int k0 = 16 * (int)(threadIdx.x % kWave >> 4);
+    const int kh = 16 * (int)(threadIdx.x % kWave >> 4);
     auto run = [&](auto uc, auto partial) {
         constexpr int U = decltype(uc)::value;
-        // PARTIAL: the last block, with F % 128 of K left; lane groups past F take zeros
+        // PARTIAL: the last block, with F % 128 of K left; pieces past F are zeros on both sides
         constexpr bool PARTIAL = decltype(partial)::value != 0;
         const int left = PARTIAL ? F % kQ8Group : kQ8Group;
         const u32x4_t z = {0u, 0u, 0u, 0u};
-        u32x4_t wv[2 * U];
+        u32x4_t wv[U][2];
         float fw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                wv[2 * u + i] = !PARTIAL || k0 + 64 * i < left ? load_w(w, wo + (uint32_t)(b + u) * kQ8Group + 64 * i) : z;
+                wv[u][i] = !PARTIAL || kp < left ? load_w(w, wo[i] + (uint32_t)(b + u) * kQ8Group) : z;
             fw[u] = sw[b + u];
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            u32x4_t hv[4 * U];
+            u32x4_t hv[U][4];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    hv[4 * u + i] = !PARTIAL || k0 + 64 * (i / 2) < left
-                                        ? load_x(h, ho[n] + (uint32_t)(b + u) * (2 * kQ8Group) + 128 * (i / 2) + 16 * (i & 1))
-                                        : z;
+                    hv[u][i] = !PARTIAL || kh + 64 * (i / 2) < left
+                                   ? load_x(h, ho[n] + (uint32_t)(b + u) * (2 * kQ8Group) + 128 * (i / 2) + 16 * (i & 1))
+                                   : z;
+            if (n == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) swap_halves(wv[u][0], wv[u][1]);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const u32x4_t v = wv[2 * u + i];
-                    p = mfma_bf16(fp8_to_bf16(v.x, v.y), hv[4 * u + 2 * i], p);
-                    p = mfma_bf16(fp8_to_bf16(v.z, v.w), hv[4 * u + 2 * i + 1], p);
+                    const u32x4_t v = wv[u][i];
+                    p = mfma_bf16(fp8_to_bf16(v.x, v.y), hv[u][2 * i], p);
+                    p = mfma_bf16(fp8_to_bf16(v.z, v.w), hv[u][2 * i + 1], p);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[n][q] = __builtin_fmaf(p[q], fw[u], acc[n][q]);
@@ -523,12 +579,15 @@ __device__ __forceinline__ void down_expert(const LayerArgs &a, const RowsLds &s
     }
     const char *h = (const char *)(a.h + (size_t)row0 * a.F);
     const char *w = (const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * (Q8 ? 1 : 2);
-    const uint32_t wo = (uint32_t)(c * a.F) * (Q8 ? 1 : 2) + 16 * g;
+    const int piece = g + 4 * (c >> 3);
+    uint32_t wo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)((8 * i + (c & 7)) * a.F) * (Q8 ? 1 : 2) + 16 * piece;
     if constexpr (Q8) {
         const int nf = (a.F + kQ8Group - 1) / kQ8Group;
-        down_q8<NT>(w, wo, h, ho, a.s_dn + ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * nf, a.F, wave, acc);
+        down_q8<NT>(w, wo, 16 * piece, h, ho, a.s_dn + ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * nf, a.F, wave, acc);
     } else {
-        down_bf16<NT>(w, wo, h, ho, a.F, wave, acc);
+        down_bf16<NT>(w, wo, 8 * piece, h, ho, a.F, wave, acc);
     }
     // tokens of an expert are distinct, so no two lanes add to one word
 #pragma unroll
