@@ -144,17 +144,48 @@ __device__ __forceinline__ int valid_tokens(const LayerArgs &a)
     return a.t_valid ? max(0, min(*a.t_valid, a.T)) : a.T;
 }
 
-template <int N>
-struct IntC {
-    static constexpr int value = N;
-};
-
-// 16 bytes at a uniform base plus the lane's 32-bit offset; load_w: weights, which no other workgroup reads.
-__device__ __forceinline__ u32x4_t load_w(const char *base, uint32_t off)
+// Buffer resource of `bytes` from base (both uniform): a load is base + the lane's 32-bit offset + a scalar offset, with
+// no address arithmetic in the vector registers, and a lane offset past the end reads zeros without a memory access.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *base, uint32_t bytes)
 {
-    return __builtin_nontemporal_load((const u32x4_t *)(base + off));
+    const uint64_t b = (uint64_t)base;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)(((uint64_t)hi << 32) | lo), (short)0,
+                                             (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
-__device__ __forceinline__ u32x4_t load_x(const char *base, uint32_t off) { return *(const u32x4_t *)(base + off); }
+
+// load_w: weights, which no other workgroup reads (non-temporal); load_x: activations, which stay in the L2.
+__device__ __forceinline__ u32x4_t load_w(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff)
+{
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 2));
+}
+__device__ __forceinline__ u32x4_t load_x(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff)
+{
+    return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
+}
+__device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, soff, 0));
+}
+// N consecutive floats (4-byte aligned) in one load.
+template <int N>
+__device__ __forceinline__ void load_floats(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff, float (&f)[N])
+{
+    static_assert(N == 1 || N == 2 || N == 4, "one load");
+    if constexpr (N == 1) {
+        f[0] = load_f32(r, off, soff);
+    } else if constexpr (N == 2) {
+        typedef uint32_t u32x2_v __attribute__((ext_vector_type(2)));
+        const u32x2_v v = __builtin_bit_cast(u32x2_v, __builtin_amdgcn_raw_buffer_load_b64(r, off, soff, 0));
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+    } else {
+        const u32x4_t v = load_x(r, off, soff);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+    }
+}
 
 // Sixteen weight rows x 128 bytes come in as two loads of 8 rows x 128 bytes, so that each load reads whole cache lines:
 // non-temporal loads of 16 rows x 64 bytes, which the operand layout below would give, fetch every line twice (measured
@@ -169,6 +200,30 @@ __device__ __forceinline__ void swap_halves(u32x4_t &a, u32x4_t &b)
         const int x = (int)a[j], y = (int)b[j];
         a[j] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, kRor8, 0xF, 0xC, false);
         b[j] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, kRor8, 0xF, 0x3, false);
+    }
+}
+
+// The tokens' operand comes in the same way: 8 tokens x 128 bytes per load, group i of 8 tokens in v[i], two neighbouring
+// groups exchanged into the two halves of a 16-token tile.  A single group (8 tokens or fewer, the ordinary case of a
+// decode step) needs no second load: its own lanes i >= 8 hold the other pieces, one rotation away, and what the
+// columns past 8 get does not matter.  With 16 tokens x 64 bytes per load the loads of four tokens' rows slowed the
+// weight stream by 5%.
+template <int N8>
+__device__ __forceinline__ void pair_tokens(u32x4_t (&v)[N8], u32x4_t (&first)[(N8 + 1) / 2],
+                                            u32x4_t (&second)[(N8 + 1) / 2])
+{
+    if constexpr (N8 == 1) {
+        first[0] = v[0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            second[0][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)v[0][j], (int)v[0][j], 0x128, 0xF, 0xF, false);
+    } else {
+#pragma unroll
+        for (int n = 0; n < N8 / 2; ++n) {
+            first[n] = v[2 * n];
+            second[n] = v[2 * n + 1];
+            swap_halves(first[n], second[n]);
+        }
     }
 }
 
@@ -200,125 +255,34 @@ __device__ __forceinline__ u32x4_t fp8_to_bf16(uint32_t lo, uint32_t hi)
 
 // ---------------------------------------------------------------- gate|up
 
-// acc[r][n] += W tile r (16 rows) x token tile n over K steps s0 .. s1 - 1 of 64.  wo[r][0], wo[r][1]: the lane's byte
-// offsets from w of the tile's rows 0 - 7 and 8 - 15 (swap_halves) at K = 0; xo[n]: of its token from x, with 16 g.  U
-// steps are in flight at a time.
-template <int R, int NT>
-__device__ __forceinline__ void up_bf16(const char *w, const uint32_t (&wo)[R][2], const char *x,
-                                        const uint32_t (&xo)[NT], int s0, int s1, f32x4_t (&acc)[R][NT])
-{
-    int s = s0;
-    auto run = [&](auto uc) {
-        constexpr int U = decltype(uc)::value;
-        u32x4_t wv[R][U][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) wv[r][u][i] = load_w(w, wo[r][i] + (uint32_t)(s + u) * 128);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            u32x4_t xv[U][2];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) xv[u][i] = load_x(x, xo[n] + (uint32_t)(s + u) * 128 + 64 * i);
-            if (n == 0) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) swap_halves(wv[r][u][0], wv[r][u][1]);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) acc[r][n] = mfma_bf16(wv[r][u][i], xv[u][i], acc[r][n]);
-            if (NT >= 4) __builtin_amdgcn_sched_barrier(0);   // keeps later tiles' loads out of the registers
-        }
-        s += U;
-    };
-    constexpr int U = R == 1 ? 4 : NT <= 2 ? 2 : 1;
-    while (s + U <= s1) run(IntC<U>());
-    while (s < s1) run(IntC<1>());
-}
-
-// The same for e4m3 operands over 128-wide blocks b0 .. b1 - 1: a block's product, times the token's and the weights'
-// scales of the block, joins the sum in fp32.  sw[r]: the tile's scales (this lane's rows), sx + so[n]: the lane's token's.
-template <int R, int NT>
-__device__ __forceinline__ void up_q8(const char *w, const uint32_t (&wo)[R][2], const char *x,
-                                      const uint32_t (&xo)[NT], const float *const (&sw)[R], const float *sx,
-                                      const uint32_t (&so)[NT], int b0, int b1, f32x4_t (&acc)[R][NT])
-{
-    int b = b0;
-    auto run = [&](auto uc) {
-        constexpr int U = decltype(uc)::value;
-        u32x4_t wv[R][U][2];
-        float fw[R][U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) wv[r][u][i] = load_w(w, wo[r][i] + (uint32_t)(b + u) * kQ8Group);
-                fw[r][u] = sw[r][b + u];
-            }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            u32x4_t xv[U][2];
-            float fx[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) xv[u][i] = load_x(x, xo[n] + (uint32_t)(b + u) * kQ8Group + 64 * i);
-                fx[u] = sx[so[n] + b + u];
-            }
-            if (n == 0) {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int r = 0; r < R; ++r) swap_halves(wv[r][u][0], wv[r][u][1]);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
-                    p = mfma_fp8_64(wv[r][u][0], xv[u][0], p);
-                    p = mfma_fp8_64(wv[r][u][1], xv[u][1], p);
-                    const float f = fw[r][u] * fx[u];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[r][n][q] = __builtin_fmaf(p[q], f, acc[r][n][q]);
-                }
-            if (NT >= 4) __builtin_amdgcn_sched_barrier(0);   // keeps later tiles' loads out of the registers
-        }
-        b += U;
-    };
-    constexpr int U = R == 1 ? 4 : NT == 1 ? 2 : 1;
-    while (b + U <= b1) run(IntC<U>());
-    while (b < b1) run(IntC<1>());
-}
+template <int N>
+struct IntC {
+    static constexpr int value = N;
+};
 
 constexpr int kUpWaves = 4;
+constexpr int kUpRedBytes = 2 * kUpWaves * 2 * 256 * 4;   // two halves of up_task's exchange
 
-// One gate|up task: features f0 .. f0 + 8 R - 1 of local expert e, whose rows are row0 .. row0 + cnt - 1 (cnt <= 16 NT).
+// One gate|up task: features f0 .. f0 + 8 R - 1 of local expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8).
 // R = 1: one weight tile of 8 gate and 8 up rows; R = 2: a tile of 16 gate rows and one of 16 up rows.
+// The wave sums its share of K in steps of 128 bytes of a weight row (64 bf16, or one 128-wide block of e4m3, whose
+// product is scaled by the token's and the weights' scales before it joins the sum).
 // red: 2 x kUpWaves x R x 256 floats; par: which half the next exchange uses.
-template <bool Q8, int R, int NT>
+template <bool Q8, int R, int N8>
 __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, int e, int f0, int row0, int cnt,
                                         float *red, int &par)
 {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    constexpr int NT = (N8 + 1) / 2;   // 16-column tiles
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
-    f32x4_t acc[R][NT];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    // the lane's weight rows of the expert in each tile (features past F repeat the last; never stored)
-    uint32_t wo[R][2], xo[NT];
+    const uint32_t pitch = (uint32_t)a.d * (Q8 ? 1 : 2);
+    const int steps = (int)(pitch / 128), s0 = steps * wave / kUpWaves, s1 = steps * (wave + 1) / kUpWaves;
+    const uint32_t wbytes = 2 * (uint32_t)a.F * pitch;
+    const __amdgpu_buffer_rsrc_t w = buffer_of((const char *)a.w_gu + (size_t)e * wbytes, wbytes);
+    const __amdgpu_buffer_rsrc_t x = buffer_of(Q8 ? (const void *)a.xq : (const void *)a.x, (uint32_t)a.T * pitch);
+    // the lane's weight rows in each tile (features past F repeat the last; never stored)
+    uint32_t wo[R][2], xo[N8], so[NT];
     if (R == 1) {
         wo[0][0] = f0 + (c & 7);
         wo[0][1] = a.F + wo[0][0];
@@ -329,41 +293,96 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
             wo[R - 1][i] = a.F + wo[0][i];
         }
     }
-    // the lane's token in each tile (columns past cnt repeat the last; never stored)
-    uint32_t tok[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) tok[n] = s.tok[row0 + min(16 * n + c, cnt - 1)];
-    const size_t we = (size_t)e * 2 * a.F * a.d;
-    constexpr int kBytes = Q8 ? 1 : 2;
-    const char *w = (const char *)a.w_gu + we * kBytes, *x = Q8 ? (const char *)a.xq : (const char *)a.x;
-    const uint32_t pitch = (uint32_t)a.d * kBytes;
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) wo[r][i] = wo[r][i] * pitch + 16 * (g + 4 * (c >> 3));
+    // the lane's token in each group of 8 (past cnt the last again; columns never stored)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xo[n] = tok[n] * pitch + 16 * g;
-    if constexpr (Q8) {
-        const int nb = a.d / kQ8Group, nf = (a.F + kQ8Group - 1) / kQ8Group;
-        const float *sw[R];
-        uint32_t so[NT];
-        const float *se = a.s_gu + (size_t)e * 2 * nf * nb + (size_t)(f0 / kQ8Group) * nb;
-        // accumulator rows 4 g .. 4 g + 3: in the mixed tile groups 0, 1 are gate rows and 2, 3 up rows
-        if (R == 1) {
-            sw[0] = se + (g < 2 ? 0 : (size_t)nf * nb);
-        } else {
-            sw[0] = se;
-            sw[R - 1] = se + (size_t)nf * nb;
+    for (int n = 0; n < N8; ++n)
+        xo[n] = s.tok[row0 + min(8 * n + (c & 7), cnt - 1)] * pitch + 16 * (g + 4 * (c >> 3));
+    // 8-bit form: the scales of its column's token (a step is a block)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) so[n] = Q8 ? s.tok[row0 + min(16 * n + c, cnt - 1)] * (uint32_t)steps * 4 : 0;
+    f32x4_t acc[R][NT];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    // 8-bit form: block scales of the wave's share, lane l holds block s0 + l of the gate and of the up rows (at most 64
+    // blocks: d <= 32768 over four waves)
+    int fg = 0, fu = 0;
+    if (Q8) {
+        const int nf = (a.F + kQ8Group - 1) / kQ8Group;
+        const float *sg = a.s_gu + ((size_t)e * 2 * nf + f0 / kQ8Group) * steps + min(s0 + lane, steps - 1);
+        fg = __float_as_int(sg[0]);
+        fu = __float_as_int(sg[(size_t)nf * steps]);
+    }
+    const __amdgpu_buffer_rsrc_t sx = buffer_of(a.xs, (uint32_t)a.T * steps * 4);
+    int k = s0;
+    // U steps: all their loads, then all their products.  (Four workgroups a CU cover each other's waits; a ring of
+    // single steps per wave measured no faster.)
+    auto run = [&](auto uc) {
+        constexpr int U = decltype(uc)::value;
+        u32x4_t wv[U][R][2], xv[U][N8];
+        float fx[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) wv[u][r][i] = load_w(w, wo[r][i] + 128 * u, k * 128);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int n = 0; n < N8; ++n) xv[u][n] = load_x(x, xo[n] + 128 * u, k * 128);
+        if constexpr (Q8) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float f[U];
+                load_floats<U>(sx, so[n], k * 4, f);
+#pragma unroll
+                for (int u = 0; u < U; ++u) fx[u][n] = f[u];
+            }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) so[n] = tok[n] * (uint32_t)nb;
-        up_q8<R, NT>(w, wo, x, xo, sw, a.xs, so, nb * wave / kUpWaves, nb * (wave + 1) / kUpWaves, acc);
-    } else {
-        const int ns = a.d / 64;
-        up_bf16<R, NT>(w, wo, x, xo, ns * wave / kUpWaves, ns * (wave + 1) / kUpWaves, acc);
-    }
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) swap_halves(wv[u][r][0], wv[u][r][1]);
+            u32x4_t x0[NT], x1[NT];
+            pair_tokens<N8>(xv[u], x0, x1);
+            if constexpr (Q8) {
+                const float wg = __int_as_float(__builtin_amdgcn_readlane(fg, k - s0 + u));
+                const float wu = __int_as_float(__builtin_amdgcn_readlane(fu, k - s0 + u));
+                // accumulator rows 4 g .. 4 g + 3: in the mixed tile groups 0, 1 are gate rows and 2, 3 up rows
+                const float fw[2] = {R == 1 ? (g < 2 ? wg : wu) : wg, wu};
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+                        p = mfma_fp8_64(wv[u][r][0], x0[n], p);
+                        p = mfma_fp8_64(wv[u][r][1], x1[n], p);
+                        const float f = fw[r] * fx[u][n];
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[r][n][v] = __builtin_fmaf(p[v], f, acc[r][n][v]);
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int r = 0; r < R; ++r) acc[r][n] = mfma_bf16(wv[u][r][i], i == 0 ? x0[n] : x1[n], acc[r][n]);
+            }
+        }
+        k += U;
+    };
+    constexpr int U = R == 1 ? 4 : N8 == 8 ? 1 : 2;
+    while (k + U <= s1) run(IntC<U>());
+    while (k < s1) run(IntC<1>());
     // The waves' parts of a token tile meet in LDS ([column][row], so a lane's four rows are one 16-byte word), are
-    // added in wave order, and become h.  Halves alternate: one barrier per tile.
+    // added in wave order, and become h, two features a thread.  Halves alternate: one barrier per tile.
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         float *rb = red + par * kUpWaves * R * 256;
@@ -371,29 +390,35 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
 #pragma unroll
         for (int r = 0; r < R; ++r) *(f32x4_t *)(rb + (wave * R + r) * 256 + c * 16 + 4 * g) = acc[r][n];
         __syncthreads();
-        const int fi = (int)threadIdx.x % (8 * R), ci = (int)threadIdx.x / (8 * R);
+        const int fi = 2 * ((int)threadIdx.x % (4 * R)), ci = (int)threadIdx.x / (4 * R);
         const int row = 16 * n + ci;
         if (ci < 16 && row < cnt && f0 + fi < a.F) {
-            float gs = 0.0f, us = 0.0f;
+            float2 gs = make_float2(0.0f, 0.0f), us = gs;
 #pragma unroll
-            for (int w = 0; w < kUpWaves; ++w) {
-                const float *q = rb + w * R * 256 + ci * 16 + fi;
-                gs += q[0];
-                us += q[R == 1 ? 8 : 256];
+            for (int v = 0; v < kUpWaves; ++v) {
+                const float *q = rb + v * R * 256 + ci * 16 + fi;
+                const float2 gv = *(const float2 *)q, uv = *(const float2 *)(q + (R == 1 ? 8 : 256));
+                gs.x += gv.x;
+                gs.y += gv.y;
+                us.x += uv.x;
+                us.y += uv.y;
             }
-            const float v = gs / (1.0f + expf(-gs)) * us * s.gate[row0 + row];
-            a.h[(size_t)(row0 + row) * a.F + f0 + fi] = f32_to_bf16(v);
+            const float gate = s.gate[row0 + row];
+            const float h0 = gs.x / (1.0f + expf(-gs.x)) * us.x * gate;
+            const float h1 = gs.y / (1.0f + expf(-gs.y)) * us.y * gate;
+            *(uint32_t *)(a.h + (size_t)(row0 + row) * a.F + f0 + fi) =
+                (uint32_t)f32_to_bf16(h0) | (uint32_t)f32_to_bf16(h1) << 16;
         }
     }
 }
 
 // SELF: the workgroup selects the experts of the few tokens itself from the router's partial sums.
-template <bool Q8, int R, bool SELF>
+template <bool Q8, bool SELF>
 __global__ __launch_bounds__(64 * kUpWaves, 4) void k_layer_up(LayerArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     float *red = (float *)lds;
-    const RowsLds s = rows_lds(lds + 2 * kUpWaves * R * 256 * 4, a, true);
+    const RowsLds s = rows_lds(lds + kUpRedBytes, a, true);
     const int T = valid_tokens(a);
     if constexpr (SELF) {
         const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -433,176 +458,210 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_layer_up(LayerArgs a)
             if (a.w_user) a.w_user[i] = s.w[i];
         }
     build_rows(s, a, T);
-    const int nf = (a.F + 8 * R - 1) / (8 * R);
-    const int tasks = s.n[0] * nf;
+    // Tasks of 16 features, two weight tiles beside one load of the tokens.  Where they are too few to give every CU a
+    // couple (a token or two at a few experts), of 8.
+    const int hits = s.n[0];
+    const bool small = a.T <= 16 && (long)hits * ((a.F + 15) / 16) < a.few_tasks;
+    const int fs = small ? 8 : 16;
+    const int nf = (a.F + fs - 1) / fs;
     int par = 0;
-    for (int q = blockIdx.x; q < tasks; q += gridDim.x) {
-        const int hi = q / nf, f0 = (q - hi * nf) * 8 * R;
+    for (int q = blockIdx.x; q < hits * nf; q += gridDim.x) {
+        const int hi = q / nf, f0 = (q - hi * nf) * fs;
         const int e = __builtin_amdgcn_readfirstlane(s.hit[hi]);
         const int row0 = __builtin_amdgcn_readfirstlane(s.start[e]);
         const int cnt = __builtin_amdgcn_readfirstlane(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1]));
-        if (R == 1 || cnt <= 16) up_task<Q8, R, 1>(a, s, e, f0, row0, cnt, red, par);
-        else if (cnt <= 32) up_task<Q8, R, 2>(a, s, e, f0, row0, cnt, red, par);
-        else if (cnt <= 64) up_task<Q8, R, 4>(a, s, e, f0, row0, cnt, red, par);
-        else up_task<Q8, R, 8>(a, s, e, f0, row0, cnt, red, par);
+        if (small) {
+            if (cnt <= 8) up_task<Q8, 1, 1>(a, s, e, f0, row0, cnt, red, par);
+            else up_task<Q8, 1, 2>(a, s, e, f0, row0, cnt, red, par);
+            continue;
+        }
+        // up to 64 rows at once; an expert of more than 64 rows reads its weights again for the rest
+        for (int r = 0; r < cnt; r += 64) {
+            const int m = min(cnt - r, 64);
+            if (m <= 8) up_task<Q8, 2, 1>(a, s, e, f0, row0 + r, m, red, par);
+            else if (m <= 16) up_task<Q8, 2, 2>(a, s, e, f0, row0 + r, m, red, par);
+            else if (m <= 32) up_task<Q8, 2, 4>(a, s, e, f0, row0 + r, m, red, par);
+            else up_task<Q8, 2, 8>(a, s, e, f0, row0 + r, m, red, par);
+        }
     }
 }
 
 // ---------------------------------------------------------------- down
 
-constexpr int kDownWaves = 4;
-
-// One expert's part of 16 output columns: acc[n] = sum over K of W_down rows x h rows of token tile n, for this wave's
-// share of K.  wo: the lane's byte offsets from w of the rows 0 - 7 and 8 - 15 (swap_halves), ho[n]: of its h row from h
-// with 16 g, all at K = 0.  kp: the lane's piece of a weight row, in elements.
-template <int NT>
-__device__ __forceinline__ void down_bf16(const char *w, const uint32_t (&wo)[2], int kp, const char *h,
-                                          const uint32_t (&ho)[NT], int F, int wave, f32x4_t (&acc)[NT])
+// Steps of a stream held in registers: the loads of step s + D are issued as soon as step s has been used, so D steps
+// are always on their way.  total: the steps; load(slot): the next step's loads; use(slot): the oldest step's products.
+// The order is pinned, and the loop without conditions covers all but the last 2 D - 1 steps.
+template <int D, class Slot, class Load, class Use>
+__device__ __forceinline__ void stream(int total, Load &&load, Use &&use)
 {
-    const int ns = F / 64;
-    int s = ns * wave / kDownWaves;
-    const int s1 = ns * (wave + 1) / kDownWaves;
-    const int kh = 8 * (int)(threadIdx.x % kWave >> 4);
-    auto run = [&](auto uc, auto partial) {
-        constexpr int U = decltype(uc)::value;
-        // PARTIAL: the last step, with F % 64 of K left; pieces past F are zeros on both sides
-        constexpr bool PARTIAL = decltype(partial)::value != 0;
-        const int left = PARTIAL ? F % 64 : 64;
-        const u32x4_t z = {0u, 0u, 0u, 0u};
-        u32x4_t wv[U][2];
+    Slot ring[D];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+    for (int j = 0; j < D; ++j)
+        if (j < total) load(ring[j]);
+    int i = 0;
+    for (; i + 2 * D <= total; i += D) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                wv[u][i] = !PARTIAL || kp < left ? load_w(w, wo[i] + (uint32_t)(s + u) * 128) : z;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            u32x4_t hv[U][2];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    hv[u][i] = !PARTIAL || kh + 32 * i < left ? load_x(h, ho[n] + (uint32_t)(s + u) * 128 + 64 * i) : z;
-            if (n == 0) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) swap_halves(wv[u][0], wv[u][1]);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) acc[n] = mfma_bf16(wv[u][i], hv[u][i], acc[n]);
-            if (NT >= 4) __builtin_amdgcn_sched_barrier(0);   // keeps later tiles' loads out of the registers
+        for (int j = 0; j < D; ++j) {
+            use(ring[j]);
+            __builtin_amdgcn_sched_barrier(0);
+            load(ring[j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        s += U;
-    };
-    constexpr int U = NT == 1 ? 4 : 2;
-    while (s + U <= s1) run(IntC<U>(), IntC<0>());
-    while (s < s1) run(IntC<1>(), IntC<0>());
-    if (F % 64 != 0 && wave == kDownWaves - 1) run(IntC<1>(), IntC<1>());
-}
-
-// The same with e4m3 weights, converted to bf16 (exact) in front of the matrix core; sw: the column tile's scales, one
-// per 128 of K.  Lane group g holds K elements 16 g .. 16 g + 15 of a 64-wide half block in both operands.
-template <int NT>
-__device__ __forceinline__ void down_q8(const char *w, const uint32_t (&wo)[2], int kp, const char *h,
-                                        const uint32_t (&ho)[NT], const float *sw, int F, int wave,
-                                        f32x4_t (&acc)[NT])
-{
-    const int nb = F / kQ8Group;
-    int b = nb * wave / kDownWaves;
-    const int b1 = nb * (wave + 1) / kDownWaves;
-    const int kh = 16 * (int)(threadIdx.x % kWave >> 4);
-    auto run = [&](auto uc, auto partial) {
-        constexpr int U = decltype(uc)::value;
-        // PARTIAL: the last block, with F % 128 of K left; pieces past F are zeros on both sides
-        constexpr bool PARTIAL = decltype(partial)::value != 0;
-        const int left = PARTIAL ? F % kQ8Group : kQ8Group;
-        const u32x4_t z = {0u, 0u, 0u, 0u};
-        u32x4_t wv[U][2];
-        float fw[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                wv[u][i] = !PARTIAL || kp < left ? load_w(w, wo[i] + (uint32_t)(b + u) * kQ8Group) : z;
-            fw[u] = sw[b + u];
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            u32x4_t hv[U][4];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    hv[u][i] = !PARTIAL || kh + 64 * (i / 2) < left
-                                   ? load_x(h, ho[n] + (uint32_t)(b + u) * (2 * kQ8Group) + 128 * (i / 2) + 16 * (i & 1))
-                                   : z;
-            if (n == 0) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) swap_halves(wv[u][0], wv[u][1]);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const u32x4_t v = wv[u][i];
-                    p = mfma_bf16(fp8_to_bf16(v.x, v.y), hv[u][2 * i], p);
-                    p = mfma_bf16(fp8_to_bf16(v.z, v.w), hv[u][2 * i + 1], p);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[n][q] = __builtin_fmaf(p[q], fw[u], acc[n][q]);
-            }
-            if (NT >= 4) __builtin_amdgcn_sched_barrier(0);   // keeps later tiles' loads out of the registers
-        }
-        b += U;
-    };
-    constexpr int U = NT == 1 ? 2 : 1;
-    while (b + U <= b1) run(IntC<U>(), IntC<0>());
-    while (b < b1) run(IntC<1>(), IntC<0>());
-    if (F % kQ8Group != 0 && wave == kDownWaves - 1) run(IntC<1>(), IntC<1>());
-}
-
-// Adds local expert e's part of output columns n0 .. n0 + 15 to the wave's sums ([T][16] in LDS).
-template <bool Q8, int NT>
-__device__ __forceinline__ void down_expert(const LayerArgs &a, const RowsLds &s, int e, int n0, int row0, int cnt,
-                                            float *sum)
-{
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int c = lane & 15, g = lane >> 4;
-    f32x4_t acc[NT];
-    uint32_t ho[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        acc[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        ho[n] = (uint32_t)min(16 * n + c, cnt - 1) * (uint32_t)(2 * a.F) + (Q8 ? 32 : 16) * g;
     }
-    const char *h = (const char *)(a.h + (size_t)row0 * a.F);
-    const char *w = (const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * (Q8 ? 1 : 2);
-    const int piece = g + 4 * (c >> 3);
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+        if (i + j < total) use(ring[j]);
+        if (i + j + D < total) load(ring[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < D; ++j)
+        if (i + D + j < total) use(ring[j]);
+}
+
+// Registers a step takes decide how many are in flight: about 72 of the 128 a wave has.
+constexpr int ring_depth(int regs) { return regs <= 18 ? 4 : regs <= 26 ? 3 : regs <= 36 ? 2 : 1; }
+
+constexpr int kDownWaves = 8;
+
+// Groups of 8 tokens that an expert's rows are taken in (more than 64 rows: several times 8 groups).
+__device__ __forceinline__ int groups_of(int cnt) { return cnt <= 8 ? 1 : cnt <= 16 ? 2 : cnt <= 32 ? 4 : 8; }
+
+// Adds the parts of the hit experts h0 .. h1 - 1 (all taken in N8 groups of 8 tokens) to the wave's sums of output columns
+// n0 .. n0 + 15 ([T][16] in LDS): one stream of steps through all of them, over the wave's share of K of each.  A step is
+// 128 bytes of a weight row: 64 of K, or 128 of K in e4m3, converted to bf16 (exact) in front of the matrix core.
+// TAIL: F does not end on a step; pieces past F are zeros on both sides.
+template <bool Q8, int N8, bool TAIL>
+__device__ __forceinline__ void down_run(const LayerArgs &a, const RowsLds &s, int h0, int h1, int n0, float *sum)
+{
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int c = lane & 15, g = lane >> 4;
+    constexpr int NT = (N8 + 1) / 2;             // 16-column tiles
+    constexpr int KS = Q8 ? kQ8Group : 64;       // K per step
+    constexpr int KP = Q8 ? 16 : 8;              // K per 16-byte piece of a weight row
+    constexpr int kBytes = Q8 ? 1 : 2;
+    constexpr int HL = Q8 ? 2 : 1;               // 128-byte lines of an h row per step
+    const int steps = (a.F + KS - 1) / KS, mine = (steps - wave + kDownWaves - 1) / kDownWaves;
+    if (mine <= 0) return;
+    const int kp = KP * (g + 4 * (c >> 3));      // the lane's piece of a weight row (swap_halves)
+    // ... and of an h line (pair_tokens), 8 elements: bf16 pieces g and 4 + g, as the weights; e4m3, whose 16-byte piece
+    // is two pieces of h, 2 g and 2 g + 1
+    const int kh = 8 * (Q8 ? 2 * g + (c >> 3) : g + 4 * (c >> 3));
     uint32_t wo[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)((8 * i + (c & 7)) * a.F) * (Q8 ? 1 : 2) + 16 * piece;
-    if constexpr (Q8) {
-        const int nf = (a.F + kQ8Group - 1) / kQ8Group;
-        down_q8<NT>(w, wo, 16 * piece, h, ho, a.s_dn + ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * nf, a.F, wave, acc);
-    } else {
-        down_bf16<NT>(w, wo, 8 * piece, h, ho, a.F, wave, acc);
-    }
-    // tokens of an expert are distinct, so no two lanes add to one word
+    for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)((8 * i + (c & 7)) * a.F + kp) * kBytes;
+    struct Slot {
+        u32x4_t w[2], h[HL][N8];
+        float fw;
+    };
+    // the loading end: hit expert lh, rows lr .. of it, step ls
+    int lh = h0, lr = 0, ls = wave, lcnt = 0;
+    __amdgpu_buffer_rsrc_t lw, lhp, lsw;
+    uint32_t lo[N8];
+    int total = 0;
+    auto expert_at = [&](int hi, int &e, int &row0, int &cnt) {
+        e = __builtin_amdgcn_readfirstlane(s.hit[hi]);
+        row0 = __builtin_amdgcn_readfirstlane(s.start[e]);
+        cnt = __builtin_amdgcn_readfirstlane(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1]));
+    };
+    auto load_setup = [&]() {
+        int e, row0;
+        expert_at(lh, e, row0, lcnt);
+        lw = buffer_of((const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * kBytes, 16 * (uint32_t)a.F * kBytes);
+        lhp = buffer_of(a.h + (size_t)row0 * a.F, (uint32_t)lcnt * 2 * a.F);
+        if (Q8) lsw = buffer_of(a.s_dn + ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * steps, steps * 4);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (16 * n + c < cnt) {
-            f32x4_t *p = (f32x4_t *)(sum + (int)s.tok[row0 + 16 * n + c] * 16 + 4 * g);
-            f32x4_t v = *p;
+        for (int n = 0; n < N8; ++n)
+            lo[n] = (uint32_t)(min(lr + 8 * n + (c & 7), lcnt - 1) * a.F + kh) * 2;
+    };
+    // the using end
+    int uh = h0, ur = 0, us = 0;
+    f32x4_t acc[NT];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] += acc[n][q];
-            *p = v;
-        }
+    for (int n = 0; n < NT; ++n) acc[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int hi = h0; hi < h1; ++hi) {
+        int e, row0, cnt;
+        expert_at(hi, e, row0, cnt);
+        total += (cnt + 8 * N8 - 1) / (8 * N8);
     }
+    total *= mine;
+    load_setup();
+    stream<ring_depth(8 + 4 * HL * N8), Slot>(
+        total,
+        [&](Slot &q) {
+            const uint32_t kw = (uint32_t)ls * 128;
+            const int left = a.F - ls * KS;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) q.w[i] = load_w(lw, !TAIL || kp < left ? wo[i] : kPastResource, kw);
+#pragma unroll
+            for (int l = 0; l < HL; ++l)
+#pragma unroll
+                for (int n = 0; n < N8; ++n)
+                    q.h[l][n] = load_x(lhp, !TAIL || kh + 64 * l < left ? lo[n] + 128 * l : kPastResource, kw * HL);
+            if (Q8) q.fw = load_f32(lsw, 0, ls * 4);
+            if ((ls += kDownWaves) >= steps) {
+                ls = wave;
+                lr += 8 * N8;
+                if (lr >= lcnt) {
+                    lr = 0;
+                    ++lh;
+                }
+                if (lh < h1) load_setup();
+            }
+        },
+        [&](Slot &q) {
+            swap_halves(q.w[0], q.w[1]);
+            u32x4_t x[HL][2][NT];
+#pragma unroll
+            for (int l = 0; l < HL; ++l) pair_tokens<N8>(q.h[l], x[l][0], x[l][1]);
+            if constexpr (Q8) {
+                u32x4_t b[4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    b[2 * i] = fp8_to_bf16(q.w[i].x, q.w[i].y);
+                    b[2 * i + 1] = fp8_to_bf16(q.w[i].z, q.w[i].w);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p = mfma_bf16(b[i], x[HL - 1 & i / 2][i & 1][n], p);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[n][v] = __builtin_fmaf(p[v], q.fw, acc[n][v]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[n] = mfma_bf16(q.w[i], x[0][i][n], acc[n]);
+            }
+            if (++us == mine) {
+                us = 0;
+                int e, row0, cnt;
+                expert_at(uh, e, row0, cnt);
+                // tokens of an expert are distinct, so no two lanes add to one word
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int row = ur + 16 * n + c;
+                    if (row < cnt) {
+                        f32x4_t *p = (f32x4_t *)(sum + (int)s.tok[row0 + row] * 16 + 4 * g);
+                        f32x4_t v = *p;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] += acc[n][j];
+                        *p = v;
+                    }
+                    acc[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+                ur += 8 * N8;
+                if (ur >= cnt) {
+                    ur = 0;
+                    ++uh;
+                }
+            }
+        });
 }
 
-template <bool Q8>
+template <bool Q8, bool TAIL>
 __global__ __launch_bounds__(64 * kDownWaves, 4) void k_layer_down(LayerArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -618,14 +677,20 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_layer_down(LayerArgs a)
     for (int q = blockIdx.x; q < a.d / 16; q += gridDim.x) {
         const int n0 = 16 * q;
         for (int i = lane; i < T * 4; i += kWave) ((f32x4_t *)sum)[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int hi = 0; hi < hits; ++hi) {
-            const int e = __builtin_amdgcn_readfirstlane(s.hit[hi]);
-            const int row0 = __builtin_amdgcn_readfirstlane(s.start[e]);
-            const int cnt = __builtin_amdgcn_readfirstlane(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1]));
-            if (cnt <= 16) down_expert<Q8, 1>(a, s, e, n0, row0, cnt, sum);
-            else if (cnt <= 32) down_expert<Q8, 2>(a, s, e, n0, row0, cnt, sum);
-            else if (cnt <= 64) down_expert<Q8, 4>(a, s, e, n0, row0, cnt, sum);
-            else down_expert<Q8, 8>(a, s, e, n0, row0, cnt, sum);
+        // runs of experts that take the same number of token groups, in expert order
+        for (int h0 = 0; h0 < hits;) {
+            auto groups = [&](int hi) {
+                const int e = s.hit[hi];
+                return __builtin_amdgcn_readfirstlane(groups_of(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1])));
+            };
+            const int n8 = groups(h0);
+            int h1 = h0 + 1;
+            while (h1 < hits && groups(h1) == n8) ++h1;
+            if (n8 == 1) down_run<Q8, 1, TAIL>(a, s, h0, h1, n0, sum);
+            else if (n8 == 2) down_run<Q8, 2, TAIL>(a, s, h0, h1, n0, sum);
+            else if (n8 == 4) down_run<Q8, 4, TAIL>(a, s, h0, h1, n0, sum);
+            else down_run<Q8, 8, TAIL>(a, s, h0, h1, n0, sum);
+            h0 = h1;
         }
         __syncthreads();
         // two neighbouring columns per thread, waves in order
@@ -732,17 +797,19 @@ int device_cus()
     return cus;
 }
 
-template <bool Q8, int R>
+template <bool Q8>
 hipError_t launch_up(const LayerArgs &a, bool self, int grid, hipStream_t s)
 {
-    const size_t lds = 2 * kUpWaves * R * 256 * 4 + rows_lds_bytes(a.T, a.k, a.E_local, true);
-    if constexpr (R == 1) {   // kLayerSelfT <= 16
-        if (self) {
-            hipLaunchKernelGGL((k_layer_up<Q8, 1, true>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
-            return hipGetLastError();
-        }
-    }
-    hipLaunchKernelGGL((k_layer_up<Q8, R, false>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
+    const size_t lds = kUpRedBytes + rows_lds_bytes(a.T, a.k, a.E_local, true);
+    if (self) hipLaunchKernelGGL((k_layer_up<Q8, true>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
+    else hipLaunchKernelGGL((k_layer_up<Q8, false>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
+    return hipGetLastError();
+}
+
+template <bool Q8, bool TAIL>
+hipError_t launch_down(const LayerArgs &a, int grid, size_t lds, hipStream_t s)
+{
+    hipLaunchKernelGGL((k_layer_down<Q8, TAIL>), dim3(grid), dim3(64 * kDownWaves), lds, s, a);
     return hipGetLastError();
 }
 
@@ -759,21 +826,19 @@ hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s)
 {
     const int cus = device_cus();
     if (cus <= 0) return hipErrorInvalidDevice;
-    const int R = a.T <= 16 ? 1 : 2;
-    const long nf = (a.F + 8 * R - 1) / (8 * R);
-    const long most = (long)std::min(a.E_local, a.T * a.k) * nf;   // tasks, if every choice is another local expert
-    const int grid = (int)std::min<long>(most, 4L * cus);
-    hipError_t e;
-    if (q8) e = R == 1 ? launch_up<true, 1>(a, self, grid, s) : launch_up<true, 2>(a, self, grid, s);
-    else e = R == 1 ? launch_up<false, 1>(a, self, grid, s) : launch_up<false, 2>(a, self, grid, s);
-    if (e != hipSuccess) return e;
     LayerArgs b = a;
+    b.few_tasks = 2 * cus;
+    const long most = (long)std::min(a.E_local, a.T * a.k) * ((a.F + 7) / 8);   // tasks, if every choice is another local expert
+    const int grid = (int)std::min<long>(most, 4L * cus);
+    const hipError_t e = q8 ? launch_up<true>(b, self, grid, s) : launch_up<false>(b, self, grid, s);
+    if (e != hipSuccess) return e;
     if (self) b.ids = a.ids_ws;
     const size_t lds = (size_t)kDownWaves * a.T * 64 + rows_lds_bytes(a.T, a.k, a.E_local, false);
     const int gd = std::min(a.d / 16, 4 * cus);
-    if (q8) hipLaunchKernelGGL(k_layer_down<true>, dim3(gd), dim3(64 * kDownWaves), lds, s, b);
-    else hipLaunchKernelGGL(k_layer_down<false>, dim3(gd), dim3(64 * kDownWaves), lds, s, b);
-    return hipGetLastError();
+    const bool tail = a.F % (q8 ? kQ8Group : 64) != 0;
+    if (q8 && tail) return launch_down<true, true>(b, gd, lds, s);
+    if (q8) return launch_down<true, false>(b, gd, lds, s);
+    return tail ? launch_down<false, true>(b, gd, lds, s) : launch_down<false, false>(b, gd, lds, s);
 }
 
 }  // namespace mk
