@@ -482,18 +482,24 @@ void *g_scratch_dev[kMaxDevices];
 
 // ---------------------------------------------------------------- the few-token MoE layer
 
-// Workspace: router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] bf16.
+// Workspace: the plan, router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] bf16 and
+// y [T min(k, E_local), d] fp32.
 struct LayerWs {
-    size_t ids, w, h, total;
+    size_t rec, row_of, part, ids, w, h, y, total;
 };
 
 LayerWs layer_ws(const mk_shape *s)
 {
+    const size_t rows = (size_t)layer_rows_cap(s->T, s->k, s->E_local), tk = (size_t)s->T * s->k;
     LayerWs L;
-    L.ids = align256((size_t)kRouterSegments * s->T * s->E * 4);
-    L.w = L.ids + align256((size_t)s->T * s->k * 4);
-    L.h = L.w + align256((size_t)s->T * s->k * 4);
-    L.total = L.h + align256((size_t)s->T * std::min(s->k, s->E_local) * (s->N / 2) * 2) + 256;
+    L.rec = 256;
+    L.row_of = L.rec + align256((size_t)layer_hits_cap(s->T, s->k, s->E_local) * sizeof(LayerRec));
+    L.part = L.row_of + align256(tk * 4);
+    L.ids = L.part + align256((size_t)kRouterSegments * s->T * s->E * 4);
+    L.w = L.ids + align256(tk * 4);
+    L.h = L.w + align256(tk * 4);
+    L.y = L.h + align256(rows * (s->N / 2) * 2);
+    L.total = L.y + align256(rows * s->d * 4) + 256;
     return L;
 }
 
@@ -538,15 +544,19 @@ mk_status layer_impl(const mk_shape *s, bool q8, const void *x, const void *x_q8
     a.w_dn = w_down;
     a.s_gu = gate_up_scale;
     a.s_dn = down_scale;
-    a.ids_ws = (int32_t *)(ws + L.ids);
-    a.ids = given ? topk_ids_in : a.ids_ws;
+    int32_t *ids_ws = (int32_t *)(ws + L.ids);
+    a.ids = given ? topk_ids_in : ids_ws;
     a.gates = given ? topk_w_in : (const float *)(ws + L.w);
     a.ids_user = topk_ids_out;
     a.w_user = topk_w_out;
-    a.part = (float *)ws;
+    a.part = (float *)(ws + L.part);
     a.wr = w_router;
     a.bias = bias;
+    a.plan.n = (int32_t *)ws;
+    a.plan.rec = (LayerRec *)(ws + L.rec);
+    a.plan.row_of = (int32_t *)(ws + L.row_of);
     a.h = (uint16_t *)(ws + L.h);
+    a.y = (float *)(ws + L.y);
     a.out = (uint16_t *)out;
     a.t_valid = t_valid;
     a.T = s->T;
@@ -577,7 +587,7 @@ mk_status layer_impl(const mk_shape *s, bool q8, const void *x, const void *x_q8
             TopkArgs ta{};
             ta.part = a.part;
             ta.bias = bias;
-            ta.ids = a.ids_ws;
+            ta.ids = ids_ws;
             ta.w_user = (float *)(ws + L.w);
             ta.T = s->T;
             ta.E = s->E;

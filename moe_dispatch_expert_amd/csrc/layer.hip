@@ -11,10 +11,14 @@
 //     the tokens of the expert its B operand (16 columns), loaded from the L2;
 //   - K is split over the waves of a workgroup, so that a workgroup's unit of
 //     work is a thin slab of weights and a few experts already fill the device;
-//   - the down kernel owns output columns over all experts, so the combine is a
-//     sum inside one workgroup in a fixed order: no atomics, no second pass.
-// Two kernels follow the router: "up" writes h = w * silu(g) * u (bf16, the
-// gate folded in before the one rounding), "down" sums W_down[e] . h.
+//   - few waves with many registers each: a wave's loads of the next steps are
+//     all on their way before it multiplies (two workgroups of four waves per CU
+//     stream the weights as fast as four of them, with a quarter of the
+//     instructions' register pressure).
+// Launches: the router and the selection (unless the caller routed), "up", which
+// writes h = w * silu(g) * u (bf16, the gate folded in before the one rounding),
+// "down", which writes W_down[e] . h per row in fp32, and "sum", which adds each
+// token's rows in expert order.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -40,24 +44,21 @@ struct RowsLds {
     int32_t *hit;       // [<= min(E_local, T k)] experts with rows
     int32_t *n;         // [2] number of hit experts, number of rows
     uint8_t *tok;       // [T min(k, E_local)]
-    float *gate;        // [T min(k, E_local)] or nullptr (down kernel)
+    float *gate;        // [T min(k, E_local)]
     int32_t *ids;       // [T k]
-    float *w;           // [T k] (up kernel)
+    float *w;           // [T k]
 };
 
-__host__ __device__ inline int rows_cap(int T, int k, int E_local) { return T * (k < E_local ? k : E_local); }
-
-__host__ __device__ inline size_t rows_lds_bytes(int T, int k, int E_local, bool gates)
+__host__ __device__ inline size_t rows_lds_bytes(int T, int k, int E_local)
 {
-    const size_t r = (size_t)rows_cap(T, k, E_local), tk = (size_t)T * k;
-    const size_t hits = (size_t)E_local < tk ? (size_t)E_local : tk;
-    size_t b = (size_t)E_local * 20 + hits * 4 + 8 + tk * 4 + (gates ? (tk + r) * 4 : 0) + r;
+    const size_t r = (size_t)layer_rows_cap(T, k, E_local), tk = (size_t)T * k;
+    const size_t b = (size_t)E_local * 20 + (size_t)layer_hits_cap(T, k, E_local) * 4 + 8 + (2 * tk + r) * 4 + r;
     return (b + 15) & ~(size_t)15;
 }
 
-__device__ __forceinline__ RowsLds rows_lds(char *p, const LayerArgs &a, bool gates)
+__device__ __forceinline__ RowsLds rows_lds(char *p, const LayerArgs &a)
 {
-    const int r = rows_cap(a.T, a.k, a.E_local), tk = a.T * a.k;
+    const int r = layer_rows_cap(a.T, a.k, a.E_local), tk = a.T * a.k;
     RowsLds s;
     s.mask = (uint64_t *)p;
     p += (size_t)a.E_local * 16;
@@ -69,13 +70,10 @@ __device__ __forceinline__ RowsLds rows_lds(char *p, const LayerArgs &a, bool ga
     p += 8;
     s.ids = (int32_t *)p;
     p += (size_t)tk * 4;
-    s.w = s.gate = nullptr;
-    if (gates) {
-        s.w = (float *)p;
-        p += (size_t)tk * 4;
-        s.gate = (float *)p;
-        p += (size_t)r * 4;
-    }
+    s.w = (float *)p;
+    p += (size_t)tk * 4;
+    s.gate = (float *)p;
+    p += (size_t)r * 4;
     s.tok = (uint8_t *)p;
     return s;
 }
@@ -86,8 +84,9 @@ __device__ __forceinline__ int rank_of(const uint64_t *m, int t)
     return t < 64 ? __popcll(m[0] & ((1ull << t) - 1)) : __popcll(m[0]) + __popcll(m[1] & ((1ull << (t - 64)) - 1));
 }
 
-// Builds the rows from s.ids (and s.w), which the caller has filled for tokens < T; ends with a barrier.
-__device__ __forceinline__ void build_rows(const RowsLds &s, const LayerArgs &a, int T)
+// Builds the rows from s.ids and s.w, which the caller has filled for tokens < T; ends with a barrier.  publish: this
+// workgroup also writes what the later kernels need.
+__device__ __forceinline__ void build_rows(const RowsLds &s, const LayerArgs &a, int T, bool publish)
 {
     for (int i = threadIdx.x; i < 2 * a.E_local; i += blockDim.x) s.mask[i] = 0;
     __syncthreads();
@@ -110,31 +109,42 @@ __device__ __forceinline__ void build_rows(const RowsLds &s, const LayerArgs &a,
                 if (l >= o) incl += v;
             }
             const uint64_t b = __ballot(cnt > 0);
-            if (e < a.E_local) s.start[e] = rows + incl - cnt;
-            if (cnt > 0) s.hit[hits + __popcll(b & lanemask_lt())] = e;
+            const int hi = hits + __popcll(b & lanemask_lt()), row0 = rows + incl - cnt;
+            if (e < a.E_local) s.start[e] = row0;
+            if (cnt > 0) {
+                s.hit[hi] = e;
+                if (publish) a.plan.rec[hi] = LayerRec{e, row0, cnt, 0};
+            }
             rows += __shfl(incl, kWave - 1);
             hits += __popcll(b);
         }
         if (l == 0) {
             s.n[0] = hits;
             s.n[1] = rows;
+            if (publish) {
+                a.plan.n[0] = hits;
+                a.plan.n[1] = T;
+            }
         }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < T * a.k; i += blockDim.x) {
         const int t = i / a.k, id = s.ids[i], e = id - a.e_begin;
-        if (e < 0 || e >= a.E_local) continue;
-        bool first = true;
-        float w = s.w ? s.w[i] : 0.0f;
-        if (a.given) {   // an id given twice for a token: one row, the gates added up
-            for (int j = t * a.k; j < i; ++j) first &= s.ids[j] != id;
-            if (s.w)
+        int r = -1;
+        if (e >= 0 && e < a.E_local) {
+            bool first = true;
+            float w = s.w[i];
+            if (a.given) {   // an id given twice for a token: one row, the gates added up
+                for (int j = t * a.k; j < i; ++j) first &= s.ids[j] != id;
                 for (int j = i + 1; j < (t + 1) * a.k; ++j) w += s.ids[j] == id ? s.w[j] : 0.0f;
+            }
+            if (first) {
+                r = s.start[e] + rank_of(s.mask + 2 * e, t);
+                s.tok[r] = (uint8_t)t;
+                s.gate[r] = w;
+            }
         }
-        if (!first) continue;
-        const int r = s.start[e] + rank_of(s.mask + 2 * e, t);
-        s.tok[r] = (uint8_t)t;
-        if (s.gate) s.gate[r] = w;
+        if (publish) a.plan.row_of[i] = r;
     }
     __syncthreads();
 }
@@ -414,11 +424,11 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
 
 // SELF: the workgroup selects the experts of the few tokens itself from the router's partial sums.
 template <bool Q8, bool SELF>
-__global__ __launch_bounds__(64 * kUpWaves, 4) void k_layer_up(LayerArgs a)
+__global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     float *red = (float *)lds;
-    const RowsLds s = rows_lds(lds + kUpRedBytes, a, true);
+    const RowsLds s = rows_lds(lds + kUpRedBytes, a);
     const int T = valid_tokens(a);
     if constexpr (SELF) {
         const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -442,7 +452,6 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_layer_up(LayerArgs a)
             if (lane < a.k) {
                 s.ids[t * a.k + lane] = p.id;
                 s.w[t * a.k + lane] = p.gate();
-                if (blockIdx.x == 0) a.ids_ws[t * a.k + lane] = p.id;
             }
         }
     } else {
@@ -457,7 +466,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_layer_up(LayerArgs a)
             if (a.ids_user) a.ids_user[i] = s.ids[i];
             if (a.w_user) a.w_user[i] = s.w[i];
         }
-    build_rows(s, a, T);
+    build_rows(s, a, T, blockIdx.x == 0);
     // Tasks of 16 features, two weight tiles beside one load of the tokens.  Where they are too few to give every CU a
     // couple (a token or two at a few experts), of 8.
     const int hits = s.n[0];
@@ -488,226 +497,185 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_layer_up(LayerArgs a)
 
 // ---------------------------------------------------------------- down
 
-// Steps of a stream held in registers: the loads of step s + D are issued as soon as step s has been used, so D steps
-// are always on their way.  total: the steps; load(slot): the next step's loads; use(slot): the oldest step's products.
-// The order is pinned, and the loop without conditions covers all but the last 2 D - 1 steps.
-template <int D, class Slot, class Load, class Use>
-__device__ __forceinline__ void stream(int total, Load &&load, Use &&use)
+constexpr int kDownWaves = 4;
+constexpr int kDownRedBytes = 2 * kDownWaves * 2 * 256 * 4;
+
+// One down task: output columns n0 .. n0 + 16 R - 1 of expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8), written
+// to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3,
+// converted to bf16 (exact) in front of the matrix core and scaled per step.  TAIL: F does not end on a step; pieces past
+// F are zeros on both sides.  red, par: as in up_task.
+template <bool Q8, int R, int N8, bool TAIL>
+__device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int row0, int cnt, float *red, int &par)
 {
-    Slot ring[D];
-#pragma unroll
-    for (int j = 0; j < D; ++j)
-        if (j < total) load(ring[j]);
-    int i = 0;
-    for (; i + 2 * D <= total; i += D) {
-#pragma unroll
-        for (int j = 0; j < D; ++j) {
-            use(ring[j]);
-            __builtin_amdgcn_sched_barrier(0);
-            load(ring[j]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < D; ++j) {
-        if (i + j < total) use(ring[j]);
-        if (i + j + D < total) load(ring[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < D; ++j)
-        if (i + D + j < total) use(ring[j]);
-}
-
-// Registers a step takes decide how many are in flight: about 72 of the 128 a wave has.
-constexpr int ring_depth(int regs) { return regs <= 18 ? 4 : regs <= 26 ? 3 : regs <= 36 ? 2 : 1; }
-
-constexpr int kDownWaves = 8;
-
-// Groups of 8 tokens that an expert's rows are taken in (more than 64 rows: several times 8 groups).
-__device__ __forceinline__ int groups_of(int cnt) { return cnt <= 8 ? 1 : cnt <= 16 ? 2 : cnt <= 32 ? 4 : 8; }
-
-// Adds the parts of the hit experts h0 .. h1 - 1 (all taken in N8 groups of 8 tokens) to the wave's sums of output columns
-// n0 .. n0 + 15 ([T][16] in LDS): one stream of steps through all of them, over the wave's share of K of each.  A step is
-// 128 bytes of a weight row: 64 of K, or 128 of K in e4m3, converted to bf16 (exact) in front of the matrix core.
-// TAIL: F does not end on a step; pieces past F are zeros on both sides.
-template <bool Q8, int N8, bool TAIL>
-__device__ __forceinline__ void down_run(const LayerArgs &a, const RowsLds &s, int h0, int h1, int n0, float *sum)
-{
-    const int lane = threadIdx.x % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-    const int c = lane & 15, g = lane >> 4;
     constexpr int NT = (N8 + 1) / 2;             // 16-column tiles
     constexpr int KS = Q8 ? kQ8Group : 64;       // K per step
     constexpr int KP = Q8 ? 16 : 8;              // K per 16-byte piece of a weight row
     constexpr int kBytes = Q8 ? 1 : 2;
     constexpr int HL = Q8 ? 2 : 1;               // 128-byte lines of an h row per step
-    const int steps = (a.F + KS - 1) / KS, mine = (steps - wave + kDownWaves - 1) / kDownWaves;
-    if (mine <= 0) return;
+    const int lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+    const int c = lane & 15, g = lane >> 4;
     const int kp = KP * (g + 4 * (c >> 3));      // the lane's piece of a weight row (swap_halves)
     // ... and of an h line (pair_tokens), 8 elements: bf16 pieces g and 4 + g, as the weights; e4m3, whose 16-byte piece
     // is two pieces of h, 2 g and 2 g + 1
     const int kh = 8 * (Q8 ? 2 * g + (c >> 3) : g + 4 * (c >> 3));
-    uint32_t wo[2];
+    const int steps = (a.F + KS - 1) / KS, s1 = steps * (wave + 1) / kDownWaves;
+    const uint32_t wbytes = 16 * R * (uint32_t)a.F * kBytes;
+    const __amdgpu_buffer_rsrc_t w = buffer_of((const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * kBytes, wbytes);
+    const __amdgpu_buffer_rsrc_t h = buffer_of(a.h + (size_t)row0 * a.F, (uint32_t)cnt * 2 * a.F);
+    const __amdgpu_buffer_rsrc_t sw =
+        buffer_of(a.s_dn + (Q8 ? ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * steps : 0), Q8 ? steps * 4 : 0);
+    uint32_t wo[R][2], ho[N8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) wo[i] = (uint32_t)((8 * i + (c & 7)) * a.F + kp) * kBytes;
-    struct Slot {
-        u32x4_t w[2], h[HL][N8];
-        float fw;
-    };
-    // the loading end: hit expert lh, rows lr .. of it, step ls
-    int lh = h0, lr = 0, ls = wave, lcnt = 0;
-    __amdgpu_buffer_rsrc_t lw, lhp, lsw;
-    uint32_t lo[N8];
-    int total = 0;
-    auto expert_at = [&](int hi, int &e, int &row0, int &cnt) {
-        e = __builtin_amdgcn_readfirstlane(s.hit[hi]);
-        row0 = __builtin_amdgcn_readfirstlane(s.start[e]);
-        cnt = __builtin_amdgcn_readfirstlane(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1]));
-    };
-    auto load_setup = [&]() {
-        int e, row0;
-        expert_at(lh, e, row0, lcnt);
-        lw = buffer_of((const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * kBytes, 16 * (uint32_t)a.F * kBytes);
-        lhp = buffer_of(a.h + (size_t)row0 * a.F, (uint32_t)lcnt * 2 * a.F);
-        if (Q8) lsw = buffer_of(a.s_dn + ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * steps, steps * 4);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int n = 0; n < N8; ++n)
-            lo[n] = (uint32_t)(min(lr + 8 * n + (c & 7), lcnt - 1) * a.F + kh) * 2;
-    };
-    // the using end
-    int uh = h0, ur = 0, us = 0;
-    f32x4_t acc[NT];
+        for (int i = 0; i < 2; ++i) wo[r][i] = (uint32_t)((16 * r + 8 * i + (c & 7)) * a.F + kp) * kBytes;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int hi = h0; hi < h1; ++hi) {
-        int e, row0, cnt;
-        expert_at(hi, e, row0, cnt);
-        total += (cnt + 8 * N8 - 1) / (8 * N8);
-    }
-    total *= mine;
-    load_setup();
-    stream<ring_depth(8 + 4 * HL * N8), Slot>(
-        total,
-        [&](Slot &q) {
-            const uint32_t kw = (uint32_t)ls * 128;
-            const int left = a.F - ls * KS;
+    for (int n = 0; n < N8; ++n) ho[n] = (uint32_t)(min(8 * n + (c & 7), cnt - 1) * a.F + kh) * 2;
+    f32x4_t acc[R][NT];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) q.w[i] = load_w(lw, !TAIL || kp < left ? wo[i] : kPastResource, kw);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    int s = steps * wave / kDownWaves;
+    auto run = [&](auto uc) {
+        constexpr int U = decltype(uc)::value;
+        u32x4_t wv[U][R][2], hv[U][HL][N8];
+        float fw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    wv[u][r][i] =
+                        load_w(w, !TAIL || kp + (s + u) * KS < a.F ? wo[r][i] + 128 * u : kPastResource, s * 128);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int l = 0; l < HL; ++l)
 #pragma unroll
                 for (int n = 0; n < N8; ++n)
-                    q.h[l][n] = load_x(lhp, !TAIL || kh + 64 * l < left ? lo[n] + 128 * l : kPastResource, kw * HL);
-            if (Q8) q.fw = load_f32(lsw, 0, ls * 4);
-            if ((ls += kDownWaves) >= steps) {
-                ls = wave;
-                lr += 8 * N8;
-                if (lr >= lcnt) {
-                    lr = 0;
-                    ++lh;
-                }
-                if (lh < h1) load_setup();
-            }
-        },
-        [&](Slot &q) {
-            swap_halves(q.w[0], q.w[1]);
+                    hv[u][l][n] = load_x(h, !TAIL || kh + 64 * l + (s + u) * KS < a.F ? ho[n] + 128 * (HL * u + l)
+                                                                                     : kPastResource,
+                                         s * 128 * HL);
+        if constexpr (Q8) load_floats<U>(sw, 0, s * 4, fw);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             u32x4_t x[HL][2][NT];
 #pragma unroll
-            for (int l = 0; l < HL; ++l) pair_tokens<N8>(q.h[l], x[l][0], x[l][1]);
-            if constexpr (Q8) {
-                u32x4_t b[4];
+            for (int l = 0; l < HL; ++l) pair_tokens<N8>(hv[u][l], x[l][0], x[l][1]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    b[2 * i] = fp8_to_bf16(q.w[i].x, q.w[i].y);
-                    b[2 * i + 1] = fp8_to_bf16(q.w[i].z, q.w[i].w);
-                }
+            for (int r = 0; r < R; ++r) {
+                swap_halves(wv[u][r][0], wv[u][r][1]);
+                if constexpr (Q8) {
+                    u32x4_t b[4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) p = mfma_bf16(b[i], x[HL - 1 & i / 2][i & 1][n], p);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[n][v] = __builtin_fmaf(p[v], q.fw, acc[n][v]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[n] = mfma_bf16(q.w[i], x[0][i][n], acc[n]);
-            }
-            if (++us == mine) {
-                us = 0;
-                int e, row0, cnt;
-                expert_at(uh, e, row0, cnt);
-                // tokens of an expert are distinct, so no two lanes add to one word
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int row = ur + 16 * n + c;
-                    if (row < cnt) {
-                        f32x4_t *p = (f32x4_t *)(sum + (int)s.tok[row0 + row] * 16 + 4 * g);
-                        f32x4_t v = *p;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] += acc[n][j];
-                        *p = v;
+                    for (int i = 0; i < 2; ++i) {
+                        b[2 * i] = fp8_to_bf16(wv[u][r][i].x, wv[u][r][i].y);
+                        b[2 * i + 1] = fp8_to_bf16(wv[u][r][i].z, wv[u][r][i].w);
                     }
-                    acc[n] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-                }
-                ur += 8 * N8;
-                if (ur >= cnt) {
-                    ur = 0;
-                    ++uh;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p = mfma_bf16(b[i], x[i / 2][i & 1][n], p);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) acc[r][n][v] = __builtin_fmaf(p[v], fw[u], acc[r][n][v]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) acc[r][n] = mfma_bf16(wv[u][r][i], x[0][i][n], acc[r][n]);
                 }
             }
-        });
+        }
+        s += U;
+    };
+    constexpr int U = R == 1 ? 4 : N8 == 8 ? 1 : 2;
+    while (s + U <= s1) run(IntC<U>());
+    while (s < s1) run(IntC<1>());
+    // the waves' parts meet in LDS as in up_task; two neighbouring columns a thread
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float *rb = red + par * kDownWaves * R * 256;
+        par ^= 1;
+#pragma unroll
+        for (int r = 0; r < R; ++r) *(f32x4_t *)(rb + (wave * R + r) * 256 + c * 16 + 4 * g) = acc[r][n];
+        __syncthreads();
+        const int ni = 2 * ((int)threadIdx.x % (8 * R)), ci = (int)threadIdx.x / (8 * R);
+        const int row = 16 * n + ci;
+        if (ci < 16 && row < cnt) {
+            float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < kDownWaves; ++j) {
+                const float2 p = *(const float2 *)(rb + (j * R + (ni >> 4)) * 256 + ci * 16 + (ni & 15));
+                v.x += p.x;
+                v.y += p.y;
+            }
+            *(float2 *)(a.y + (size_t)(row0 + row) * a.d + n0 + ni) = v;
+        }
+    }
 }
 
 template <bool Q8, bool TAIL>
-__global__ __launch_bounds__(64 * kDownWaves, 4) void k_layer_down(LayerArgs a)
+__global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
 {
-    extern __shared__ __attribute__((aligned(16))) char lds[];
-    float *sums = (float *)lds;   // [kDownWaves][T][16]
-    const RowsLds s = rows_lds(lds + (size_t)kDownWaves * a.T * 64, a, false);
-    const int T = valid_tokens(a);
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    for (int i = threadIdx.x; i < T * a.k; i += blockDim.x) s.ids[i] = a.ids[i];
-    __syncthreads();
-    build_rows(s, a, T);
-    const int hits = s.n[0];
-    float *sum = sums + (size_t)wave * a.T * 16;
-    for (int q = blockIdx.x; q < a.d / 16; q += gridDim.x) {
-        const int n0 = 16 * q;
-        for (int i = lane; i < T * 4; i += kWave) ((f32x4_t *)sum)[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        // runs of experts that take the same number of token groups, in expert order
-        for (int h0 = 0; h0 < hits;) {
-            auto groups = [&](int hi) {
-                const int e = s.hit[hi];
-                return __builtin_amdgcn_readfirstlane(groups_of(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1])));
-            };
-            const int n8 = groups(h0);
-            int h1 = h0 + 1;
-            while (h1 < hits && groups(h1) == n8) ++h1;
-            if (n8 == 1) down_run<Q8, 1, TAIL>(a, s, h0, h1, n0, sum);
-            else if (n8 == 2) down_run<Q8, 2, TAIL>(a, s, h0, h1, n0, sum);
-            else if (n8 == 4) down_run<Q8, 4, TAIL>(a, s, h0, h1, n0, sum);
-            else down_run<Q8, 8, TAIL>(a, s, h0, h1, n0, sum);
-            h0 = h1;
+    __shared__ __attribute__((aligned(16))) char lds[kDownRedBytes];
+    float *red = (float *)lds;
+    const int hits = a.plan.n[0];
+    const bool small = a.T <= 16 && (long)hits * (a.d / 32) < a.few_tasks;   // as in k_layer_up
+    const int nc = a.d / (small ? 16 : 32);
+    int par = 0;
+    for (int q = blockIdx.x; q < hits * nc; q += gridDim.x) {
+        const int hi = q / nc, n0 = (q - hi * nc) * (small ? 16 : 32);
+        const LayerRec rec = a.plan.rec[hi];
+        const int e = __builtin_amdgcn_readfirstlane(rec.e);
+        const int row0 = __builtin_amdgcn_readfirstlane(rec.row0);
+        const int cnt = __builtin_amdgcn_readfirstlane(rec.cnt);
+        if (small) {
+            if (cnt <= 8) down_task<Q8, 1, 1, TAIL>(a, e, n0, row0, cnt, red, par);
+            else down_task<Q8, 1, 2, TAIL>(a, e, n0, row0, cnt, red, par);
+            continue;
         }
-        __syncthreads();
-        // two neighbouring columns per thread, waves in order
-        for (int i = threadIdx.x; i < T * 8; i += blockDim.x) {
-            const int t = i >> 3, n = 2 * (i & 7);
-            float v0 = 0.0f, v1 = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kDownWaves; ++w) {
-                const float *p = sums + ((size_t)w * a.T + t) * 16 + n;
-                v0 += p[0];
-                v1 += p[1];
-            }
-            *(uint32_t *)(a.out + (size_t)t * a.d + n0 + n) =
-                (uint32_t)f32_to_bf16(v0) | (uint32_t)f32_to_bf16(v1) << 16;
+        // up to 64 rows at once; an expert of more rows reads its weights again for the rest
+        for (int r = 0; r < cnt; r += 64) {
+            const int m = min(cnt - r, 64);
+            if (m <= 8) down_task<Q8, 2, 1, TAIL>(a, e, n0, row0 + r, m, red, par);
+            else if (m <= 16) down_task<Q8, 2, 2, TAIL>(a, e, n0, row0 + r, m, red, par);
+            else if (m <= 32) down_task<Q8, 2, 4, TAIL>(a, e, n0, row0 + r, m, red, par);
+            else down_task<Q8, 2, 8, TAIL>(a, e, n0, row0 + r, m, red, par);
         }
-        __syncthreads();
     }
+}
+
+// The smallest of the lanes' row numbers, -1 (none) counting as the largest.
+__device__ __forceinline__ uint32_t wave_min_row(int v) { return ~wave_max_u32(~(uint32_t)v); }
+
+// out[t] = sum of the token's rows of y in expert order.  A workgroup takes 1024 columns of a token.
+__global__ __launch_bounds__(256) void k_layer_sum(LayerArgs a)
+{
+    const int nc = (a.d + 1023) / 1024;
+    const int t = (int)blockIdx.x / nc, col = ((int)blockIdx.x - t * nc) * 1024 + 4 * (int)threadIdx.x;
+    if (t >= a.plan.n[1]) return;
+    const bool in = col < a.d;   // every lane stays for the reductions
+    const int lane = threadIdx.x % kWave;
+    // lane j of every wave holds the token's j-th row; rows of higher experts have higher numbers, so the ascending order
+    // is the experts'
+    int mine = lane < a.k ? a.plan.row_of[t * a.k + lane] : -1;
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (;;) {
+        const uint32_t key = wave_min_row(mine);
+        if (key == 0xFFFFFFFFu) break;
+        if ((uint32_t)mine == key) mine = -1;
+        if (in) v += *(const f32x4_t *)(a.y + (size_t)key * a.d + col);
+    }
+    if (!in) return;
+    typedef uint32_t u32x2_v __attribute__((ext_vector_type(2)));
+    *(u32x2_v *)(a.out + (size_t)t * a.d + col) =
+        u32x2_v{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
 }
 
 // ---------------------------------------------------------------- router of up to kLayerSelfT tokens
@@ -800,16 +768,9 @@ int device_cus()
 template <bool Q8>
 hipError_t launch_up(const LayerArgs &a, bool self, int grid, hipStream_t s)
 {
-    const size_t lds = kUpRedBytes + rows_lds_bytes(a.T, a.k, a.E_local, true);
+    const size_t lds = kUpRedBytes + rows_lds_bytes(a.T, a.k, a.E_local);
     if (self) hipLaunchKernelGGL((k_layer_up<Q8, true>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
     else hipLaunchKernelGGL((k_layer_up<Q8, false>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
-    return hipGetLastError();
-}
-
-template <bool Q8, bool TAIL>
-hipError_t launch_down(const LayerArgs &a, int grid, size_t lds, hipStream_t s)
-{
-    hipLaunchKernelGGL((k_layer_down<Q8, TAIL>), dim3(grid), dim3(64 * kDownWaves), lds, s, a);
     return hipGetLastError();
 }
 
@@ -828,17 +789,21 @@ hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s)
     if (cus <= 0) return hipErrorInvalidDevice;
     LayerArgs b = a;
     b.few_tasks = 2 * cus;
-    const long most = (long)std::min(a.E_local, a.T * a.k) * ((a.F + 7) / 8);   // tasks, if every choice is another local expert
-    const int grid = (int)std::min<long>(most, 4L * cus);
+    const long most = (long)layer_hits_cap(a.T, a.k, a.E_local) * ((a.F + 7) / 8);   // tasks, if every choice is another local expert
+    const int grid = (int)std::min<long>(most, 2L * cus);
     const hipError_t e = q8 ? launch_up<true>(b, self, grid, s) : launch_up<false>(b, self, grid, s);
     if (e != hipSuccess) return e;
-    if (self) b.ids = a.ids_ws;
-    const size_t lds = (size_t)kDownWaves * a.T * 64 + rows_lds_bytes(a.T, a.k, a.E_local, false);
-    const int gd = std::min(a.d / 16, 4 * cus);
     const bool tail = a.F % (q8 ? kQ8Group : 64) != 0;
-    if (q8 && tail) return launch_down<true, true>(b, gd, lds, s);
-    if (q8) return launch_down<true, false>(b, gd, lds, s);
-    return tail ? launch_down<false, true>(b, gd, lds, s) : launch_down<false, false>(b, gd, lds, s);
+    const int gd = (int)std::min<long>((long)layer_hits_cap(a.T, a.k, a.E_local) * (a.d / 16), 2L * cus);
+    const dim3 block(64 * kDownWaves);
+    if (q8 && tail) hipLaunchKernelGGL((k_layer_down<true, true>), dim3(gd), block, 0, s, b);
+    else if (q8) hipLaunchKernelGGL((k_layer_down<true, false>), dim3(gd), block, 0, s, b);
+    else if (tail) hipLaunchKernelGGL((k_layer_down<false, true>), dim3(gd), block, 0, s, b);
+    else hipLaunchKernelGGL((k_layer_down<false, false>), dim3(gd), block, 0, s, b);
+    const hipError_t e2 = hipGetLastError();
+    if (e2 != hipSuccess) return e2;
+    hipLaunchKernelGGL(k_layer_sum, dim3(a.T * ((a.d + 1023) / 1024)), dim3(256), 0, s, b);
+    return hipGetLastError();
 }
 
 }  // namespace mk

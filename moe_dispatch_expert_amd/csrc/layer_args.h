@@ -13,6 +13,17 @@ constexpr int kLayerSelfT = 8;       // tokens up to which the vector router run
 constexpr int kLayerSelfE = 256;     // ... and experts, for the selection
 constexpr int kQ8Group = 128;        // columns (and rows of weights) per scale
 
+// What the up kernel's first workgroup writes for the later ones: the experts with tokens in ascending order (per expert
+// the tokens ascend, row by row), and the row of every choice.
+struct LayerRec {
+    int32_t e, row0, cnt, pad;       // local expert, its first row, its rows
+};
+struct LayerPlan {
+    int32_t *n;                      // [2] experts with tokens, valid tokens
+    LayerRec *rec;                   // [min(E_local, T k)]
+    int32_t *row_of;                 // [T, k] row of the choice in h and y, or -1
+};
+
 struct LayerArgs {
     const uint16_t *x;               // [T, d] bf16: router input, and the experts' in the bf16 form
     const uint8_t *xq;               // [T, d] e4m3 (8-bit form)
@@ -21,17 +32,21 @@ struct LayerArgs {
     const float *s_gu, *s_dn;        // [E_local, 2 ceil(F / 128), d / 128], [E_local, d / 128, ceil(F / 128)]
     const int32_t *ids;              // [T, k] given or selected ids (what the up kernel reads unless it selects)
     const float *gates;              // [T, k]
-    int32_t *ids_ws;                 // [T, k] ids the down kernel reads, written by the up kernel when it selects
+    LayerPlan plan;
     int32_t *ids_user;               // NULL or [T, k]: copies for the caller
     float *w_user;
     float *part;                     // [8, T, E] router partial sums
     const float *wr, *bias;          // router
     uint16_t *h;                     // [T min(k, E_local), F] bf16: gate * silu(g) * u, rows in expert order
+    float *y;                        // [T min(k, E_local), d]: the rows' products with W_down
     uint16_t *out;                   // [T, d] bf16
     const int32_t *t_valid;          // NULL or the number of tokens to compute (device)
     int32_t T, d, E, k, e_begin, E_local, F;
     int32_t few_tasks;               // fewer gate|up tasks than this: smaller ones (set by the launcher)
     int32_t given;                   // ids came from the caller: they may repeat
 };
+
+__host__ __device__ inline int layer_rows_cap(int T, int k, int E_local) { return T * (k < E_local ? k : E_local); }
+__host__ __device__ inline int layer_hits_cap(int T, int k, int E_local) { return E_local < T * k ? E_local : T * k; }
 
 }  // namespace mk
