@@ -270,11 +270,23 @@ struct IntC {
     static constexpr int value = N;
 };
 
+// Weight tiles per task.  More of them share one load of the tokens' rows, whose traffic out of the L2 costs as much as
+// that of the weights out of memory once an expert has 16 rows or more; fewer make more tasks.  n1: tasks per expert at
+// one tile.  Four tiles where the workgroups get at least four tasks each or come out nearly even; one tile (8 tokens'
+// rows beside 16 weight rows) only where two would not give every workgroup one.
+__device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workgroups)
+{
+    const long t2 = (long)hits * ((n1 + 1) / 2), t4 = (long)hits * ((n1 + 3) / 4);
+    const long rounds = (t4 + workgroups - 1) / workgroups;
+    if (t4 >= 4L * workgroups || 10 * t4 >= 9 * rounds * workgroups) return t4 > 0 ? 4 : 2;
+    return t2 < workgroups && T <= 16 ? 1 : 2;
+}
+
 constexpr int kUpWaves = 4;
-constexpr int kUpRedBytes = 2 * kUpWaves * 2 * 256 * 4;   // two halves of up_task's exchange
+constexpr int kUpRedBytes = 2 * kUpWaves * 4 * 256 * 4;   // two halves of up_task's exchange
 
 // One gate|up task: features f0 .. f0 + 8 R - 1 of local expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8).
-// R = 1: one weight tile of 8 gate and 8 up rows; R = 2: a tile of 16 gate rows and one of 16 up rows.
+// R = 1: one weight tile of 8 gate and 8 up rows; R = 2 or 4: R / 2 tiles of 16 gate rows, then as many of up rows.
 // The wave sums its share of K in steps of 128 bytes of a weight row (64 bf16, or one 128-wide block of e4m3, whose
 // product is scaled by the token's and the weights' scales before it joins the sum).
 // red: 2 x kUpWaves x R x 256 floats; par: which half the next exchange uses.
@@ -293,15 +305,17 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
     const __amdgpu_buffer_rsrc_t x = buffer_of(Q8 ? (const void *)a.xq : (const void *)a.x, (uint32_t)a.T * pitch);
     // the lane's weight rows in each tile (features past F repeat the last; never stored)
     uint32_t wo[R][2], xo[N8], so[NT];
-    if (R == 1) {
+    if constexpr (R == 1) {
         wo[0][0] = f0 + (c & 7);
         wo[0][1] = a.F + wo[0][0];
     } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            wo[0][i] = min(f0 + 8 * i + (c & 7), a.F - 1);
-            wo[R - 1][i] = a.F + wo[0][i];
-        }
+        for (int r = 0; r < R / 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                wo[r][i] = min(f0 + 16 * r + 8 * i + (c & 7), a.F - 1);
+                wo[R / 2 + r][i] = a.F + wo[r][i];
+            }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -330,8 +344,8 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
     }
     const __amdgpu_buffer_rsrc_t sx = buffer_of(a.xs, (uint32_t)a.T * steps * 4);
     int k = s0;
-    // U steps: all their loads, then all their products.  (Four workgroups a CU cover each other's waits; a ring of
-    // single steps per wave measured no faster.)
+    // U steps: all their loads, then all their products; the CU's other waves load meanwhile (a ring of single steps per
+    // wave measured no faster)
     auto run = [&](auto uc) {
         constexpr int U = decltype(uc)::value;
         u32x4_t wv[U][R][2], xv[U][N8];
@@ -365,7 +379,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
                 const float wg = __int_as_float(__builtin_amdgcn_readlane(fg, k - s0 + u));
                 const float wu = __int_as_float(__builtin_amdgcn_readlane(fu, k - s0 + u));
                 // accumulator rows 4 g .. 4 g + 3: in the mixed tile groups 0, 1 are gate rows and 2, 3 up rows
-                const float fw[2] = {R == 1 ? (g < 2 ? wg : wu) : wg, wu};
+                const float mixed = g < 2 ? wg : wu;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -373,7 +387,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
                         f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
                         p = mfma_fp8_64(wv[u][r][0], x0[n], p);
                         p = mfma_fp8_64(wv[u][r][1], x1[n], p);
-                        const float f = fw[r] * fx[u][n];
+                        const float f = (R == 1 ? mixed : r < R / 2 ? wg : wu) * fx[u][n];
 #pragma unroll
                         for (int v = 0; v < 4; ++v) acc[r][n][v] = __builtin_fmaf(p[v], f, acc[r][n][v]);
                     }
@@ -388,7 +402,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
         }
         k += U;
     };
-    constexpr int U = R == 1 ? 4 : N8 == 8 ? 1 : 2;
+    constexpr int U = R == 1 ? 4 : R == 4 && N8 == 8 ? 1 : 2;
     while (k + U <= s1) run(IntC<U>());
     while (k < s1) run(IntC<1>());
     // The waves' parts of a token tile meet in LDS ([column][row], so a lane's four rows are one 16-byte word), are
@@ -406,8 +420,8 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
             float2 gs = make_float2(0.0f, 0.0f), us = gs;
 #pragma unroll
             for (int v = 0; v < kUpWaves; ++v) {
-                const float *q = rb + v * R * 256 + ci * 16 + fi;
-                const float2 gv = *(const float2 *)q, uv = *(const float2 *)(q + (R == 1 ? 8 : 256));
+                const float *q = rb + (v * R + (fi >> 4)) * 256 + ci * 16 + (fi & 15);
+                const float2 gv = *(const float2 *)q, uv = *(const float2 *)(q + (R == 1 ? 8 : R / 2 * 256));
                 gs.x += gv.x;
                 gs.y += gv.y;
                 us.x += uv.x;
@@ -467,11 +481,9 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
             if (a.w_user) a.w_user[i] = s.w[i];
         }
     build_rows(s, a, T, blockIdx.x == 0);
-    // Tasks of 16 features, two weight tiles beside one load of the tokens.  Where they are too few to give every CU a
-    // couple (a token or two at a few experts), of 8.
     const int hits = s.n[0];
-    const bool small = a.T <= 16 && (long)hits * ((a.F + 15) / 16) < a.few_tasks;
-    const int fs = small ? 8 : 16;
+    const int tiles = tiles_per_task(hits, (a.F + 7) / 8, a.T, (int)gridDim.x);
+    const int fs = 8 * tiles;
     const int nf = (a.F + fs - 1) / fs;
     int par = 0;
     for (int q = blockIdx.x; q < hits * nf; q += gridDim.x) {
@@ -479,18 +491,23 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
         const int e = __builtin_amdgcn_readfirstlane(s.hit[hi]);
         const int row0 = __builtin_amdgcn_readfirstlane(s.start[e]);
         const int cnt = __builtin_amdgcn_readfirstlane(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1]));
-        if (small) {
+        if (tiles == 1) {
             if (cnt <= 8) up_task<Q8, 1, 1>(a, s, e, f0, row0, cnt, red, par);
             else up_task<Q8, 1, 2>(a, s, e, f0, row0, cnt, red, par);
             continue;
         }
-        // up to 64 rows at once; an expert of more than 64 rows reads its weights again for the rest
+        // up to 64 rows at once; an expert of more rows reads its weights again for the rest
         for (int r = 0; r < cnt; r += 64) {
             const int m = min(cnt - r, 64);
-            if (m <= 8) up_task<Q8, 2, 1>(a, s, e, f0, row0 + r, m, red, par);
-            else if (m <= 16) up_task<Q8, 2, 2>(a, s, e, f0, row0 + r, m, red, par);
-            else if (m <= 32) up_task<Q8, 2, 4>(a, s, e, f0, row0 + r, m, red, par);
-            else up_task<Q8, 2, 8>(a, s, e, f0, row0 + r, m, red, par);
+            auto rows = [&](auto tc) {
+                constexpr int R = decltype(tc)::value;
+                if (m <= 8) up_task<Q8, R, 1>(a, s, e, f0, row0 + r, m, red, par);
+                else if (m <= 16) up_task<Q8, R, 2>(a, s, e, f0, row0 + r, m, red, par);
+                else if (m <= 32) up_task<Q8, R, 4>(a, s, e, f0, row0 + r, m, red, par);
+                else up_task<Q8, R, 8>(a, s, e, f0, row0 + r, m, red, par);
+            };
+            if (tiles == 4) rows(IntC<4>());
+            else rows(IntC<2>());
         }
     }
 }
@@ -498,7 +515,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
 // ---------------------------------------------------------------- down
 
 constexpr int kDownWaves = 4;
-constexpr int kDownRedBytes = 2 * kDownWaves * 2 * 256 * 4;
+constexpr int kDownRedBytes = 2 * kDownWaves * 4 * 256 * 4;
 
 // One down task: output columns n0 .. n0 + 16 R - 1 of expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8), written
 // to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3,
@@ -604,13 +621,13 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
 #pragma unroll
         for (int r = 0; r < R; ++r) *(f32x4_t *)(rb + (wave * R + r) * 256 + c * 16 + 4 * g) = acc[r][n];
         __syncthreads();
-        const int ni = 2 * ((int)threadIdx.x % (8 * R)), ci = (int)threadIdx.x / (8 * R);
-        const int row = 16 * n + ci;
-        if (ci < 16 && row < cnt) {
+        for (int j = threadIdx.x; j < 8 * R * 16; j += 64 * kDownWaves) {
+            const int ni = 2 * (j % (8 * R)), row = 16 * n + j / (8 * R);
+            if (row >= cnt) break;
             float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < kDownWaves; ++j) {
-                const float2 p = *(const float2 *)(rb + (j * R + (ni >> 4)) * 256 + ci * 16 + (ni & 15));
+            for (int v2 = 0; v2 < kDownWaves; ++v2) {
+                const float2 p = *(const float2 *)(rb + (v2 * R + (ni >> 4)) * 256 + (row & 15) * 16 + (ni & 15));
                 v.x += p.x;
                 v.y += p.y;
             }
@@ -625,16 +642,16 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
     __shared__ __attribute__((aligned(16))) char lds[kDownRedBytes];
     float *red = (float *)lds;
     const int hits = a.plan.n[0];
-    const bool small = a.T <= 16 && (long)hits * (a.d / 32) < a.few_tasks;   // as in k_layer_up
-    const int nc = a.d / (small ? 16 : 32);
+    const int tiles = tiles_per_task(hits, a.d / 16, a.T, (int)gridDim.x);
+    const int nc = a.d / (16 * tiles);   // d % 128 == 0
     int par = 0;
     for (int q = blockIdx.x; q < hits * nc; q += gridDim.x) {
-        const int hi = q / nc, n0 = (q - hi * nc) * (small ? 16 : 32);
+        const int hi = q / nc, n0 = (q - hi * nc) * 16 * tiles;
         const LayerRec rec = a.plan.rec[hi];
         const int e = __builtin_amdgcn_readfirstlane(rec.e);
         const int row0 = __builtin_amdgcn_readfirstlane(rec.row0);
         const int cnt = __builtin_amdgcn_readfirstlane(rec.cnt);
-        if (small) {
+        if (tiles == 1) {
             if (cnt <= 8) down_task<Q8, 1, 1, TAIL>(a, e, n0, row0, cnt, red, par);
             else down_task<Q8, 1, 2, TAIL>(a, e, n0, row0, cnt, red, par);
             continue;
@@ -642,10 +659,15 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
         // up to 64 rows at once; an expert of more rows reads its weights again for the rest
         for (int r = 0; r < cnt; r += 64) {
             const int m = min(cnt - r, 64);
-            if (m <= 8) down_task<Q8, 2, 1, TAIL>(a, e, n0, row0 + r, m, red, par);
-            else if (m <= 16) down_task<Q8, 2, 2, TAIL>(a, e, n0, row0 + r, m, red, par);
-            else if (m <= 32) down_task<Q8, 2, 4, TAIL>(a, e, n0, row0 + r, m, red, par);
-            else down_task<Q8, 2, 8, TAIL>(a, e, n0, row0 + r, m, red, par);
+            auto rows = [&](auto tc) {
+                constexpr int R = decltype(tc)::value;
+                if (m <= 8) down_task<Q8, R, 1, TAIL>(a, e, n0, row0 + r, m, red, par);
+                else if (m <= 16) down_task<Q8, R, 2, TAIL>(a, e, n0, row0 + r, m, red, par);
+                else if (m <= 32) down_task<Q8, R, 4, TAIL>(a, e, n0, row0 + r, m, red, par);
+                else down_task<Q8, R, 8, TAIL>(a, e, n0, row0 + r, m, red, par);
+            };
+            if (tiles == 4) rows(IntC<4>());
+            else rows(IntC<2>());
         }
     }
 }
@@ -787,22 +809,20 @@ hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s)
 {
     const int cus = device_cus();
     if (cus <= 0) return hipErrorInvalidDevice;
-    LayerArgs b = a;
-    b.few_tasks = 2 * cus;
     const long most = (long)layer_hits_cap(a.T, a.k, a.E_local) * ((a.F + 7) / 8);   // tasks, if every choice is another local expert
     const int grid = (int)std::min<long>(most, 2L * cus);
-    const hipError_t e = q8 ? launch_up<true>(b, self, grid, s) : launch_up<false>(b, self, grid, s);
+    const hipError_t e = q8 ? launch_up<true>(a, self, grid, s) : launch_up<false>(a, self, grid, s);
     if (e != hipSuccess) return e;
     const bool tail = a.F % (q8 ? kQ8Group : 64) != 0;
     const int gd = (int)std::min<long>((long)layer_hits_cap(a.T, a.k, a.E_local) * (a.d / 16), 2L * cus);
     const dim3 block(64 * kDownWaves);
-    if (q8 && tail) hipLaunchKernelGGL((k_layer_down<true, true>), dim3(gd), block, 0, s, b);
-    else if (q8) hipLaunchKernelGGL((k_layer_down<true, false>), dim3(gd), block, 0, s, b);
-    else if (tail) hipLaunchKernelGGL((k_layer_down<false, true>), dim3(gd), block, 0, s, b);
-    else hipLaunchKernelGGL((k_layer_down<false, false>), dim3(gd), block, 0, s, b);
+    if (q8 && tail) hipLaunchKernelGGL((k_layer_down<true, true>), dim3(gd), block, 0, s, a);
+    else if (q8) hipLaunchKernelGGL((k_layer_down<true, false>), dim3(gd), block, 0, s, a);
+    else if (tail) hipLaunchKernelGGL((k_layer_down<false, true>), dim3(gd), block, 0, s, a);
+    else hipLaunchKernelGGL((k_layer_down<false, false>), dim3(gd), block, 0, s, a);
     const hipError_t e2 = hipGetLastError();
     if (e2 != hipSuccess) return e2;
-    hipLaunchKernelGGL(k_layer_sum, dim3(a.T * ((a.d + 1023) / 1024)), dim3(256), 0, s, b);
+    hipLaunchKernelGGL(k_layer_sum, dim3(a.T * ((a.d + 1023) / 1024)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

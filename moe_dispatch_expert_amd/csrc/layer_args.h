@@ -42,7 +42,6 @@ struct LayerArgs {
     uint16_t *out;                   // [T, d] bf16
     const int32_t *t_valid;          // NULL or the number of tokens to compute (device)
     int32_t T, d, E, k, e_begin, E_local, F;
-    int32_t few_tasks;               // fewer gate|up tasks than this: smaller ones (set by the launcher)
     int32_t given;                   // ids came from the caller: they may repeat
 };
 
