@@ -146,6 +146,8 @@ __device__ __forceinline__ void build_rows(const RowsLds &s, const LayerArgs &a,
         }
         if (publish) a.plan.row_of[i] = r;
     }
+    if (publish)   // tokens past the valid ones have no rows
+        for (int i = T * a.k + (int)threadIdx.x; i < a.T * a.k; i += blockDim.x) a.plan.row_of[i] = -1;
     __syncthreads();
 }
 
@@ -680,20 +682,28 @@ __global__ __launch_bounds__(256) void k_layer_sum(LayerArgs a)
 {
     const int nc = (a.d + 1023) / 1024;
     const int t = (int)blockIdx.x / nc, col = ((int)blockIdx.x - t * nc) * 1024 + 4 * (int)threadIdx.x;
-    if (t >= a.plan.n[1]) return;
     const bool in = col < a.d;   // every lane stays for the reductions
     const int lane = threadIdx.x % kWave;
     // lane j of every wave holds the token's j-th row; rows of higher experts have higher numbers, so the ascending order
     // is the experts'
     int mine = lane < a.k ? a.plan.row_of[t * a.k + lane] : -1;
     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (;;) {
-        const uint32_t key = wave_min_row(mine);
-        if (key == 0xFFFFFFFFu) break;
-        if ((uint32_t)mine == key) mine = -1;
-        if (in) v += *(const f32x4_t *)(a.y + (size_t)key * a.d + col);
+    for (bool more = true; more;) {   // four rows on their way at a time
+        f32x4_t p[4];
+        bool have[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t row = wave_min_row(mine);
+            have[u] = row != 0xFFFFFFFFu;
+            if ((uint32_t)mine == row) mine = -1;
+            p[u] = have[u] && in ? *(const f32x4_t *)(a.y + (size_t)row * a.d + col) : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (have[u]) v += p[u];
+        more = have[3];
     }
-    if (!in) return;
+    if (!in || t >= a.plan.n[1]) return;   // valid tokens
     typedef uint32_t u32x2_v __attribute__((ext_vector_type(2)));
     *(u32x2_v *)(a.out + (size_t)t * a.d + col) =
         u32x2_v{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
@@ -703,69 +713,92 @@ __global__ __launch_bounds__(256) void k_layer_sum(LayerArgs a)
 // ---------------------------------------------------------------- router of up to kLayerSelfT tokens
 
 // Partial sums part[s][t][e] in the library's order (one ascending fma chain per K segment), on the vector units: with
-// a few tokens the chains are few, and the time goes into fetching W_r.  A workgroup takes (segment s, 32 experts): all
-// its weights are fetched at once into LDS (a segment of d = 7168 is 112 KiB), then lane l of wave w runs the chain of
-// token 2 w + l / 32, expert l % 32.
+// a few tokens the chains are few, and the time goes into fetching W_r and into the length of a chain.  A workgroup takes
+// (segment s, up to 16 experts): its weights are fetched at once into LDS (a segment of d = 7168: 56 KiB), then every
+// lane runs one chain (16 experts x 4 tokens a wave, 8 x 8 where there are no more than 8 experts), its operands read 8
+// steps ahead.
 constexpr int kVrThreads = 512;
-constexpr int kVrExp = 32;
-constexpr int kVrRows = 896;   // weight rows per staged chunk
+constexpr int kVrRows = 1024;   // weight rows per staged chunk
 
+// LE: log2 of the experts per workgroup and of the lanes per token (3 or 4).
+template <int LE>
 __global__ __launch_bounds__(kVrThreads) void k_layer_router(LayerArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
+    constexpr int S = 1 << LE;
     const int seg = a.d / kRouterSegments;
-    const int rows_lds_n = min(seg, kVrRows);
-    float *ws = (float *)lds;                       // [rows][32]
-    float *xs = ws + (size_t)rows_lds_n * kVrExp;   // [T][rows]
-    const int s = (int)blockIdx.x % kRouterSegments, e0 = (int)blockIdx.x / kRouterSegments * kVrExp;
+    const int cap = min(seg, kVrRows);
+    const int s = (int)blockIdx.x % kRouterSegments, e0 = (int)blockIdx.x / kRouterSegments * S;
+    const int ne = min(S, a.E - e0);
+    float *ws = (float *)lds;                     // [cap][S]
+    float *xs = ws + (size_t)cap * S;             // [T][cap]
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int t = 2 * wave + lane / 32, el = lane % 32;
-    const bool mine = t < a.T && e0 + el < a.E;
+    const int t = (wave << (6 - LE)) + (lane >> LE), el = lane & (S - 1);
+    const bool mine = t < a.T && el < ne;
     float acc = 0.0f;
-    const bool full = a.E % 4 == 0 && e0 + kVrExp <= a.E;
     for (int r0 = 0; r0 < seg; r0 += kVrRows) {
         const int rows = min(kVrRows, seg - r0);   // a multiple of 16
         const float *w = a.wr + ((size_t)s * seg + r0) * a.E + e0;
-        if (full) {
-            for (int i = threadIdx.x; i < rows * 8; i += 8 * kVrThreads) {
-                f32x4_t v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int j = min(i + u * kVrThreads, rows * 8 - 1);
-                    v[u] = *(const f32x4_t *)(w + (size_t)(j >> 3) * a.E + 4 * (j & 7));
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (i + u * kVrThreads < rows * 8) *(f32x4_t *)(ws + 4 * (i + u * kVrThreads)) = v[u];
-            }
-        } else {
-            const int ne = min(kVrExp, a.E - e0);
-            for (int i = threadIdx.x; i < rows * kVrExp; i += 8 * kVrThreads) {
-                float v[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int j = min(i + u * kVrThreads, rows * kVrExp - 1);
-                    v[u] = w[(size_t)(j >> 5) * a.E + min(j & 31, ne - 1)];
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (i + u * kVrThreads < rows * kVrExp) ws[i + u * kVrThreads] = v[u];
-            }
-        }
         for (int i = threadIdx.x; i < a.T * rows / 8; i += kVrThreads) {
             const int tt = i / (rows / 8), c = i % (rows / 8);
             float f[8];
             unpack8(*(const u32x4_t *)(a.x + (size_t)tt * a.d + (size_t)s * seg + r0 + 8 * c), f);
-            f32x4_t *p = (f32x4_t *)(xs + (size_t)tt * rows_lds_n + 8 * c);
+            f32x4_t *p = (f32x4_t *)(xs + (size_t)tt * cap + 8 * c);
             p[0] = f32x4_t{f[0], f[1], f[2], f[3]};
             p[1] = f32x4_t{f[4], f[5], f[6], f[7]};
         }
+        if (ne == S && a.E % 4 == 0) {   // 16-byte pieces
+            constexpr int P = S / 4;
+            for (int i = threadIdx.x; i < rows * P; i += 8 * kVrThreads) {
+                f32x4_t v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int j = min(i + u * kVrThreads, rows * P - 1);
+                    v[u] = *(const f32x4_t *)(w + (size_t)(j / P) * a.E + 4 * (j % P));
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (i + u * kVrThreads < rows * P) *(f32x4_t *)(ws + 4 * (i + u * kVrThreads)) = v[u];
+            }
+        } else {   // columns past the last expert repeat it (never used)
+            for (int i = threadIdx.x; i < rows * S; i += 8 * kVrThreads) {
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int j = min(i + u * kVrThreads, rows * S - 1);
+                    v[u] = w[(size_t)(j / S) * a.E + min(j % S, ne - 1)];
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (i + u * kVrThreads < rows * S) ws[i + u * kVrThreads] = v[u];
+            }
+        }
         __syncthreads();
         if (mine) {
-            const float *xp = xs + (size_t)t * rows_lds_n, *wp = ws + el;
-            for (int i = 0; i < rows; i += 16) {
+            const float *xp = xs + (size_t)t * cap, *wp = ws + el;
+            struct Ops {
+                f32x4_t x[2];
+                float w[8];
+            };
+            auto fetch = [&](int i, Ops &o) {
+                o.x[0] = *(const f32x4_t *)(xp + i);
+                o.x[1] = *(const f32x4_t *)(xp + i + 4);
 #pragma unroll
-                for (int u = 0; u < 16; ++u) acc = __builtin_fmaf(xp[i + u], wp[(i + u) * kVrExp], acc);
+                for (int u = 0; u < 8; ++u) o.w[u] = wp[(i + u) * S];
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            auto chain = [&](const Ops &o) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) acc = __builtin_fmaf(o.x[u / 4][u % 4], o.w[u], acc);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            Ops p, q;
+            fetch(0, p);
+            for (int i = 0; i < rows; i += 16) {
+                fetch(i + 8, q);
+                chain(p);
+                fetch(min(i + 16, rows - 8), p);
+                chain(q);
             }
         }
         __syncthreads();
@@ -773,10 +806,13 @@ __global__ __launch_bounds__(kVrThreads) void k_layer_router(LayerArgs a)
     if (mine) a.part[((size_t)s * a.T + t) * a.E + e0 + el] = acc;
 }
 
-size_t vr_lds_bytes(const LayerArgs &a)
+template <int LE>
+hipError_t launch_vr(const LayerArgs &a, hipStream_t s)
 {
     const size_t rows = std::min(a.d / kRouterSegments, kVrRows);
-    return rows * kVrExp * 4 + (size_t)a.T * rows * 4;
+    const int grid = kRouterSegments * ((a.E + (1 << LE) - 1) >> LE);
+    hipLaunchKernelGGL(k_layer_router<LE>, dim3(grid), dim3(kVrThreads), rows * ((1 << LE) + a.T) * 4, s, a);
+    return hipGetLastError();
 }
 
 int device_cus()
@@ -800,9 +836,7 @@ hipError_t launch_up(const LayerArgs &a, bool self, int grid, hipStream_t s)
 
 hipError_t launch_layer_router(const LayerArgs &a, hipStream_t s)
 {
-    const int grid = kRouterSegments * ((a.E + kVrExp - 1) / kVrExp);
-    hipLaunchKernelGGL(k_layer_router, dim3(grid), dim3(kVrThreads), vr_lds_bytes(a), s, a);
-    return hipGetLastError();
+    return a.E <= 8 ? launch_vr<3>(a, s) : launch_vr<4>(a, s);
 }
 
 hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s)
