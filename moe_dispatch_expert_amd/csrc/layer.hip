@@ -39,10 +39,10 @@ namespace {
 // bit), the experts with a bit set in ascending order, and per expert its tokens
 // in ascending order.  Row r of h belongs to tok[r].
 struct RowsLds {
-    uint64_t *mask;     // [E_local][2]
-    int32_t *start;     // [E_local] first row of the expert
-    int32_t *hit;       // [<= min(E_local, T k)] experts with rows
-    int32_t *n;         // [2] number of hit experts, number of rows
+    LayerRec *rec;      // [<= min(E_local, T k)] the experts with rows
+    int32_t *n;         // [1] how many
+    uint64_t *mask;     // [E_local][2] (build_rows)
+    int32_t *start;     // [E_local] first row of the expert (build_rows)
     uint8_t *tok;       // [T min(k, E_local)]
     float *gate;        // [T min(k, E_local)]
     int32_t *ids;       // [T k]
@@ -52,7 +52,7 @@ struct RowsLds {
 __host__ __device__ inline size_t rows_lds_bytes(int T, int k, int E_local)
 {
     const size_t r = (size_t)layer_rows_cap(T, k, E_local), tk = (size_t)T * k;
-    const size_t b = (size_t)E_local * 20 + (size_t)layer_hits_cap(T, k, E_local) * 4 + 8 + (2 * tk + r) * 4 + r;
+    const size_t b = (size_t)layer_hits_cap(T, k, E_local) * 16 + 16 + (size_t)E_local * 20 + (2 * tk + r) * 4 + r;
     return (b + 15) & ~(size_t)15;
 }
 
@@ -60,14 +60,14 @@ __device__ __forceinline__ RowsLds rows_lds(char *p, const LayerArgs &a)
 {
     const int r = layer_rows_cap(a.T, a.k, a.E_local), tk = a.T * a.k;
     RowsLds s;
+    s.rec = (LayerRec *)p;
+    p += (size_t)layer_hits_cap(a.T, a.k, a.E_local) * 16;
+    s.n = (int32_t *)p;
+    p += 16;
     s.mask = (uint64_t *)p;
     p += (size_t)a.E_local * 16;
     s.start = (int32_t *)p;
     p += (size_t)a.E_local * 4;
-    s.hit = (int32_t *)p;
-    p += (size_t)min(a.E_local, tk) * 4;
-    s.n = (int32_t *)p;
-    p += 8;
     s.ids = (int32_t *)p;
     p += (size_t)tk * 4;
     s.w = (float *)p;
@@ -82,6 +82,59 @@ __device__ __forceinline__ RowsLds rows_lds(char *p, const LayerArgs &a)
 __device__ __forceinline__ int rank_of(const uint64_t *m, int t)
 {
     return t < 64 ? __popcll(m[0] & ((1ull << t) - 1)) : __popcll(m[0]) + __popcll(m[1] & ((1ull << (t - 64)) - 1));
+}
+
+constexpr int kFewChoices = 32;
+
+// build_rows for a few choices, by one wave without the masks, a lane per choice: a row's number is the number of choices
+// that come before it by (expert, token).
+__device__ __forceinline__ void build_few_rows(const RowsLds &s, const LayerArgs &a, int T, bool publish)
+{
+    const int l = threadIdx.x, n = T * a.k;
+    const int t = l / a.k;
+    int e = l < n ? s.ids[l] - a.e_begin : -1;
+    float w = l < n ? s.w[l] : 0.0f;
+    if (e < 0 || e >= a.E_local) e = -1;
+    if (a.given) {   // an id given twice for a token: one row, the gates added up
+        bool again = false;
+        float more = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            const int ej = __builtin_amdgcn_readlane(e, j);
+            const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j));
+            const bool same = ej == e && j / a.k == t;
+            again |= same && j < l;
+            more += same && j > l ? wj : 0.0f;
+        }
+        w += more;
+        if (again) e = -1;
+    }
+    int row = 0, cnt = 0, hi = 0;
+    bool first = e >= 0;
+    for (int j = 0; j < n; ++j) {
+        const int ej = __builtin_amdgcn_readlane(e, j);
+        if (ej < 0) continue;   // uniform
+        row += ej < e || (ej == e && j < l);
+        cnt += ej == e;
+        first &= !(ej == e && j < l);
+    }
+    const uint64_t firsts = __ballot(first);
+    for (uint64_t m = firsts; m; m &= m - 1) hi += __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)m) - 1) < e;
+    if (e >= 0) {
+        s.tok[row] = (uint8_t)t;
+        s.gate[row] = w;
+        if (first) {
+            s.rec[hi] = LayerRec{e, row, cnt, 0};
+            if (publish) a.plan.rec[hi] = LayerRec{e, row, cnt, 0};
+        }
+    }
+    if (publish && l < a.T * a.k) a.plan.row_of[l] = e >= 0 ? row : -1;
+    if (l == 0) {
+        s.n[0] = __popcll(firsts);
+        if (publish) {
+            a.plan.n[0] = __popcll(firsts);
+            a.plan.n[1] = T;
+        }
+    }
 }
 
 // Builds the rows from s.ids and s.w, which the caller has filled for tokens < T; ends with a barrier.  publish: this
@@ -112,7 +165,7 @@ __device__ __forceinline__ void build_rows(const RowsLds &s, const LayerArgs &a,
             const int hi = hits + __popcll(b & lanemask_lt()), row0 = rows + incl - cnt;
             if (e < a.E_local) s.start[e] = row0;
             if (cnt > 0) {
-                s.hit[hi] = e;
+                s.rec[hi] = LayerRec{e, row0, cnt, 0};
                 if (publish) a.plan.rec[hi] = LayerRec{e, row0, cnt, 0};
             }
             rows += __shfl(incl, kWave - 1);
@@ -120,7 +173,6 @@ __device__ __forceinline__ void build_rows(const RowsLds &s, const LayerArgs &a,
         }
         if (l == 0) {
             s.n[0] = hits;
-            s.n[1] = rows;
             if (publish) {
                 a.plan.n[0] = hits;
                 a.plan.n[1] = T;
@@ -273,15 +325,17 @@ struct IntC {
 };
 
 // Weight tiles per task.  More of them share one load of the tokens' rows, whose traffic out of the L2 costs as much as
-// that of the weights out of memory once an expert has 16 rows or more; fewer make more tasks.  n1: tasks per expert at
-// one tile.  Four tiles where the workgroups get at least four tasks each or come out nearly even; one tile (8 tokens'
-// rows beside 16 weight rows) only where two would not give every workgroup one.
-__device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workgroups)
+// that of the weights out of memory once an expert has 16 rows or more; fewer make more tasks, which come out more even.
+// n1: tasks per expert at one tile.  Four tiles where the workgroups get at least four tasks each or come out nearly even
+// (8 experts x 64 columns, 32 rows each: down 234 -> 199 us); one tile (built for 16 tokens at most) where two would not
+// give every workgroup `few` (7 experts of 2048 features, one tile against two: up 57 against 61 us, few = 2; down of 46
+// experts x 2048 columns: 22 against 19 us, few = 1).
+__device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workgroups, int few)
 {
     const long t2 = (long)hits * ((n1 + 1) / 2), t4 = (long)hits * ((n1 + 3) / 4);
     const long rounds = (t4 + workgroups - 1) / workgroups;
-    if (t4 >= 4L * workgroups || 10 * t4 >= 9 * rounds * workgroups) return t4 > 0 ? 4 : 2;
-    return t2 < workgroups && T <= 16 ? 1 : 2;
+    if (t4 >= 4L * workgroups || (t4 > 0 && 10 * t4 >= 9 * rounds * workgroups)) return 4;
+    return t2 < few * workgroups && T <= 16 ? 1 : 2;
 }
 
 constexpr int kUpWaves = 4;
@@ -482,17 +536,23 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
             if (a.ids_user) a.ids_user[i] = s.ids[i];
             if (a.w_user) a.w_user[i] = s.w[i];
         }
-    build_rows(s, a, T, blockIdx.x == 0);
+    if (a.T * a.k <= kFewChoices) {
+        if (threadIdx.x < kWave) build_few_rows(s, a, T, blockIdx.x == 0);
+        __syncthreads();
+    } else {
+        build_rows(s, a, T, blockIdx.x == 0);
+    }
     const int hits = s.n[0];
-    const int tiles = tiles_per_task(hits, (a.F + 7) / 8, a.T, (int)gridDim.x);
+    const int tiles = tiles_per_task(hits, (a.F + 7) / 8, a.T, (int)gridDim.x, 2);
     const int fs = 8 * tiles;
     const int nf = (a.F + fs - 1) / fs;
     int par = 0;
     for (int q = blockIdx.x; q < hits * nf; q += gridDim.x) {
         const int hi = q / nf, f0 = (q - hi * nf) * fs;
-        const int e = __builtin_amdgcn_readfirstlane(s.hit[hi]);
-        const int row0 = __builtin_amdgcn_readfirstlane(s.start[e]);
-        const int cnt = __builtin_amdgcn_readfirstlane(__popcll(s.mask[2 * e]) + __popcll(s.mask[2 * e + 1]));
+        const LayerRec rec = s.rec[hi];
+        const int e = __builtin_amdgcn_readfirstlane(rec.e);
+        const int row0 = __builtin_amdgcn_readfirstlane(rec.row0);
+        const int cnt = __builtin_amdgcn_readfirstlane(rec.cnt);
         if (tiles == 1) {
             if (cnt <= 8) up_task<Q8, 1, 1>(a, s, e, f0, row0, cnt, red, par);
             else up_task<Q8, 1, 2>(a, s, e, f0, row0, cnt, red, par);
@@ -644,7 +704,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
     __shared__ __attribute__((aligned(16))) char lds[kDownRedBytes];
     float *red = (float *)lds;
     const int hits = a.plan.n[0];
-    const int tiles = tiles_per_task(hits, a.d / 16, a.T, (int)gridDim.x);
+    const int tiles = tiles_per_task(hits, a.d / 16, a.T, (int)gridDim.x, 1);
     const int nc = a.d / (16 * tiles);   // d % 128 == 0
     int par = 0;
     for (int q = blockIdx.x; q < hits * nc; q += gridDim.x) {
