@@ -482,8 +482,8 @@ void *g_scratch_dev[kMaxDevices];
 
 // ---------------------------------------------------------------- the few-token MoE layer
 
-// Workspace: the plan, router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] bf16 and
-// y [T min(k, E_local), d] fp32.
+// Workspace: the plan, router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] in two
+// parts of at most 2 bytes and y [T min(k, E_local), d] fp32.
 struct LayerWs {
     size_t rec, row_of, part, ids, w, h, y, total;
 };
@@ -498,7 +498,7 @@ LayerWs layer_ws(const mk_shape *s)
     L.ids = L.part + align256((size_t)kRouterSegments * s->T * s->E * 4);
     L.w = L.ids + align256(tk * 4);
     L.h = L.w + align256(tk * 4);
-    L.y = L.h + align256(rows * (s->N / 2) * 2);
+    L.y = L.h + align256(rows * s->N * 2);
     L.total = L.y + align256(rows * s->d * 4) + 256;
     return L;
 }
@@ -555,7 +555,7 @@ mk_status layer_impl(const mk_shape *s, bool q8, const void *x, const void *x_q8
     a.plan.n = (int32_t *)ws;
     a.plan.rec = (LayerRec *)(ws + L.rec);
     a.plan.row_of = (int32_t *)(ws + L.row_of);
-    a.h = (uint16_t *)(ws + L.h);
+    a.h = ws + L.h;
     a.y = (float *)(ws + L.y);
     a.out = (uint16_t *)out;
     a.t_valid = t_valid;

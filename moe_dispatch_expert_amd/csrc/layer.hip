@@ -16,8 +16,7 @@
 //     stream the weights as fast as four of them, with a quarter of the
 //     instructions' register pressure).
 // Launches: the router and the selection (unless the caller routed), "up", which
-// writes h = w * silu(g) * u (bf16, the gate folded in before the one rounding),
-// "down", which writes W_down[e] . h per row in fp32, and "sum", which adds each
+// writes h = w * silu(g) * u, "down", which writes W_down[e] . h per row in fp32, and "sum", which adds each
 // token's rows in expert order.
 #include <hip/hip_runtime.h>
 
@@ -296,13 +295,17 @@ __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, u32x4_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
 }
-// Two K = 32 products of e4m3 operands: K element 16 g + i of a 64-wide step sits in lane group g, byte i, in both.
-__device__ __forceinline__ f32x4_t mfma_fp8_64(u32x4_t a, u32x4_t b, f32x4_t c)
+// One K = 128 product of 8-bit operands, e4m3 by e4m3, or (REST) by 2^-8 times e5m2: bytes 0 - 15 of both operands in
+// a0, b0 and 16 - 31 in a1, b1, the same K in the same place of both.  The block scales are powers of two (exponent + 127
+// in every byte).
+template <bool REST>
+__device__ __forceinline__ f32x4_t mfma_fp8(u32x4_t a0, u32x4_t a1, u32x4_t b0, u32x4_t b1, f32x4_t c)
 {
-    const long a0 = (long)(((uint64_t)a.y << 32) | a.x), a1 = (long)(((uint64_t)a.w << 32) | a.z);
-    const long b0 = (long)(((uint64_t)b.y << 32) | b.x), b1 = (long)(((uint64_t)b.w << 32) | b.z);
-    c = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(a0, b0, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(a1, b1, c, 0, 0, 0);
+    typedef int i32x8_v __attribute__((ext_vector_type(8)));
+    const i32x8_v a = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
+    const i32x8_v b = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, REST ? 1 : 0, 0, 0x7F7F7F7F, 0,
+                                                            REST ? 0x77777777 : 0x7F7F7F7F);
 }
 
 // Eight e4m3 codes as bf16 (exact).
@@ -338,6 +341,35 @@ __device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workg
     return t2 < few * workgroups && T <= 16 ? 1 : 2;
 }
 
+// h is kept in two parts, so that its rounding does not show beside the output's own (one bf16 part alone made the
+// layer's error 1.4 times a single rounding's): hi = bf16(h), and the rest h - hi, at most 2^-8 |h|, as bf16 for bf16
+// weights and as e5m2 of 2^8 times it (which the matrix core multiplies with e4m3 as it is) for 8-bit ones, leaving 2^-17
+// and 2^-11 |h|.  A rest that is not finite or past e5m2 (|h| > 57344) is left out.  The second part costs 2% of a
+// decode-shaped layer.  A row: F bf16, then F bf16 or F e5m2.
+template <bool Q8>
+__host__ __device__ constexpr int h_row_bytes(int F)
+{
+    return Q8 ? 3 * F : 4 * F;
+}
+constexpr float kRestScale = 256.0f, kRestMax = 57344.0f;
+
+template <bool Q8>
+__device__ __forceinline__ void store_h(const LayerArgs &a, int row, int f, float h0, float h1)
+{
+    char *p = (char *)a.h + (size_t)row * h_row_bytes<Q8>(a.F);
+    const uint32_t b0 = f32_to_bf16(h0), b1 = f32_to_bf16(h1);
+    const float limit = Q8 ? kRestMax / kRestScale : __builtin_inff();
+    float r0 = h0 - bf16_to_f32(b0), r1 = h1 - bf16_to_f32(b1);
+    r0 = fabsf(r0) < limit ? r0 : 0.0f;
+    r1 = fabsf(r1) < limit ? r1 : 0.0f;
+    *(uint32_t *)(p + 2 * f) = b0 | b1 << 16;
+    if constexpr (Q8)
+        *(uint16_t *)(p + 2 * a.F + f) =
+            (uint16_t)__builtin_amdgcn_cvt_pk_bf8_f32(r0 * kRestScale, r1 * kRestScale, 0, false);
+    else
+        *(uint32_t *)(p + 2 * a.F + 2 * f) = (uint32_t)f32_to_bf16(r0) | (uint32_t)f32_to_bf16(r1) << 16;
+}
+
 constexpr int kUpWaves = 4;
 constexpr int kUpRedBytes = 2 * kUpWaves * 4 * 256 * 4;   // two halves of up_task's exchange
 
@@ -351,6 +383,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
                                         float *red, int &par)
 {
     constexpr int NT = (N8 + 1) / 2;   // 16-column tiles
+    constexpr int NS = N8 < 4 ? N8 : 4, NST = (NS + 1) / 2;   // row groups (tiles) whose x is in registers at a time
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
@@ -404,8 +437,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
     // wave measured no faster)
     auto run = [&](auto uc) {
         constexpr int U = decltype(uc)::value;
-        u32x4_t wv[U][R][2], xv[U][N8];
-        float fx[U][NT];
+        u32x4_t wv[U][R][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -413,48 +445,60 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
 #pragma unroll
                 for (int i = 0; i < 2; ++i) wv[u][r][i] = load_w(w, wo[r][i] + 128 * u, k * 128);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int n0 = 0; n0 < N8; n0 += NS) {
+            u32x4_t xv[U][NS];
+            float fx[U][NST];
 #pragma unroll
-            for (int n = 0; n < N8; ++n) xv[u][n] = load_x(x, xo[n] + 128 * u, k * 128);
-        if constexpr (Q8) {
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float f[U];
-                load_floats<U>(sx, so[n], k * 4, f);
-#pragma unroll
-                for (int u = 0; u < U; ++u) fx[u][n] = f[u];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) swap_halves(wv[u][r][0], wv[u][r][1]);
-            u32x4_t x0[NT], x1[NT];
-            pair_tokens<N8>(xv[u], x0, x1);
+                for (int n = 0; n < NS; ++n) xv[u][n] = load_x(x, xo[n0 + n] + 128 * u, k * 128);
             if constexpr (Q8) {
-                const float wg = __int_as_float(__builtin_amdgcn_readlane(fg, k - s0 + u));
-                const float wu = __int_as_float(__builtin_amdgcn_readlane(fu, k - s0 + u));
-                // accumulator rows 4 g .. 4 g + 3: in the mixed tile groups 0, 1 are gate rows and 2, 3 up rows
-                const float mixed = g < 2 ? wg : wu;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NST; ++n) {
+                    float f[U];
+                    load_floats<U>(sx, so[n0 / 2 + n], k * 4, f);
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
-                        p = mfma_fp8_64(wv[u][r][0], x0[n], p);
-                        p = mfma_fp8_64(wv[u][r][1], x1[n], p);
-                        const float f = (R == 1 ? mixed : r < R / 2 ? wg : wu) * fx[u][n];
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[r][n][v] = __builtin_fmaf(p[v], f, acc[r][n][v]);
-                    }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int r = 0; r < R; ++r) acc[r][n] = mfma_bf16(wv[u][r][i], i == 0 ? x0[n] : x1[n], acc[r][n]);
+                    for (int u = 0; u < U; ++u) fx[u][n] = f[u];
+                }
             }
+            if (n0 == 0) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) swap_halves(wv[u][r][0], wv[u][r][1]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                u32x4_t x0[NST], x1[NST];
+                pair_tokens<NS>(xv[u], x0, x1);
+                if constexpr (Q8) {
+                    const float wg = __int_as_float(__builtin_amdgcn_readlane(fg, k - s0 + u));
+                    const float wu = __int_as_float(__builtin_amdgcn_readlane(fu, k - s0 + u));
+                    // accumulator rows 4 g .. 4 g + 3: in the mixed tile groups 0, 1 are gate rows and 2, 3 up rows
+                    const float mixed = g < 2 ? wg : wu;
+#pragma unroll
+                    for (int n = 0; n < NST; ++n)
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const f32x4_t p = mfma_fp8<false>(wv[u][r][0], wv[u][r][1], x0[n], x1[n],
+                                                              f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+                            const float f = (R == 1 ? mixed : r < R / 2 ? wg : wu) * fx[u][n];
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                acc[r][n0 / 2 + n][v] = __builtin_fmaf(p[v], f, acc[r][n0 / 2 + n][v]);
+                        }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < NST; ++n)
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+                                acc[r][n0 / 2 + n] =
+                                    mfma_bf16(wv[u][r][i], i == 0 ? x0[n] : x1[n], acc[r][n0 / 2 + n]);
+                }
+            }
+            if (N8 > NS) __builtin_amdgcn_sched_barrier(0);
         }
         k += U;
     };
@@ -486,8 +530,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
             const float gate = s.gate[row0 + row];
             const float h0 = gs.x / (1.0f + expf(-gs.x)) * us.x * gate;
             const float h1 = gs.y / (1.0f + expf(-gs.y)) * us.y * gate;
-            *(uint32_t *)(a.h + (size_t)(row0 + row) * a.F + f0 + fi) =
-                (uint32_t)f32_to_bf16(h0) | (uint32_t)f32_to_bf16(h1) << 16;
+            store_h<Q8>(a, row0 + row, f0 + fi, h0, h1);
         }
     }
 }
@@ -580,8 +623,8 @@ constexpr int kDownWaves = 4;
 constexpr int kDownRedBytes = 2 * kDownWaves * 4 * 256 * 4;
 
 // One down task: output columns n0 .. n0 + 16 R - 1 of expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8), written
-// to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3,
-// converted to bf16 (exact) in front of the matrix core and scaled per step.  TAIL: F does not end on a step; pieces past
+// to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3, which
+// meets h's bf16 part converted to bf16 (exact) and h's rest as it is, and is scaled per step.  TAIL: F does not end on a step; pieces past
 // F are zeros on both sides.  red, par: as in up_task.
 template <bool Q8, int R, int N8, bool TAIL>
 __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int row0, int cnt, float *red, int &par)
@@ -590,27 +633,32 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     constexpr int KS = Q8 ? kQ8Group : 64;       // K per step
     constexpr int KP = Q8 ? 16 : 8;              // K per 16-byte piece of a weight row
     constexpr int kBytes = Q8 ? 1 : 2;
-    constexpr int HL = Q8 ? 2 : 1;               // 128-byte lines of an h row per step
+    constexpr int NS = N8 < 4 ? N8 : 4, NST = (NS + 1) / 2;   // row groups (tiles) whose h is in registers at a time
+    constexpr int HL = Q8 ? 3 : 2;               // 128-byte lines of an h row per step: the bf16 part's, then the rest's
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
     const int kp = KP * (g + 4 * (c >> 3));      // the lane's piece of a weight row (swap_halves)
-    // ... and of an h line (pair_tokens), 8 elements: bf16 pieces g and 4 + g, as the weights; e4m3, whose 16-byte piece
-    // is two pieces of h, 2 g and 2 g + 1
+    // ... and of a line of h's bf16 part (pair_tokens), 8 elements: with bf16 weights pieces g and 4 + g, as theirs; with
+    // e4m3, whose 16-byte piece is two pieces of h, 2 g and 2 g + 1.  The rest's pieces are as the weights'.
     const int kh = 8 * (Q8 ? 2 * g + (c >> 3) : g + 4 * (c >> 3));
     const int steps = (a.F + KS - 1) / KS, s1 = steps * (wave + 1) / kDownWaves;
     const uint32_t wbytes = 16 * R * (uint32_t)a.F * kBytes;
     const __amdgpu_buffer_rsrc_t w = buffer_of((const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * kBytes, wbytes);
-    const __amdgpu_buffer_rsrc_t h = buffer_of(a.h + (size_t)row0 * a.F, (uint32_t)cnt * 2 * a.F);
+    const __amdgpu_buffer_rsrc_t h = buffer_of((const char *)a.h + (size_t)row0 * h_row_bytes<Q8>(a.F), (uint32_t)cnt * h_row_bytes<Q8>(a.F));
     const __amdgpu_buffer_rsrc_t sw =
         buffer_of(a.s_dn + (Q8 ? ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * steps : 0), Q8 ? steps * 4 : 0);
-    uint32_t wo[R][2], ho[N8];
+    uint32_t wo[R][2], ho[N8], lo[N8];   // lo: of the rest
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) wo[r][i] = (uint32_t)((16 * r + 8 * i + (c & 7)) * a.F + kp) * kBytes;
 #pragma unroll
-    for (int n = 0; n < N8; ++n) ho[n] = (uint32_t)(min(8 * n + (c & 7), cnt - 1) * a.F + kh) * 2;
+    for (int n = 0; n < N8; ++n) {
+        ho[n] = (uint32_t)min(8 * n + (c & 7), cnt - 1) * h_row_bytes<Q8>(a.F);
+        lo[n] = ho[n] + 2 * a.F + kp * kBytes;
+        ho[n] += 2 * kh;
+    }
     f32x4_t acc[R][NT];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -619,7 +667,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     int s = steps * wave / kDownWaves;
     auto run = [&](auto uc) {
         constexpr int U = decltype(uc)::value;
-        u32x4_t wv[U][R][2], hv[U][HL][N8];
+        u32x4_t wv[U][R][2];
         float fw[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -629,50 +677,83 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
                 for (int i = 0; i < 2; ++i)
                     wv[u][r][i] =
                         load_w(w, !TAIL || kp + (s + u) * KS < a.F ? wo[r][i] + 128 * u : kPastResource, s * 128);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int l = 0; l < HL; ++l)
-#pragma unroll
-                for (int n = 0; n < N8; ++n)
-                    hv[u][l][n] = load_x(h, !TAIL || kh + 64 * l + (s + u) * KS < a.F ? ho[n] + 128 * (HL * u + l)
-                                                                                     : kPastResource,
-                                         s * 128 * HL);
         if constexpr (Q8) load_floats<U>(sw, 0, s * 4, fw);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            u32x4_t x[HL][2][NT];
+        for (int n0 = 0; n0 < N8; n0 += NS) {
+            u32x4_t hv[U][HL][NS];
 #pragma unroll
-            for (int l = 0; l < HL; ++l) pair_tokens<N8>(hv[u][l], x[l][0], x[l][1]);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                swap_halves(wv[u][r][0], wv[u][r][1]);
-                if constexpr (Q8) {
-                    u32x4_t b[4];
+                for (int l = 0; l < HL; ++l)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        b[2 * i] = fp8_to_bf16(wv[u][r][i].x, wv[u][r][i].y);
-                        b[2 * i + 1] = fp8_to_bf16(wv[u][r][i].z, wv[u][r][i].w);
+                    for (int n = 0; n < NS; ++n) {
+                        const bool rest = l == HL - 1;
+                        const int k = rest ? kp : kh + 64 * l;
+                        const uint32_t off = rest ? lo[n0 + n] + 128 * u : ho[n0 + n] + 128 * ((HL - 1) * u + l);
+                        hv[u][l][n] = load_x(h, !TAIL || k + (s + u) * KS < a.F ? off : kPastResource,
+                                             rest ? s * 128 : s * 128 * (HL - 1));
                     }
+            if (n0 == 0) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) p = mfma_bf16(b[i], x[i / 2][i & 1][n], p);
+                    for (int r = 0; r < R; ++r) swap_halves(wv[u][r][0], wv[u][r][1]);
+            }
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) acc[r][n][v] = __builtin_fmaf(p[v], fw[u], acc[r][n][v]);
+            for (int u = 0; u < U; ++u) {
+                u32x4_t x[HL][2][NST];
+#pragma unroll
+                for (int l = 0; l < HL; ++l) pair_tokens<NS>(hv[u][l], x[l][0], x[l][1]);
+                if constexpr (Q8) {
+                    // RG tiles at a time, so that their chains of products interleave
+                    constexpr int RG = NST == 1 && R > 1 ? 2 : 1;
+#pragma unroll
+                    for (int r0 = 0; r0 < R; r0 += RG) {
+                        u32x4_t b[RG][4];
+#pragma unroll
+                        for (int r = 0; r < RG; ++r)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const u32x4_t v = wv[u][r0 + r][i];
+                                b[r][2 * i] = fp8_to_bf16(v.x, v.y);
+                                b[r][2 * i + 1] = fp8_to_bf16(v.z, v.w);
+                            }
+#pragma unroll
+                        for (int n = 0; n < NST; ++n) {
+                            f32x4_t p[RG];
+#pragma unroll
+                            for (int r = 0; r < RG; ++r)
+                                p[r] = mfma_fp8<true>(wv[u][r0 + r][0], wv[u][r0 + r][1], x[HL - 1][0][n],
+                                                      x[HL - 1][1][n], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int r = 0; r < RG; ++r) p[r] = mfma_bf16(b[r][i], x[i / 2][i & 1][n], p[r]);
+#pragma unroll
+                            for (int r = 0; r < RG; ++r)
+#pragma unroll
+                                for (int v = 0; v < 4; ++v)
+                                    acc[r0 + r][n0 / 2 + n][v] =
+                                        __builtin_fmaf(p[r][v], fw[u], acc[r0 + r][n0 / 2 + n][v]);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int l = 0; l < 2; ++l)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) acc[r][n] = mfma_bf16(wv[u][r][i], x[0][i][n], acc[r][n]);
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int n = 0; n < NST; ++n)
+#pragma unroll
+                                for (int r = 0; r < R; ++r)
+                                    acc[r][n0 / 2 + n] = mfma_bf16(wv[u][r][i], x[l][i][n], acc[r][n0 / 2 + n]);
                 }
             }
+            if (N8 > NS) __builtin_amdgcn_sched_barrier(0);
         }
         s += U;
     };
-    constexpr int U = R == 1 ? 4 : N8 == 8 ? 1 : 2;
+    constexpr int U = R == 1 && N8 == 1 ? 4 : N8 >= (Q8 && R == 4 ? 2 : Q8 ? 4 : 8) ? 1 : 2;   // 256 registers
     while (s + U <= s1) run(IntC<U>());
     while (s < s1) run(IntC<1>());
     // the waves' parts meet in LDS as in up_task; two neighbouring columns a thread
@@ -726,7 +807,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
                 if (m <= 8) down_task<Q8, R, 1, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else if (m <= 16) down_task<Q8, R, 2, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else if (m <= 32) down_task<Q8, R, 4, TAIL>(a, e, n0, row0 + r, m, red, par);
-                else down_task<Q8, R, 8, TAIL>(a, e, n0, row0 + r, m, red, par);
+                else   // four e4m3 tiles by four token tiles would not fit the registers
+                    for (int i = 0; i < (Q8 ? R / 2 : 1); ++i)
+                        down_task<Q8, Q8 ? 2 : R, 8, TAIL>(a, e, n0 + 32 * i, row0 + r, m, red, par);
             };
             if (tiles == 4) rows(IntC<4>());
             else rows(IntC<2>());

@@ -37,7 +37,7 @@ struct LayerArgs {
     float *w_user;
     float *part;                     // [8, T, E] router partial sums
     const float *wr, *bias;          // router
-    uint16_t *h;                     // [T min(k, E_local), F] bf16: gate * silu(g) * u, rows in expert order
+    void *h;                         // gate * silu(g) * u, rows in expert order, in two parts (layer.hip)
     float *y;                        // [T min(k, E_local), d]: the rows' products with W_down
     uint16_t *out;                   // [T, d] bf16
     const int32_t *t_valid;          // NULL or the number of tokens to compute (device)
