@@ -364,9 +364,12 @@ mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma,
  * this library's reading, as for mk_swiglu and mk_combine:
  *   out[t] = bf16_rne( sum over t's local choices e of
  *              w[t, e] * W_down[e] . ( silu(W_gate[e] . x[t]) * (W_up[e] . x[t]) ) )
- * fp32 sums and activation.  One intermediate is rounded: w * silu(g) * u, to
- * bf16 (g and u themselves are not, unlike mk_dispatch_gemm followed by
- * mk_swiglu, and the gate is folded in before that rounding).
+ * fp32 sums and activation.  The intermediate w * silu(g) * u is kept in two
+ * parts, 16 significant bits (mk_moe_layer_q8: 11), so the output's is the one
+ * rounding that shows (g and u are not rounded to bf16, unlike in
+ * mk_dispatch_gemm followed by mk_swiglu).  Every sum has a fixed order, which
+ * does not depend on the other tokens of the call: a token's row has the same
+ * bits alone and in any batch.
  *   s           the shape, with N = 2F as for mk_dispatch_gemm_swiglu; T <= 128
  *   w_router, bias   routing inside the call, ids and gates bit for bit those of
  *               mk_route_topk; or
@@ -385,7 +388,6 @@ mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma,
  *   topk_ids_out, topk_w_out   NULL or [T, k]: the choices, as used
  *   workspace   mk_moe_layer_workspace_bytes(s) bytes, any contents; two calls
  *               in flight must not share one.
- * Results do not depend on the device's load: every sum has a fixed order.
  * Requires the shape of mk_dispatch_gemm, F % 8 == 0 (else MK_EINVAL), T <= 128,
  * d <= 32768, k <= 32, 2F * d * 2 < 2^31 (else MK_EUNSUPPORTED).  T == 0 is a
  * no-op returning MK_OK.  The call allocates nothing and may be captured. */
@@ -401,8 +403,8 @@ mk_status mk_moe_layer(const mk_shape *s, const void *x, const float *w_router, 
  *   W_gate[e][f,i] = w_gate_up_q8[e, f, i]     * gate_up_scale[e, f / 128, i / 128]
  *   W_up[e][f, i]  = w_gate_up_q8[e, F + f, i] * gate_up_scale[e, nf + f / 128, i / 128],  nf = ceil(F / 128)
  *   W_down[e][n,f] = w_down_q8[e, n, f]        * down_scale[e, n / 128, f / 128]
- * The products are of the 8-bit values (of bf16 w * silu(g) * u with the 8-bit
- * W_down), summed in fp32 over 128 columns, scaled, and summed in fp32.
+ * The products are of the 8-bit values (with W_down: of its 8-bit values and the
+ * intermediate), summed in fp32 over 128 columns, scaled, and summed in fp32.
  *   x             [T, d] bf16, the router's input (NULL with topk_ids_in)
  *   x_q8, x_scale [T, d] e4m3 (OCP), [T, d / 128] fp32
  *   w_gate_up_q8, gate_up_scale   [E_local, 2F, d] e4m3, [E_local, 2 nf, d / 128] fp32

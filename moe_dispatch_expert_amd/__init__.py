@@ -395,33 +395,33 @@ def mk_grouped_gemm_workspace_bytes(E_local: int) -> int:
     return int(load().mk_grouped_gemm_workspace_bytes(E_local))
 
 
-_FP8 = torch.float8_e4m3fn
+_FP8, _BF16, _F32, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
 
 
-def _on(dev: torch.device, what: str, **tensors) -> None:
-    """Checks name=(tensor, dtype, shape) against the call's device and the library's layout; a tensor may be None."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.device != dev or not t.is_cuda:
-            raise ValueError(f"{what}: {name} is on {t.device}, expected a device tensor on {dev}")
-        if t.dtype is not dtype or t.shape != shape:
-            raise ValueError(f"{what}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: {name} must be contiguous")
+def _need(what: str, name: str, t: torch.Tensor, dev: torch.device, dtype: torch.dtype, shape) -> int:
+    """The address of a tensor that has to be contiguous, on the call's device and of this type and shape."""
+    if t.device != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous {dtype} tensor {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
 
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _may(what: str, name: str, t: Optional[torch.Tensor], dev, dtype, shape):
+    return None if t is None else _need(what, name, t, dev, dtype, shape)
 
 
 def _call_on(dev: torch.device, stream, fn, what: str, *args) -> None:
     """Runs fn(*args, stream) with `dev` current, on the caller's stream or dev's current one."""
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: libmk takes device tensors only, got {dev}")
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call_on(dev, stream, fn, what, *args)
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    _check(fn(*args, s.cuda_stream), what)
+    # the raw handle: a decode step makes many of these calls, and building a Stream object takes 2 us
+    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    st = fn(*args, s)
+    if st != MK_OK:
+        raise MkError(st, what)
 
 
 def mk_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None, *,
@@ -432,31 +432,34 @@ def mk_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torc
     Returns a dict of the outputs: "residual" (h = x + residual, if a residual is given), "y" (with bf16=True) and
     "q8", "q8_scale" (with q8=True: e4m3 [T, d] and fp32 [T, d / 128]).  Tensors given in `out` under these names
     receive them (residual and y may be x or residual itself); the others are allocated."""
-    T, d = x.shape
+    what = "mk_add_rmsnorm"
+    shape = T, d = x.shape
     dev = x.device
     o = {}
-    given = out or {}
+    given = out or o
+
+    def output(name, dtype, of):
+        t = given.get(name)
+        if t is None:
+            t = torch.empty_like(x) if dtype is _BF16 else torch.empty(of, dtype=dtype, device=dev)
+            p = t.data_ptr()
+        else:
+            p = _need(what, name, t, dev, dtype, of)
+        o[name] = t
+        return p
+
+    px = _need(what, "x", x, dev, _BF16, shape)
+    pg = _need(what, "gamma", gamma, dev, _BF16, (d,))
+    pr = po = py = pq = ps = None
     if residual is not None:
-        o["residual"] = given.get("residual")
-        if o["residual"] is None:
-            o["residual"] = torch.empty_like(x)
+        pr = _need(what, "residual", residual, dev, _BF16, shape)
+        po = output("residual", _BF16, shape)
     if bf16:
-        o["y"] = given.get("y")
-        if o["y"] is None:
-            o["y"] = torch.empty_like(x)
+        py = output("y", _BF16, shape)
     if q8:
-        o["q8"], o["q8_scale"] = given.get("q8"), given.get("q8_scale")
-        if o["q8"] is None:
-            o["q8"] = torch.empty(T, d, dtype=_FP8, device=dev)
-        if o["q8_scale"] is None:
-            o["q8_scale"] = torch.empty(T, d // 128, dtype=torch.float32, device=dev)
-    res_out, y, q, qs = o.get("residual"), o.get("y"), o.get("q8"), o.get("q8_scale")
-    bf = torch.bfloat16
-    _on(dev, "mk_add_rmsnorm", x=(x, bf, x.shape), gamma=(gamma, bf, (d,)), residual=(residual, bf, x.shape),
-        residual_out=(res_out, bf, x.shape), y=(y, bf, x.shape), q8=(q, _FP8, x.shape),
-        q8_scale=(qs, torch.float32, (T, d // 128)))
-    _call_on(dev, stream, load().mk_add_rmsnorm, "mk_add_rmsnorm", x.data_ptr(), _addr(residual), gamma.data_ptr(),
-             T, d, eps, _addr(res_out), _addr(y), _addr(q), _addr(qs))
+        pq = output("q8", _FP8, shape)
+        ps = output("q8_scale", _F32, (T, d // 128))
+    _call_on(dev, stream, (_lib or load()).mk_add_rmsnorm, what, px, pr, pg, T, d, eps, po, py, pq, ps)
     return o
 
 
@@ -477,37 +480,37 @@ def _moe_layer(what, x, x_q8, x_scale, w_gate_up, gate_up_scale, w_down, down_sc
     if E is None:
         E = w_router.shape[1] if w_router is not None else E_local
     given = out or {}
-    o = {"out": given.get("out"), "topk_ids": given.get("topk_ids"), "topk_w": given.get("topk_w")}
-    if o["out"] is None:
-        o["out"] = torch.empty(T, d, dtype=torch.bfloat16, device=dev)
-    shape = _shape(T, d, E, k, e_begin, E_local, two_f)
-    lib = load()
-    if workspace is None:
-        nbytes = int(lib.mk_moe_layer_workspace_bytes(ctypes.byref(shape)))
-        if nbytes == 0:   # the call itself names the reason
-            nbytes = 256
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    wt, f32 = (_FP8 if q8 else torch.bfloat16), torch.float32
-    nf = -(-F // 128)
-    _on(dev, what, x=(x, torch.bfloat16, (T, d)), x_q8=(x_q8, _FP8, (T, d)), x_scale=(x_scale, f32, (T, d // 128)),
-        w_router=(w_router, f32, (d, E)), bias=(bias, f32, (E,)), topk_ids_in=(topk_ids_in, torch.int32, (T, k)),
-        topk_w_in=(topk_w_in, f32, (T, k)), w_gate_up=(w_gate_up, wt, (E_local, two_f, d)),
-        gate_up_scale=(gate_up_scale, f32, (E_local, 2 * nf, d // 128)), w_down=(w_down, wt, (E_local, d, F)),
-        down_scale=(down_scale, f32, (E_local, d // 128, nf)), t_valid=(t_valid, torch.int32, (1,)),
-        out=(o["out"], torch.bfloat16, (T, d)), topk_ids=(o["topk_ids"], torch.int32, (T, k)),
-        topk_w=(o["topk_w"], f32, (T, k)), workspace=(workspace, torch.uint8, workspace.shape))
-    routing = (_addr(w_router), _addr(bias), _addr(topk_ids_in), _addr(topk_w_in))
-    outs = (_addr(t_valid), o["out"].data_ptr(), _addr(o["topk_ids"]), _addr(o["topk_w"]), workspace.data_ptr(),
-            workspace.numel())
-    if q8:
-        _call_on(dev, stream, lib.mk_moe_layer_q8, what, ctypes.byref(shape), _addr(x), x_q8.data_ptr(),
-                 _addr(x_scale), *routing, w_gate_up.data_ptr(), _addr(gate_up_scale), w_down.data_ptr(),
-                 _addr(down_scale), *outs)
+    y, ids, gates = given.get("out"), given.get("topk_ids"), given.get("topk_w")
+    if y is None:
+        y = torch.empty((T, d), dtype=_BF16, device=dev)
+        py = y.data_ptr()
     else:
-        _call_on(dev, stream, lib.mk_moe_layer, what, ctypes.byref(shape), x.data_ptr(), *routing,
-                 w_gate_up.data_ptr(), w_down.data_ptr(), *outs)
-    o["workspace"] = workspace
-    return o
+        py = _need(what, "out", y, dev, _BF16, (T, d))
+    lib = _lib or load()
+    shape = _shape(T, d, E, k, e_begin, E_local, two_f)
+    if workspace is None:   # (for a shape that the call refuses the size is 0, and the call names the reason)
+        workspace = torch.empty(max(256, lib.mk_moe_layer_workspace_bytes(ctypes.byref(shape))), dtype=torch.uint8,
+                                device=dev)
+    routing = (_may(what, "w_router", w_router, dev, _F32, (d, E)), _may(what, "bias", bias, dev, _F32, (E,)),
+               _may(what, "topk_ids_in", topk_ids_in, dev, _I32, (T, k)),
+               _may(what, "topk_w_in", topk_w_in, dev, _F32, (T, k)))
+    outs = (_may(what, "t_valid", t_valid, dev, _I32, (1,)), py, _may(what, "topk_ids", ids, dev, _I32, (T, k)),
+            _may(what, "topk_w", gates, dev, _F32, (T, k)),
+            _need(what, "workspace", workspace, dev, torch.uint8, workspace.shape), workspace.numel())
+    px = _may(what, "x", x, dev, _BF16, (T, d))
+    if q8:
+        nb, nf = d // 128, -(-F // 128)
+        _call_on(dev, stream, lib.mk_moe_layer_q8, what, ctypes.byref(shape), px,
+                 _need(what, "x_q8", x_q8, dev, _FP8, (T, d)), _need(what, "x_scale", x_scale, dev, _F32, (T, nb)),
+                 *routing, _need(what, "w_gate_up", w_gate_up, dev, _FP8, (E_local, two_f, d)),
+                 _need(what, "gate_up_scale", gate_up_scale, dev, _F32, (E_local, 2 * nf, nb)),
+                 _need(what, "w_down", w_down, dev, _FP8, (E_local, d, F)),
+                 _need(what, "down_scale", down_scale, dev, _F32, (E_local, nb, nf)), *outs)
+    else:
+        _call_on(dev, stream, lib.mk_moe_layer, what, ctypes.byref(shape), px, *routing,
+                 _need(what, "w_gate_up", w_gate_up, dev, _BF16, (E_local, two_f, d)),
+                 _need(what, "w_down", w_down, dev, _BF16, (E_local, d, F)), *outs)
+    return {"out": y, "topk_ids": ids, "topk_w": gates, "workspace": workspace}
 
 
 def mk_moe_layer(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: torch.Tensor, k: int, *,

@@ -493,7 +493,7 @@ LayerWs layer_ws(const mk_shape *s)
     const size_t rows = (size_t)layer_rows_cap(s->T, s->k, s->E_local), tk = (size_t)s->T * s->k;
     LayerWs L;
     L.rec = 256;
-    L.row_of = L.rec + align256((size_t)layer_hits_cap(s->T, s->k, s->E_local) * sizeof(LayerRec));
+    L.row_of = L.rec + align256(std::min<size_t>(tk, 1024) * sizeof(LayerRec));   // E_local <= 1024
     L.part = L.row_of + align256(tk * 4);
     L.ids = L.part + align256((size_t)kRouterSegments * s->T * s->E * 4);
     L.w = L.ids + align256(tk * 4);
