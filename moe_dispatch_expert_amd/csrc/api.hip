@@ -498,7 +498,7 @@ LayerWs layer_ws(const mk_shape *s)
     L.ids = L.part + align256((size_t)kRouterSegments * s->T * s->E * 4);
     L.w = L.ids + align256(tk * 4);
     L.h = L.w + align256(tk * 4);
-    L.y = L.h + align256(rows * s->N * 2);
+    L.y = L.h + align256(rows * std::max(layer_h_row_bytes(false, s->N / 2), layer_h_row_bytes(true, s->N / 2)));
     L.total = L.y + align256(rows * s->d * 4) + 256;
     return L;
 }

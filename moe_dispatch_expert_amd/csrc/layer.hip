@@ -252,25 +252,41 @@ __device__ __forceinline__ void load_floats(__amdgpu_buffer_rsrc_t r, uint32_t o
 
 // Sixteen weight rows x 128 bytes come in as two loads of 8 rows x 128 bytes, so that each load reads whole cache lines:
 // non-temporal loads of 16 rows x 64 bytes, which the operand layout below would give, fetch every line twice (measured
-// over 2 GiB, rows 14336 bytes apart: 5.5 against 7.1 TB/s).  Lane i + 16 g of load a (rows 0 - 7) and of load b (rows
-// 8 - 15) takes row i % 8, 16-byte piece g + 4 (i / 8).  Exchanging a's lanes i >= 8 with b's lanes i < 8 inside each 16
-// lanes leaves the matrix core's layout, lane i + 16 g = row i: piece g in a, piece 4 + g in b.
-__device__ __forceinline__ void swap_halves(u32x4_t &a, u32x4_t &b)
+// over 2 GiB, rows 14336 bytes apart: 5.5 against 7.1 TB/s).  Neighbouring lanes take neighbouring 16-byte pieces, since
+// the address unit takes a cycle per lane otherwise (out of the L2: 9.7 TB/s, 19 with pairs, 30 with fours, which would
+// need a second exchange): lane i + 16 g of load a (even rows) and of load b (odd rows) takes row i - i % 2 (+ 1), piece
+// 2 g + i % 2.  Exchanging a's odd lanes with b's even ones leaves the matrix core's layout, lane i + 16 g = row i: piece
+// 2 g in a, piece 2 g + 1 in b.
+constexpr int kDppPairs = 0xB1;   // quad_perm:[1,0,3,2]
+__device__ __forceinline__ uint32_t neighbour(uint32_t v)
 {
-    constexpr int kRor8 = 0x128;   // DPP row_ror:8
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kDppPairs, 0xF, 0xF, true);
+}
+__device__ __forceinline__ void swap_pairs(u32x4_t &a, u32x4_t &b)
+{
+    const bool odd = threadIdx.x & 1;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int x = (int)a[j], y = (int)b[j];
-        a[j] = (uint32_t)__builtin_amdgcn_update_dpp(x, y, kRor8, 0xF, 0xC, false);
-        b[j] = (uint32_t)__builtin_amdgcn_update_dpp(y, x, kRor8, 0xF, 0x3, false);
+        const uint32_t x = a[j], y = b[j], nx = neighbour(x), ny = neighbour(y);
+        a[j] = odd ? ny : x;
+        b[j] = odd ? y : nx;
     }
 }
 
-// The tokens' operand comes in the same way: 8 tokens x 128 bytes per load, group i of 8 tokens in v[i], two neighbouring
-// groups exchanged into the two halves of a 16-token tile.  A single group (8 tokens or fewer, the ordinary case of a
-// decode step) needs no second load: its own lanes i >= 8 hold the other pieces, one rotation away, and what the
-// columns past 8 get does not matter.  With 16 tokens x 64 bytes per load the loads of four tokens' rows slowed the
-// weight stream by 5%.
+// The tokens' operand comes in the same way: 8 tokens x 128 bytes per load; two neighbouring loads v[2 n], v[2 n + 1] take
+// the even and the odd tokens of a 16-token tile and are exchanged.  A single group (8 tokens or fewer, the ordinary case
+// of a decode step) needs no second load: token i takes column 2 i, whose lane's neighbour holds the other piece, and what
+// the odd columns get does not matter.
+template <int N8>
+__device__ __forceinline__ int token_of(int n, int c)   // of group n, in the lane of column c
+{
+    return N8 == 1 ? c >> 1 : 8 * (n & ~1) + (c & 14) + (n & 1);
+}
+template <int N8>
+__device__ __forceinline__ int column_of(int token)   // in the tile of its 16 tokens
+{
+    return N8 == 1 ? 2 * token : token & 15;
+}
 template <int N8>
 __device__ __forceinline__ void pair_tokens(u32x4_t (&v)[N8], u32x4_t (&first)[(N8 + 1) / 2],
                                             u32x4_t (&second)[(N8 + 1) / 2])
@@ -278,14 +294,13 @@ __device__ __forceinline__ void pair_tokens(u32x4_t (&v)[N8], u32x4_t (&first)[(
     if constexpr (N8 == 1) {
         first[0] = v[0];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            second[0][j] = (uint32_t)__builtin_amdgcn_update_dpp((int)v[0][j], (int)v[0][j], 0x128, 0xF, 0xF, false);
+        for (int j = 0; j < 4; ++j) second[0][j] = neighbour(v[0][j]);
     } else {
 #pragma unroll
         for (int n = 0; n < N8 / 2; ++n) {
             first[n] = v[2 * n];
             second[n] = v[2 * n + 1];
-            swap_halves(first[n], second[n]);
+            swap_pairs(first[n], second[n]);
         }
     }
 }
@@ -345,29 +360,28 @@ __device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workg
 // layer's error 1.4 times a single rounding's): hi = bf16(h), and the rest h - hi, at most 2^-8 |h|, as bf16 for bf16
 // weights and as e5m2 of 2^8 times it (which the matrix core multiplies with e4m3 as it is) for 8-bit ones, leaving 2^-17
 // and 2^-11 |h|.  A rest that is not finite or past e5m2 (|h| > 57344) is left out.  The second part costs 2% of a
-// decode-shaped layer.  A row: F bf16, then F bf16 or F e5m2.
-template <bool Q8>
-__host__ __device__ constexpr int h_row_bytes(int F)
-{
-    return Q8 ? 3 * F : 4 * F;
-}
+// decode-shaped layer.  A row: the bf16 part, then the rest.  With 8-bit weights the bf16 part's 16-byte pieces of every
+// 128 elements are stored as pieces 0 1 4 5 8 9 12 13, 2 3 6 7 10 11 14 15, so that the lane of weight piece 2 g, 2 g + 1
+// (elements 32 g .. 32 g + 31) finds its four in two loads of whole cache lines.
 constexpr float kRestScale = 256.0f, kRestMax = 57344.0f;
 
 template <bool Q8>
 __device__ __forceinline__ void store_h(const LayerArgs &a, int row, int f, float h0, float h1)
 {
-    char *p = (char *)a.h + (size_t)row * h_row_bytes<Q8>(a.F);
+    char *p = (char *)a.h + (size_t)row * layer_h_row_bytes(Q8, a.F);
+    const int at = Q8 ? (f & ~0x78) | (f & 8) | (f & 0x10) << 2 | (f & 0x60) >> 1 : f;
     const uint32_t b0 = f32_to_bf16(h0), b1 = f32_to_bf16(h1);
     const float limit = Q8 ? kRestMax / kRestScale : __builtin_inff();
     float r0 = h0 - bf16_to_f32(b0), r1 = h1 - bf16_to_f32(b1);
     r0 = fabsf(r0) < limit ? r0 : 0.0f;
     r1 = fabsf(r1) < limit ? r1 : 0.0f;
-    *(uint32_t *)(p + 2 * f) = b0 | b1 << 16;
+    *(uint32_t *)(p + 2 * at) = b0 | b1 << 16;
+    p += layer_h_rest(Q8, a.F);
     if constexpr (Q8)
-        *(uint16_t *)(p + 2 * a.F + f) =
+        *(uint16_t *)(p + f) =
             (uint16_t)__builtin_amdgcn_cvt_pk_bf8_f32(r0 * kRestScale, r1 * kRestScale, 0, false);
     else
-        *(uint32_t *)(p + 2 * a.F + 2 * f) = (uint32_t)f32_to_bf16(r0) | (uint32_t)f32_to_bf16(r1) << 16;
+        *(uint32_t *)(p + 2 * f) = (uint32_t)f32_to_bf16(r0) | (uint32_t)f32_to_bf16(r1) << 16;
 }
 
 constexpr int kUpWaves = 4;
@@ -387,7 +401,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
-    const uint32_t pitch = (uint32_t)a.d * (Q8 ? 1 : 2);
+    const uint32_t pitch = (uint32_t)a.d * (Q8 ? 1 : 2), piece = 16 * (2 * g + (c & 1));
     const int steps = (int)(pitch / 128), s0 = steps * wave / kUpWaves, s1 = steps * (wave + 1) / kUpWaves;
     const uint32_t wbytes = 2 * (uint32_t)a.F * pitch;
     const __amdgpu_buffer_rsrc_t w = buffer_of((const char *)a.w_gu + (size_t)e * wbytes, wbytes);
@@ -395,28 +409,28 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
     // the lane's weight rows in each tile (features past F repeat the last; never stored)
     uint32_t wo[R][2], xo[N8], so[NT];
     if constexpr (R == 1) {
-        wo[0][0] = f0 + (c & 7);
-        wo[0][1] = a.F + wo[0][0];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wo[0][i] = f0 + (c & 6) + i + (c < 8 ? 0 : a.F);
     } else {
 #pragma unroll
         for (int r = 0; r < R / 2; ++r)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                wo[r][i] = min(f0 + 16 * r + 8 * i + (c & 7), a.F - 1);
+                wo[r][i] = min(f0 + 16 * r + (c & 14) + i, a.F - 1);
                 wo[R / 2 + r][i] = a.F + wo[r][i];
             }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wo[r][i] = wo[r][i] * pitch + 16 * (g + 4 * (c >> 3));
+        for (int i = 0; i < 2; ++i) wo[r][i] = wo[r][i] * pitch + piece;
     // the lane's token in each group of 8 (past cnt the last again; columns never stored)
 #pragma unroll
     for (int n = 0; n < N8; ++n)
-        xo[n] = s.tok[row0 + min(8 * n + (c & 7), cnt - 1)] * pitch + 16 * (g + 4 * (c >> 3));
+        xo[n] = s.tok[row0 + min(token_of<N8>(n, c), cnt - 1)] * pitch + piece;
     // 8-bit form: the scales of its column's token (a step is a block)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) so[n] = Q8 ? s.tok[row0 + min(16 * n + c, cnt - 1)] * (uint32_t)steps * 4 : 0;
+    for (int n = 0; n < NT; ++n) so[n] = Q8 ? s.tok[row0 + min(N8 == 1 ? c >> 1 : 16 * n + c, cnt - 1)] * (uint32_t)steps * 4 : 0;
     f32x4_t acc[R][NT];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -465,7 +479,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) swap_halves(wv[u][r][0], wv[u][r][1]);
+                    for (int r = 0; r < R; ++r) swap_pairs(wv[u][r][0], wv[u][r][1]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -520,7 +534,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
             float2 gs = make_float2(0.0f, 0.0f), us = gs;
 #pragma unroll
             for (int v = 0; v < kUpWaves; ++v) {
-                const float *q = rb + (v * R + (fi >> 4)) * 256 + ci * 16 + (fi & 15);
+                const float *q = rb + (v * R + (fi >> 4)) * 256 + column_of<N8>(ci) * 16 + (fi & 15);
                 const float2 gv = *(const float2 *)q, uv = *(const float2 *)(q + (R == 1 ? 8 : R / 2 * 256));
                 gs.x += gv.x;
                 gs.y += gv.y;
@@ -638,26 +652,26 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
-    const int kp = KP * (g + 4 * (c >> 3));      // the lane's piece of a weight row (swap_halves)
-    // ... and of a line of h's bf16 part (pair_tokens), 8 elements: with bf16 weights pieces g and 4 + g, as theirs; with
-    // e4m3, whose 16-byte piece is two pieces of h, 2 g and 2 g + 1.  The rest's pieces are as the weights'.
-    const int kh = 8 * (Q8 ? 2 * g + (c >> 3) : g + 4 * (c >> 3));
+    // the lane's piece of a weight row and of the rest of an h row (swap_pairs), in elements, and of h's bf16 part, where
+    // an 8-bit weight piece is two (store_h)
+    const int kp = KP * (2 * g + (c & 1)), kh = Q8 ? 8 * (4 * g + (c & 1)) : kp;
     const int steps = (a.F + KS - 1) / KS, s1 = steps * (wave + 1) / kDownWaves;
     const uint32_t wbytes = 16 * R * (uint32_t)a.F * kBytes;
     const __amdgpu_buffer_rsrc_t w = buffer_of((const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * kBytes, wbytes);
-    const __amdgpu_buffer_rsrc_t h = buffer_of((const char *)a.h + (size_t)row0 * h_row_bytes<Q8>(a.F), (uint32_t)cnt * h_row_bytes<Q8>(a.F));
+    const __amdgpu_buffer_rsrc_t h = buffer_of((const char *)a.h + (size_t)row0 * layer_h_row_bytes(Q8, a.F),
+                                               (uint32_t)cnt * layer_h_row_bytes(Q8, a.F));
     const __amdgpu_buffer_rsrc_t sw =
         buffer_of(a.s_dn + (Q8 ? ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * steps : 0), Q8 ? steps * 4 : 0);
     uint32_t wo[R][2], ho[N8], lo[N8];   // lo: of the rest
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) wo[r][i] = (uint32_t)((16 * r + 8 * i + (c & 7)) * a.F + kp) * kBytes;
+        for (int i = 0; i < 2; ++i) wo[r][i] = (uint32_t)((16 * r + (c & 14) + i) * a.F + kp) * kBytes;
 #pragma unroll
     for (int n = 0; n < N8; ++n) {
-        ho[n] = (uint32_t)min(8 * n + (c & 7), cnt - 1) * h_row_bytes<Q8>(a.F);
-        lo[n] = ho[n] + 2 * a.F + kp * kBytes;
-        ho[n] += 2 * kh;
+        ho[n] = (uint32_t)min(token_of<N8>(n, c), cnt - 1) * layer_h_row_bytes(Q8, a.F);
+        lo[n] = ho[n] + layer_h_rest(Q8, a.F) + kp * kBytes;
+        ho[n] += 16 * (2 * g + (c & 1));
     }
     f32x4_t acc[R][NT];
 #pragma unroll
@@ -688,7 +702,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
 #pragma unroll
                     for (int n = 0; n < NS; ++n) {
                         const bool rest = l == HL - 1;
-                        const int k = rest ? kp : kh + 64 * l;
+                        const int k = rest ? kp : kh + 16 * l;
                         const uint32_t off = rest ? lo[n0 + n] + 128 * u : ho[n0 + n] + 128 * ((HL - 1) * u + l);
                         hv[u][l][n] = load_x(h, !TAIL || k + (s + u) * KS < a.F ? off : kPastResource,
                                              rest ? s * 128 : s * 128 * (HL - 1));
@@ -697,7 +711,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int r = 0; r < R; ++r) swap_halves(wv[u][r][0], wv[u][r][1]);
+                    for (int r = 0; r < R; ++r) swap_pairs(wv[u][r][0], wv[u][r][1]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -770,7 +784,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
             float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int v2 = 0; v2 < kDownWaves; ++v2) {
-                const float2 p = *(const float2 *)(rb + (v2 * R + (ni >> 4)) * 256 + (row & 15) * 16 + (ni & 15));
+                const float2 p = *(const float2 *)(rb + (v2 * R + (ni >> 4)) * 256 + column_of<N8>(row) * 16 + (ni & 15));
                 v.x += p.x;
                 v.y += p.y;
             }

@@ -48,4 +48,14 @@ struct LayerArgs {
 __host__ __device__ inline int layer_rows_cap(int T, int k, int E_local) { return T * (k < E_local ? k : E_local); }
 __host__ __device__ inline int layer_hits_cap(int T, int k, int E_local) { return E_local < T * k ? E_local : T * k; }
 
+// Bytes of a row of h and where its second part starts (8-bit weights: the first one holds whole blocks of 128).
+__host__ __device__ inline uint32_t layer_h_rest(bool q8, int F)
+{
+    return 2 * (q8 ? (uint32_t)(F + kQ8Group - 1) / kQ8Group * kQ8Group : (uint32_t)F);
+}
+__host__ __device__ inline uint32_t layer_h_row_bytes(bool q8, int F)
+{
+    return layer_h_rest(q8, F) + (q8 ? (uint32_t)F : 2 * (uint32_t)F);
+}
+
 }  // namespace mk
