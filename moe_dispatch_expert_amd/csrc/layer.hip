@@ -15,9 +15,18 @@
 //     all on their way before it multiplies (two workgroups of four waves per CU
 //     stream the weights as fast as four of them, with a quarter of the
 //     instructions' register pressure).
-// Launches: the router and the selection (unless the caller routed), "up", which
-// writes h = w * silu(g) * u, "down", which writes W_down[e] . h per row in fp32, and "sum", which adds each
+// Launches: the router and the selection (unless the caller routed; for a few
+// tokens the up kernel selects by itself), "up", which writes h = w * silu(g) * u,
+// "down", which writes W_down[e] . h per row in fp32, and "sum", which adds each
 // token's rows in expert order.
+//
+// Bound by memory; a kernel that only reads reaches 7.0 - 7.1 TB/s here.  Kernel times, bf16 / e4m3:
+//   128 tokens, 32 of 256 experts, d = 7168, F = 2048:   router 18.5, selection 4.7, up 275 - 289 / 144 - 149 (6.5 - 6.8 TB/s
+//                                                        / 6.3 - 6.5), down 142 - 148 / 79 - 82, sum 4.8 us
+//   1 token, 2 of 8 experts, d = 4096, F = 14336, bf16:  router 5.8, up 73 (6.4 TB/s), down 37.5 (6.3), sum 4.6 us
+//   128 tokens, 2 of 8 experts, same sizes (32 rows each): up 340 - 352 / 210, down 220 / 172 us
+// With 32 rows an expert the tokens' and h's loads weigh as much as the weights', and a wave's loads and products no
+// longer overlap as well.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -336,6 +345,11 @@ __device__ __forceinline__ u32x4_t fp8_to_bf16(uint32_t lo, uint32_t hi)
 }
 
 // ---------------------------------------------------------------- gate|up
+//
+// A workgroup takes tasks of (expert, 8 to 32 features) in a fixed stride: tickets from an atomic counter measured slower
+// (309 -> 320 us at 128 tokens), and so did each XCD working on experts of its own where their row counts differ (128 tokens
+// at 64 experts with a skewed router: up 72 -> 141 us), without a gain where they do not.  Its four waves split K, so that
+// a slab of 16 weight rows by 1/4 of K is one wave's, and their sums meet once per task in LDS.
 
 template <int N>
 struct IntC {
@@ -647,7 +661,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     constexpr int KS = Q8 ? kQ8Group : 64;       // K per step
     constexpr int KP = Q8 ? 16 : 8;              // K per 16-byte piece of a weight row
     constexpr int kBytes = Q8 ? 1 : 2;
-    constexpr int NS = N8 < 4 ? N8 : 4, NST = (NS + 1) / 2;   // row groups (tiles) whose h is in registers at a time
+    constexpr int NS = N8 == 6 ? 2 : N8 < 4 ? N8 : 4, NST = (NS + 1) / 2;   // row groups (tiles) whose h is in registers at a time
     constexpr int HL = Q8 ? 3 : 2;               // 128-byte lines of an h row per step: the bf16 part's, then the rest's
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -767,7 +781,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
         }
         s += U;
     };
-    constexpr int U = R == 1 && N8 == 1 ? 4 : N8 >= (Q8 && R == 4 ? 2 : Q8 ? 4 : 8) ? 1 : 2;   // 256 registers
+    constexpr int U = R == 1 && N8 == 1 ? 4 : N8 >= (Q8 && R == 4 ? 2 : Q8 ? 4 : 6) ? 1 : 2;   // 256 registers
     while (s + U <= s1) run(IntC<U>());
     while (s < s1) run(IntC<1>());
     // the waves' parts meet in LDS as in up_task; two neighbouring columns a thread
@@ -821,6 +835,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
                 if (m <= 8) down_task<Q8, R, 1, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else if (m <= 16) down_task<Q8, R, 2, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else if (m <= 32) down_task<Q8, R, 4, TAIL>(a, e, n0, row0 + r, m, red, par);
+                else if (!Q8 && m <= 48)   // 256 choices over 8 experts, 14336 features: 220 us, without this form 246
+                    down_task<Q8, R, Q8 ? 8 : 6, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else   // four e4m3 tiles by four token tiles would not fit the registers
                     for (int i = 0; i < (Q8 ? R / 2 : 1); ++i)
                         down_task<Q8, Q8 ? 2 : R, 8, TAIL>(a, e, n0 + 32 * i, row0 + r, m, red, par);
@@ -834,7 +850,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
 // The smallest of the lanes' row numbers, -1 (none) counting as the largest.
 __device__ __forceinline__ uint32_t wave_min_row(int v) { return ~wave_max_u32(~(uint32_t)v); }
 
-// out[t] = sum of the token's rows of y in expert order.  A workgroup takes 1024 columns of a token.
+// out[t] = sum of the token's rows of y in expert order.  A workgroup takes 1024 columns of a token.  4.6 us after the
+// weights' stream (1.6 with y and the code still in the caches): the launch and two dependent fetches.
 __global__ __launch_bounds__(256) void k_layer_sum(LayerArgs a)
 {
     const int nc = (a.d + 1023) / 1024;
@@ -869,7 +886,8 @@ __global__ __launch_bounds__(256) void k_layer_sum(LayerArgs a)
 
 // ---------------------------------------------------------------- router of up to kLayerSelfT tokens
 
-// Partial sums part[s][t][e] in the library's order (one ascending fma chain per K segment), on the vector units: with
+// Partial sums part[s][t][e] in the library's order (one ascending fma chain per K segment), on the vector units (d = 4096,
+// E = 8: 5.8 us; the matrix units' router 10.5, whose dependent products follow each other in 48 cycles).  With
 // a few tokens the chains are few, and the time goes into fetching W_r and into the length of a chain.  A workgroup takes
 // (segment s, up to 16 experts): its weights are fetched at once into LDS (a segment of d = 7168: 56 KiB), then every
 // lane runs one chain (16 experts x 4 tokens a wave, 8 x 8 where there are no more than 8 experts), its operands read 8

@@ -38,7 +38,7 @@ def test_selection_switches(T, k, E, q8):
 # shapes whose tasks take one or two, and four weight tiles: few columns, many features, many columns
 @pytest.mark.parametrize("q8", [False, True])
 @pytest.mark.parametrize("d,F", [(256, 48), (128, 16384), (32768, 80)])
-@pytest.mark.parametrize("rows", [(1, 128), (8, 9), (16, 17), (32, 33), (64, 65), (31, 127)])
+@pytest.mark.parametrize("rows", [(1, 128), (8, 9), (16, 17), (32, 33), (41, 48), (49, 56), (64, 65), (31, 127)])
 def test_rows_of_an_expert(d, F, rows, q8):
     """Two experts with the given numbers of rows, on the last tokens and on the first."""
     c = Case(128, d, 4, 2, 4, F, q8=q8)
