@@ -21,8 +21,8 @@
 // token's rows in expert order.
 //
 // Bound by memory; a kernel that only reads reaches 7.0 - 7.1 TB/s here.  Kernel times, bf16 / e4m3:
-//   128 tokens, 32 of 256 experts, d = 7168, F = 2048:   router 18.5, selection 4.7, up 275 - 289 / 144 - 149 (6.5 - 6.8 TB/s
-//                                                        / 6.3 - 6.5), down 142 - 148 / 79 - 82, sum 4.8 us
+//   128 tokens, 32 of 256 experts, d = 7168, F = 2048:   router 18.5, selection 4.7, up 275 - 289 / 144 - 149
+//                                                        (6.5 - 6.8 / 6.3 - 6.5 TB/s), down 142 - 148 / 79 - 82, sum 4.8 us
 //   1 token, 2 of 8 experts, d = 4096, F = 14336, bf16:  router 5.8, up 73 (6.4 TB/s), down 37.5 (6.3), sum 4.6 us
 //   128 tokens, 2 of 8 experts, same sizes (32 rows each): up 340 - 352 / 210, down 220 / 172 us
 // With 32 rows an expert the tokens' and h's loads weigh as much as the weights', and a wave's loads and products no
@@ -356,18 +356,18 @@ struct IntC {
     static constexpr int value = N;
 };
 
-// Weight tiles per task.  More of them share one load of the tokens' rows, whose traffic out of the L2 costs as much as
-// that of the weights out of memory once an expert has 16 rows or more; fewer make more tasks, which come out more even.
-// n1: tasks per expert at one tile.  Four tiles where the workgroups get at least four tasks each or come out nearly even
-// (8 experts x 64 columns, 32 rows each: down 234 -> 199 us); one tile (built for 16 tokens at most) where two would not
-// give every workgroup `few` (7 experts of 2048 features, one tile against two: up 57 against 61 us, few = 2; down of 46
-// experts x 2048 columns: 22 against 19 us, few = 1).
+// Weight tiles per task.  More of them share one load of the tokens' rows, which cost as much as the weights once an
+// expert has 16 rows or more; fewer make more tasks, which come out more even.  n1: tasks per expert at one tile.  Four
+// tiles where the workgroups get at least four tasks each or come out nearly even (8 experts of 32 rows: up 352 us, with
+// two tiles 405).  One tile (built for 16 tokens at most) where that gives a workgroup `few` tasks or fewer: up, few = 4
+// (1 expert of 2048 features, d = 7168: 15 us, with two tiles 23), and down, whose tasks are shorter, few = 1 (6 experts
+// of e4m3, d = 2048, twice as many tasks as workgroups: 8.4 us, with two tiles 7.0).
 __device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workgroups, int few)
 {
-    const long t2 = (long)hits * ((n1 + 1) / 2), t4 = (long)hits * ((n1 + 3) / 4);
+    const long t4 = (long)hits * ((n1 + 3) / 4);
     const long rounds = (t4 + workgroups - 1) / workgroups;
     if (t4 >= 4L * workgroups || (t4 > 0 && 10 * t4 >= 9 * rounds * workgroups)) return 4;
-    return t2 < few * workgroups && T <= 16 ? 1 : 2;
+    return (long)hits * n1 <= (long)few * workgroups && T <= 16 ? 1 : 2;
 }
 
 // h is kept in two parts, so that its rounding does not show beside the output's own (one bf16 part alone made the
@@ -444,7 +444,8 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
         xo[n] = s.tok[row0 + min(token_of<N8>(n, c), cnt - 1)] * pitch + piece;
     // 8-bit form: the scales of its column's token (a step is a block)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) so[n] = Q8 ? s.tok[row0 + min(N8 == 1 ? c >> 1 : 16 * n + c, cnt - 1)] * (uint32_t)steps * 4 : 0;
+    for (int n = 0; n < NT; ++n)
+        so[n] = Q8 ? s.tok[row0 + min(N8 == 1 ? c >> 1 : 16 * n + c, cnt - 1)] * (uint32_t)steps * 4 : 0;
     f32x4_t acc[R][NT];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -614,7 +615,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
         build_rows(s, a, T, blockIdx.x == 0);
     }
     const int hits = s.n[0];
-    const int tiles = tiles_per_task(hits, (a.F + 7) / 8, a.T, (int)gridDim.x, 2);
+    const int tiles = tiles_per_task(hits, (a.F + 7) / 8, a.T, (int)gridDim.x, 4);
     const int fs = 8 * tiles;
     const int nf = (a.F + fs - 1) / fs;
     int par = 0;
@@ -652,8 +653,8 @@ constexpr int kDownRedBytes = 2 * kDownWaves * 4 * 256 * 4;
 
 // One down task: output columns n0 .. n0 + 16 R - 1 of expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8), written
 // to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3, which
-// meets h's bf16 part converted to bf16 (exact) and h's rest as it is, and is scaled per step.  TAIL: F does not end on a step; pieces past
-// F are zeros on both sides.  red, par: as in up_task.
+// converted to bf16 (exact) meets h's bf16 part, and as it is h's rest, and is scaled per step.  TAIL: F does not end on a
+// step; pieces past F are zeros on both sides.  red, par: as in up_task.
 template <bool Q8, int R, int N8, bool TAIL>
 __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int row0, int cnt, float *red, int &par)
 {
@@ -661,7 +662,8 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     constexpr int KS = Q8 ? kQ8Group : 64;       // K per step
     constexpr int KP = Q8 ? 16 : 8;              // K per 16-byte piece of a weight row
     constexpr int kBytes = Q8 ? 1 : 2;
-    constexpr int NS = N8 == 6 ? 2 : N8 < 4 ? N8 : 4, NST = (NS + 1) / 2;   // row groups (tiles) whose h is in registers at a time
+    // row groups (tiles) whose h is in registers at a time
+    constexpr int NS = N8 == 6 ? 2 : N8 < 4 ? N8 : 4, NST = (NS + 1) / 2;
     constexpr int HL = Q8 ? 3 : 2;               // 128-byte lines of an h row per step: the bf16 part's, then the rest's
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
@@ -1018,7 +1020,8 @@ hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s)
 {
     const int cus = device_cus();
     if (cus <= 0) return hipErrorInvalidDevice;
-    const long most = (long)layer_hits_cap(a.T, a.k, a.E_local) * ((a.F + 7) / 8);   // tasks, if every choice is another local expert
+    // tasks, if every choice is another local expert
+    const long most = (long)layer_hits_cap(a.T, a.k, a.E_local) * ((a.F + 7) / 8);
     const int grid = (int)std::min<long>(most, 2L * cus);
     const hipError_t e = q8 ? launch_up<true>(a, self, grid, s) : launch_up<false>(a, self, grid, s);
     if (e != hipSuccess) return e;
