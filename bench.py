@@ -341,6 +341,80 @@ def time_ffn(case, R: int, steps: int, warmup: int, ms_step: float) -> dict:
                      "TFLOP/s": tf(down_flops, ms_down), "frac": round(tf(down_flops, ms_down) / PEAK_BF16_TFLOPS, 4)}}
 
 
+def _blocks_e4m3(w):
+    """e4m3 codes and fp32 scales of matrices [E, R, C], one scale per 128 x 128 block (the last ones may be smaller)."""
+    import torch
+    E, R, C = w.shape
+    nr, nc = -(-R // 128), -(-C // 128)
+    q = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device)
+    s = torch.empty(E, nr, nc, device=w.device)
+    for e in range(E):
+        b = torch.nn.functional.pad(w[e].float(), (0, nc * 128 - C, 0, nr * 128 - R)).view(nr, 128, nc, 128)
+        s[e] = b.abs().amax(dim=(1, 3)).clamp_min(2.0 ** -40) / 448.0
+        q[e] = (b / s[e][:, None, :, None]).view(nr * 128, nc * 128)[:R, :C].to(q.dtype)
+    return q, s
+
+
+def time_layer(case, steps: int, warmup: int) -> dict:
+    """A decode step's MoE layer on the workload's first min(T, 128) tokens, its expert weights read as [gate | up]
+    (F = N / 2), routed inside the call, each part timed K times between two events on the current stream:
+      norm       mk_add_rmsnorm of the tokens (residual added; bf16 and e4m3 outputs)
+      bf16       mk_moe_layer
+      e4m3       mk_moe_layer_q8 on the norm's 8-bit output, weights in 128 x 128 blocks
+    alg_bytes: the weights of the experts hit, read once."""
+    import torch
+    import moe_dispatch_expert_amd as mk
+    wl = case.wl
+    F = wl.N // 2
+    if wl.N % 32:
+        return {"skipped": f"F = N / 2 = {wl.N / 2} is not a multiple of 16"}
+    x = (case.xs[0] if isinstance(case.xs, list) else case.xs)[:128].contiguous()
+    T = x.shape[0]
+    g = torch.Generator(device=x.device).manual_seed(case.seed * 1000 + 6)
+    gu = case.we
+    dn = torch.empty(wl.E_local, wl.d, F, dtype=torch.bfloat16, device=x.device)
+    for e in range(wl.E_local):
+        dn[e] = torch.randn(wl.d, F, generator=g, device=x.device) / F ** 0.5
+    (gq, gs), (uq, us), (dnq, dns) = _blocks_e4m3(gu[:, :F]), _blocks_e4m3(gu[:, F:]), _blocks_e4m3(dn)
+    guq = torch.cat([gq.view(torch.uint8), uq.view(torch.uint8)], 1).view(gq.dtype)   # gate rows, then up rows
+    gus = torch.cat([gs, us], 1)
+    gamma = torch.ones(wl.d, dtype=torch.bfloat16, device=x.device)
+    res = torch.randn(T, wl.d, generator=g, device=x.device).to(torch.bfloat16)
+    ws = torch.empty(mk.mk_moe_layer_workspace_bytes(T, wl.d, wl.E, wl.k, wl.e_begin, wl.E_local, F),
+                     dtype=torch.uint8, device=x.device)
+    n = mk.mk_add_rmsnorm(x, gamma, res, bf16=True, q8=True)
+    out = {"topk_ids": torch.empty(T, wl.k, dtype=torch.int32, device=x.device)}
+    kw = dict(w_router=case.wr, bias=case.bias, e_begin=wl.e_begin, workspace=ws)
+    mk.mk_moe_layer(n["y"], gu, dn, wl.k, out=out, **kw)
+    ids = out["topk_ids"]
+    hit = int(torch.unique(ids[(ids >= wl.e_begin) & (ids < wl.e_begin + wl.E_local)]).numel())
+
+    def timed(fn):
+        for _ in range(warmup):
+            fn()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        for _ in range(steps):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / steps
+
+    def entry(ms, alg):
+        gbs = alg / (ms * 1e-3) / 1e9
+        return {"ms": round(ms, 4), "alg_bytes": alg, "achieved": round(gbs, 1), "unit": "GB/s",
+                "frac": round(gbs / PEAK_HBM_GBS, 4)}
+
+    weights = hit * 3 * F * wl.d
+    return {"T": T, "F": F, "experts_hit": hit,
+            "norm": entry(timed(lambda: mk.mk_add_rmsnorm(x, gamma, res, bf16=True, q8=True)),
+                          T * wl.d * 9 + T * wl.d // 32),
+            "bf16": entry(timed(lambda: mk.mk_moe_layer(n["y"], gu, dn, wl.k, **kw)), 2 * weights),
+            "e4m3": entry(timed(lambda: mk.mk_moe_layer_q8(n["q8"], n["q8_scale"], guq, gus, dnq, dns, wl.k, x=n["y"],
+                                                           **kw)), weights)}
+
+
 def cpu_baseline(inp, R_gpu: int, budget_s: float = 12.0) -> dict:
     import oracle
     wl = inp["wl"]
@@ -594,6 +668,9 @@ def main():
                     help="also time the expert FFN over the step's layout (the expert weights read as [gate | up], "
                          "F = N / 2): mk_dispatch_gemm_swiglu, mk_swiglu, and the down-projection mk_grouped_gemm "
                          "(reported apart, not in value)")
+    ap.add_argument("--layer", action="store_true",
+                    help="also time the few-token MoE layer on the workload's first 128 tokens: mk_add_rmsnorm, "
+                         "mk_moe_layer, mk_moe_layer_q8 (reported apart, not in value)")
     ap.add_argument("--library-gemm", action="store_true",
                     help="only time the dense library GEMM (torch linear) of the workload's expert shape and exit")
     ap.add_argument("--combine", action="store_true",
@@ -671,6 +748,8 @@ def main():
         rec["combine"] = time_combine(case.bufs, R, args.steps, args.warmup)
     if args.ffn:
         rec["ffn"] = time_ffn(case, R, args.steps, args.warmup, ms_step)
+    if args.layer:
+        rec["layer"] = time_layer(case, args.steps, args.warmup)
     if not args.no_cpu_baseline:
         rec["cpu_baseline"] = cpu_baseline(case.inp, R)
         rec["cpu_baseline"]["value"] = round(rec["cpu_baseline"]["value"], 6)
