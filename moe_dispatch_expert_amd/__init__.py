@@ -7,7 +7,9 @@ require CUDA (HIP) tensors.
 
 Names follow the C ABI: mk_route_topk, mk_dispatch_gemm,
 mk_dispatch_gemm_workspace_bytes, mk_route_topk_workspace_bytes,
-mk_select_tuning, mk_poll_error, mk_status_str.
+mk_select_tuning, mk_poll_error, mk_status_str; for a serving step of a few
+tokens mk_add_rmsnorm, mk_moe_layer, mk_moe_layer_q8,
+mk_moe_layer_workspace_bytes.
 """
 from __future__ import annotations
 
