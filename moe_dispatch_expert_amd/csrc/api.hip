@@ -485,7 +485,7 @@ void *g_scratch_dev[kMaxDevices];
 // Workspace: the plan, router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] in two
 // parts of at most 2 bytes and y [T min(k, E_local), d] fp32.
 struct LayerWs {
-    size_t rec, row_of, part, ids, w, h, y, total;
+    size_t rec, row_of, done, part, ids, w, h, y, total;
 };
 
 LayerWs layer_ws(const mk_shape *s)
@@ -494,7 +494,8 @@ LayerWs layer_ws(const mk_shape *s)
     LayerWs L;
     L.rec = 256;
     L.row_of = L.rec + align256(std::min<size_t>(tk, 1024) * sizeof(LayerRec));   // E_local <= 1024
-    L.part = L.row_of + align256(tk * 4);
+    L.done = L.row_of + align256(tk * 4);
+    L.part = L.done + align256((size_t)s->d / 16 * 4);
     L.ids = L.part + align256((size_t)kRouterSegments * s->T * s->E * 4);
     L.w = L.ids + align256(tk * 4);
     L.h = L.w + align256(tk * 4);
@@ -555,6 +556,7 @@ mk_status layer_impl(const mk_shape *s, bool q8, const void *x, const void *x_q8
     a.plan.n = (int32_t *)ws;
     a.plan.rec = (LayerRec *)(ws + L.rec);
     a.plan.row_of = (int32_t *)(ws + L.row_of);
+    a.plan.done = (int32_t *)(ws + L.done);
     a.h = ws + L.h;
     a.y = (float *)(ws + L.y);
     a.out = (uint16_t *)out;

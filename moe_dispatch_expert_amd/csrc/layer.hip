@@ -608,6 +608,8 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
             if (a.ids_user) a.ids_user[i] = s.ids[i];
             if (a.w_user) a.w_user[i] = s.w[i];
         }
+    if (a.T <= kLayerSelfT && blockIdx.x == 0)
+        for (int i = threadIdx.x; i < a.d / 16; i += blockDim.x) a.plan.done[i] = 0;
     if (a.T * a.k <= kFewChoices) {
         if (threadIdx.x < kWave) build_few_rows(s, a, T, blockIdx.x == 0);
         __syncthreads();
@@ -655,7 +657,7 @@ constexpr int kDownRedBytes = 2 * kDownWaves * 4 * 256 * 4;
 // to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3, which
 // converted to bf16 (exact) meets h's bf16 part, and as it is h's rest, and is scaled per step.  TAIL: F does not end on a
 // step; pieces past F are zeros on both sides.  red, par: as in up_task.
-template <bool Q8, int R, int N8, bool TAIL>
+template <bool Q8, int R, int N8, bool TAIL, bool SUM = false>
 __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int row0, int cnt, float *red, int &par)
 {
     constexpr int NT = (N8 + 1) / 2;             // 16-column tiles
@@ -804,19 +806,81 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
                 v.x += p.x;
                 v.y += p.y;
             }
-            *(float2 *)(a.y + (size_t)(row0 + row) * a.d + n0 + ni) = v;
+            float *to = a.y + (size_t)(row0 + row) * a.d + n0 + ni;
+            if constexpr (SUM) store_through((uint64_t *)to, __builtin_bit_cast(uint64_t, v));   // another XCD may add it
+            else *(float2 *)to = v;
         }
     }
 }
 
-template <bool Q8, bool TAIL>
+// Columns n0 .. n0 + nb - 1 of every token's output: the sum of its rows of y in expert order (nb even, T nb <= 2 x 256).
+// mine: this thread's choice's row (T k <= 256); sorted: LDS, 256.
+__device__ __forceinline__ void sum_columns(const LayerArgs &a, int valid, int n0, int nb, int mine, int *sorted)
+{
+    // a row's place among its token's is the number of smaller ones
+    const int i = threadIdx.x, t0 = i / a.k * a.k;
+    sorted[i] = mine;
+    __syncthreads();
+    int place = 0, rows = 0;
+    if (i < a.T * a.k)
+        for (int j = t0; j < t0 + a.k; ++j) {
+            const int r = sorted[j];
+            place += r >= 0 && r < mine;
+            rows += r >= 0;
+        }
+    __syncthreads();
+    if (i < a.T * a.k) {
+        if (mine >= 0) sorted[t0 + place] = mine;
+        if (i - t0 >= rows) sorted[i] = -1;
+    }
+    __syncthreads();
+    const int t = 2 * i / nb, col = n0 + 2 * i % nb;
+    if (t < valid) {
+        float2 v = make_float2(0.0f, 0.0f);
+        bool more = true;
+        for (int j = t * a.k; more && j < (t + 1) * a.k; j += 4) {   // four rows on their way at a time
+            uint64_t p[4];
+            int r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                r[u] = j + u < (t + 1) * a.k ? sorted[j + u] : -1;
+                // past the caches that may hold older values of a line another XCD has written to
+                p[u] = __hip_atomic_load((const uint64_t *)(a.y + (size_t)max(r[u], 0) * a.d + col), __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float2 f = __builtin_bit_cast(float2, p[u]);
+                if (r[u] >= 0) {
+                    v.x += f.x;
+                    v.y += f.y;
+                }
+            }
+            more = r[3] >= 0;
+        }
+        *(uint32_t *)(a.out + (size_t)t * a.d + col) = (uint32_t)f32_to_bf16(v.x) | (uint32_t)f32_to_bf16(v.y) << 16;
+    }
+    __syncthreads();   // sorted is the next call's
+}
+
+// SUM (at most kLayerSelfT tokens): the workgroup that finishes a column block's last task adds the block's rows up, which
+// saves the sum kernel's launch.
+template <bool Q8, bool TAIL, bool SUM>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
 {
     __shared__ __attribute__((aligned(16))) char lds[kDownRedBytes];
+    __shared__ int sorted[SUM ? 64 * kDownWaves : 1], last;
     float *red = (float *)lds;
+    const int mine = SUM && (int)threadIdx.x < a.T * a.k ? a.plan.row_of[threadIdx.x] : -1;
+    const int valid = SUM ? a.plan.n[1] : 0;
     const int hits = a.plan.n[0];
     const int tiles = tiles_per_task(hits, a.d / 16, a.T, (int)gridDim.x, 1);
     const int nc = a.d / (16 * tiles);   // d % 128 == 0
+    if (SUM && hits == 0) {
+        for (int q = blockIdx.x; q < nc; q += gridDim.x)
+            sum_columns(a, valid, q * 16 * tiles, 16 * tiles, mine, sorted);
+        return;
+    }
     int par = 0;
     for (int q = blockIdx.x; q < hits * nc; q += gridDim.x) {
         const int hi = q / nc, n0 = (q - hi * nc) * 16 * tiles;
@@ -824,6 +888,19 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
         const int e = __builtin_amdgcn_readfirstlane(rec.e);
         const int row0 = __builtin_amdgcn_readfirstlane(rec.row0);
         const int cnt = __builtin_amdgcn_readfirstlane(rec.cnt);
+        if constexpr (SUM) {
+            if (tiles == 1) down_task<Q8, 1, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
+            else if (tiles == 2) down_task<Q8, 2, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
+            else down_task<Q8, 4, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every wave's part of y is in memory
+            __syncthreads();
+            if (threadIdx.x == 0)
+                last = __hip_atomic_fetch_add(a.plan.done + n0 / (16 * tiles), 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT) == hits - 1;
+            __syncthreads();
+            if (last) sum_columns(a, valid, n0, 16 * tiles, mine, sorted);
+            continue;
+        }
         if (tiles == 1) {
             if (cnt <= 8) down_task<Q8, 1, 1, TAIL>(a, e, n0, row0, cnt, red, par);
             else down_task<Q8, 1, 2, TAIL>(a, e, n0, row0, cnt, red, par);
@@ -1009,6 +1086,13 @@ hipError_t launch_up(const LayerArgs &a, bool self, int grid, hipStream_t s)
     return hipGetLastError();
 }
 
+template <bool Q8, bool TAIL>
+void launch_down(const LayerArgs &a, bool sum, int grid, hipStream_t s)
+{
+    if (sum) hipLaunchKernelGGL((k_layer_down<Q8, TAIL, true>), dim3(grid), dim3(64 * kDownWaves), 0, s, a);
+    else hipLaunchKernelGGL((k_layer_down<Q8, TAIL, false>), dim3(grid), dim3(64 * kDownWaves), 0, s, a);
+}
+
 }  // namespace
 
 hipError_t launch_layer_router(const LayerArgs &a, hipStream_t s)
@@ -1027,13 +1111,13 @@ hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s)
     if (e != hipSuccess) return e;
     const bool tail = a.F % (q8 ? kQ8Group : 64) != 0;
     const int gd = (int)std::min<long>((long)layer_hits_cap(a.T, a.k, a.E_local) * (a.d / 16), 2L * cus);
-    const dim3 block(64 * kDownWaves);
-    if (q8 && tail) hipLaunchKernelGGL((k_layer_down<true, true>), dim3(gd), block, 0, s, a);
-    else if (q8) hipLaunchKernelGGL((k_layer_down<true, false>), dim3(gd), block, 0, s, a);
-    else if (tail) hipLaunchKernelGGL((k_layer_down<false, true>), dim3(gd), block, 0, s, a);
-    else hipLaunchKernelGGL((k_layer_down<false, false>), dim3(gd), block, 0, s, a);
+    const bool sum = a.T <= kLayerSelfT;
+    if (q8 && tail) launch_down<true, true>(a, sum, gd, s);
+    else if (q8) launch_down<true, false>(a, sum, gd, s);
+    else if (tail) launch_down<false, true>(a, sum, gd, s);
+    else launch_down<false, false>(a, sum, gd, s);
     const hipError_t e2 = hipGetLastError();
-    if (e2 != hipSuccess) return e2;
+    if (e2 != hipSuccess || sum) return e2;
     hipLaunchKernelGGL(k_layer_sum, dim3(a.T * ((a.d + 1023) / 1024)), dim3(256), 0, s, a);
     return hipGetLastError();
 }

@@ -9,7 +9,8 @@
 namespace mk {
 
 constexpr int kLayerMaxT = 128;      // tokens per call (two 64-bit token masks per expert)
-constexpr int kLayerSelfT = 8;       // tokens up to which the vector router runs and the up kernel selects by itself
+constexpr int kLayerSelfT = 8;       // tokens up to which the vector router runs, the up kernel selects by itself and the
+                                     // down kernel adds the rows up
 constexpr int kLayerSelfE = 256;     // ... and experts, for the selection
 constexpr int kQ8Group = 128;        // columns (and rows of weights) per scale
 
@@ -22,6 +23,7 @@ struct LayerPlan {
     int32_t *n;                      // [2] experts with tokens, valid tokens
     LayerRec *rec;                   // [min(E_local, T k)]
     int32_t *row_of;                 // [T, k] row of the choice in h and y, or -1
+    int32_t *done;                   // [d / 16] finished down tasks of each column block, zeroed (T <= kLayerSelfT)
 };
 
 struct LayerArgs {
