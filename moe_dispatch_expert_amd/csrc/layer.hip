@@ -17,13 +17,13 @@
 //     instructions' register pressure).
 // Launches: the router and the selection (unless the caller routed; for a few
 // tokens the up kernel selects by itself), "up", which writes h = w * silu(g) * u,
-// "down", which writes W_down[e] . h per row in fp32, and "sum", which adds each
-// token's rows in expert order.
+// "down", which writes W_down[e] . h per row in fp32 and for few tokens adds each
+// token's rows up in expert order, and "sum", which does that for more.
 //
 // Bound by memory; a kernel that only reads reaches 7.0 - 7.1 TB/s here.  Kernel times, bf16 / e4m3:
 //   128 tokens, 32 of 256 experts, d = 7168, F = 2048:   router 18.5, selection 4.7, up 275 - 289 / 144 - 149
 //                                                        (6.5 - 6.8 / 6.3 - 6.5 TB/s), down 142 - 148 / 79 - 82, sum 4.8 us
-//   1 token, 2 of 8 experts, d = 4096, F = 14336, bf16:  router 5.8, up 73 (6.4 TB/s), down 37.5 (6.3), sum 4.6 us
+//   1 token, 2 of 8 experts, d = 4096, F = 14336, bf16:  router 5.8, up 73 (6.4 TB/s), down with the sum 39 us
 //   128 tokens, 2 of 8 experts, same sizes (32 rows each): up 340 - 352 / 210, down 220 / 172 us
 // With 32 rows an expert the tokens' and h's loads weigh as much as the weights', and a wave's loads and products no
 // longer overlap as well.
@@ -608,7 +608,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
             if (a.ids_user) a.ids_user[i] = s.ids[i];
             if (a.w_user) a.w_user[i] = s.w[i];
         }
-    if (a.T <= kLayerSelfT && blockIdx.x == 0)
+    if (layer_sums_in_down(a.T, a.k) && blockIdx.x == 0)
         for (int i = threadIdx.x; i < a.d / 16; i += blockDim.x) a.plan.done[i] = 0;
     if (a.T * a.k <= kFewChoices) {
         if (threadIdx.x < kWave) build_few_rows(s, a, T, blockIdx.x == 0);
@@ -813,7 +813,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     }
 }
 
-// Columns n0 .. n0 + nb - 1 of every token's output: the sum of its rows of y in expert order (nb even, T nb <= 2 x 256).
+// Columns n0 .. n0 + nb - 1 of every valid token's output: the sum of its rows of y in expert order (nb even).
 // mine: this thread's choice's row (T k <= 256); sorted: LDS, 256.
 __device__ __forceinline__ void sum_columns(const LayerArgs &a, int valid, int n0, int nb, int mine, int *sorted)
 {
@@ -834,8 +834,8 @@ __device__ __forceinline__ void sum_columns(const LayerArgs &a, int valid, int n
         if (i - t0 >= rows) sorted[i] = -1;
     }
     __syncthreads();
-    const int t = 2 * i / nb, col = n0 + 2 * i % nb;
-    if (t < valid) {
+    for (int q = i; 2 * q < valid * nb; q += 64 * kDownWaves) {
+        const int t = 2 * q / nb, col = n0 + 2 * q % nb;
         float2 v = make_float2(0.0f, 0.0f);
         bool more = true;
         for (int j = t * a.k; more && j < (t + 1) * a.k; j += 4) {   // four rows on their way at a time
@@ -863,7 +863,7 @@ __device__ __forceinline__ void sum_columns(const LayerArgs &a, int valid, int n
     __syncthreads();   // sorted is the next call's
 }
 
-// SUM (at most kLayerSelfT tokens): the workgroup that finishes a column block's last task adds the block's rows up, which
+// SUM (layer_sums_in_down): the workgroup that finishes a column block's last task adds the block's rows up, which
 // saves the sum kernel's launch.
 template <bool Q8, bool TAIL, bool SUM>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
@@ -889,9 +889,14 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
         const int row0 = __builtin_amdgcn_readfirstlane(rec.row0);
         const int cnt = __builtin_amdgcn_readfirstlane(rec.cnt);
         if constexpr (SUM) {
-            if (tiles == 1) down_task<Q8, 1, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
-            else if (tiles == 2) down_task<Q8, 2, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
-            else down_task<Q8, 4, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
+            auto rows = [&](auto tc) {
+                constexpr int R = decltype(tc)::value;
+                if (cnt <= 8) down_task<Q8, R, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
+                else down_task<Q8, R, 2, TAIL, true>(a, e, n0, row0, cnt, red, par);
+            };
+            if (tiles == 1) rows(IntC<1>());
+            else if (tiles == 2) rows(IntC<2>());
+            else rows(IntC<4>());
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every wave's part of y is in memory
             __syncthreads();
             if (threadIdx.x == 0)
@@ -1111,7 +1116,7 @@ hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s)
     if (e != hipSuccess) return e;
     const bool tail = a.F % (q8 ? kQ8Group : 64) != 0;
     const int gd = (int)std::min<long>((long)layer_hits_cap(a.T, a.k, a.E_local) * (a.d / 16), 2L * cus);
-    const bool sum = a.T <= kLayerSelfT;
+    const bool sum = layer_sums_in_down(a.T, a.k);
     if (q8 && tail) launch_down<true, true>(a, sum, gd, s);
     else if (q8) launch_down<true, false>(a, sum, gd, s);
     else if (tail) launch_down<false, true>(a, sum, gd, s);
