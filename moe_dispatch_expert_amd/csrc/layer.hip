@@ -92,8 +92,6 @@ __device__ __forceinline__ int rank_of(const uint64_t *m, int t)
     return t < 64 ? __popcll(m[0] & ((1ull << t) - 1)) : __popcll(m[0]) + __popcll(m[1] & ((1ull << (t - 64)) - 1));
 }
 
-constexpr int kFewChoices = 32;
-
 // build_rows for a few choices, by one wave without the masks, a lane per choice: a row's number is the number of choices
 // that come before it by (expert, token).
 __device__ __forceinline__ void build_few_rows(const RowsLds &s, const LayerArgs &a, int T, bool publish)
@@ -814,7 +812,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
 }
 
 // Columns n0 .. n0 + nb - 1 of every valid token's output: the sum of its rows of y in expert order (nb even).
-// mine: this thread's choice's row (T k <= 256); sorted: LDS, 256.
+// mine: this thread's choice's row; sorted: LDS, one of each thread.
 __device__ __forceinline__ void sum_columns(const LayerArgs &a, int valid, int n0, int nb, int mine, int *sorted)
 {
     // a row's place among its token's is the number of smaller ones
@@ -869,7 +867,7 @@ template <bool Q8, bool TAIL, bool SUM>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
 {
     __shared__ __attribute__((aligned(16))) char lds[kDownRedBytes];
-    __shared__ int sorted[SUM ? 64 * kDownWaves : 1], last;
+    __shared__ int sorted[SUM ? 64 * kDownWaves : 1], last;   // T k <= 32 of sorted are choices
     float *red = (float *)lds;
     const int mine = SUM && (int)threadIdx.x < a.T * a.k ? a.plan.row_of[threadIdx.x] : -1;
     const int valid = SUM ? a.plan.n[1] : 0;
@@ -889,14 +887,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
         const int row0 = __builtin_amdgcn_readfirstlane(rec.row0);
         const int cnt = __builtin_amdgcn_readfirstlane(rec.cnt);
         if constexpr (SUM) {
-            auto rows = [&](auto tc) {
-                constexpr int R = decltype(tc)::value;
-                if (cnt <= 8) down_task<Q8, R, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
-                else down_task<Q8, R, 2, TAIL, true>(a, e, n0, row0, cnt, red, par);
-            };
-            if (tiles == 1) rows(IntC<1>());
-            else if (tiles == 2) rows(IntC<2>());
-            else rows(IntC<4>());
+            if (tiles == 1) down_task<Q8, 1, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
+            else if (tiles == 2) down_task<Q8, 2, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
+            else down_task<Q8, 4, 1, TAIL, true>(a, e, n0, row0, cnt, red, par);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // every wave's part of y is in memory
             __syncthreads();
             if (threadIdx.x == 0)

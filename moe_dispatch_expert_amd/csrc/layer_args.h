@@ -49,10 +49,12 @@ struct LayerArgs {
 __host__ __device__ inline int layer_rows_cap(int T, int k, int E_local) { return T * (k < E_local ? k : E_local); }
 __host__ __device__ inline int layer_hits_cap(int T, int k, int E_local) { return E_local < T * k ? E_local : T * k; }
 
-// Few tokens: the down kernel adds the rows up itself (13 tokens at 64 experts: 18.5 + 4.6 us in two kernels, 21.7 in one;
-// a Mixtral-shaped token: 37.5 + 4.6, 39).
-// Its workgroup of 256 threads holds a choice each.
-__host__ __device__ inline bool layer_sums_in_down(int T, int k) { return T <= 16 && T * k <= 256; }
+// A few choices: the down kernel adds the rows up itself, one launch fewer (whole calls back to back: one token at 6 experts
+// of e4m3 27.7 -> 26.5 us, a Mixtral-shaped token 120.1 -> 119.4, where the host is slower than the kernels 20 -> 17).  With
+// more the wait for other workgroups' rows costs as much or more (8 tokens, 64 choices: 92.2 -> 92.9, 16 tokens, 128
+// choices: 211.5 -> 214.5).
+constexpr int kFewChoices = 32;
+__host__ __device__ inline bool layer_sums_in_down(int T, int k) { return T <= kLayerSelfT && T * k <= kFewChoices; }
 
 // Bytes of a row of h and where its second part starts (8-bit weights: the first one holds whole blocks of 128).
 __host__ __device__ inline uint32_t layer_h_rest(bool q8, int F)

@@ -94,3 +94,48 @@ def test_choices_written_over_those_given(q8):
     else:
         got = mk.mk_moe_layer(G["x"], G["gu"], G["dn"], c.k, **kw)["out"]
     assert torch.equal(got, want) and torch.equal(di.cpu(), ids) and torch.equal(dg.cpu(), gates)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("T,k", [(1, 2), (2, 8), (8, 4)])
+def test_few_choices_replayed(T, k, q8):
+    """A captured call of a few choices, replayed with other choices, none at all, and fewer valid tokens, between eager
+    calls of its own workspace: every result is the eager one's, bit for bit."""
+    c = Case(T, 512, 16, k, 16, 80, q8=q8)
+    ids, gates = c.random_choices(1)
+    G = c.gpu
+    di, dg = ids.cuda(), gates.cuda()
+    valid = torch.tensor([T], dtype=torch.int32, device="cuda")
+    ws = torch.full((mk.mk_moe_layer_workspace_bytes(T, 512, 16, k, 0, 16, 80),), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.empty(T, 512, dtype=torch.bfloat16, device="cuda")
+
+    def call(dst, w):
+        kw = dict(topk_ids_in=di, topk_w_in=dg, E=16, t_valid=valid, workspace=w, out={"out": dst})
+        if q8:
+            mk.mk_moe_layer_q8(G["xq"], G["xs"], G["gq"], G["gs"], G["dq"], G["ds"], k, **kw)
+        else:
+            mk.mk_moe_layer(G["x"], G["gu"], G["dn"], k, **kw)
+
+    call(out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, ws)
+    for step in range(8):
+        new, _ = c.random_choices(10 + step)
+        if step % 4 == 2:
+            new.fill_(-1)
+        n = max(T - step % 3, 0)
+        di.copy_(new)
+        valid.fill_(n)
+        out.fill_(7.0)
+        eager = torch.full_like(out, 7.0)
+        graph.replay()
+        call(eager, None if step % 2 else ws)
+        graph.replay()
+        assert torch.equal(out, eager), step
+        assert (out[n:] == 7.0).all()
+        if step % 4 == 2:
+            assert (out[:n] == 0).all()
+        elif n:
+            c.check(out, torch.where(torch.arange(T)[:, None] < n, new, -1), gates, rows=slice(0, n))
