@@ -396,14 +396,13 @@ __device__ __forceinline__ void store_h(const LayerArgs &a, int row, int f, floa
         *(uint32_t *)(p + 2 * f) = (uint32_t)f32_to_bf16(r0) | (uint32_t)f32_to_bf16(r1) << 16;
 }
 
-constexpr int kUpWaves = 4;
-constexpr int kUpRedBytes = 2 * kUpWaves * 4 * 256 * 4;   // two halves of up_task's exchange
+constexpr int kUpWaves = kLayerWaves;
 
 // One gate|up task: features f0 .. f0 + 8 R - 1 of local expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8).
 // R = 1: one weight tile of 8 gate and 8 up rows; R = 2 or 4: R / 2 tiles of 16 gate rows, then as many of up rows.
 // The wave sums its share of K in steps of 128 bytes of a weight row (64 bf16, or one 128-wide block of e4m3, whose
 // product is scaled by the token's and the weights' scales before it joins the sum).
-// red: 2 x kUpWaves x R x 256 floats; par: which half the next exchange uses.
+// red: kExchangeBytes; par: which half the next exchange uses.
 template <bool Q8, int R, int N8>
 __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, int e, int f0, int row0, int cnt,
                                         float *red, int &par)
@@ -536,7 +535,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
     // added in wave order, and become h, two features a thread.  Halves alternate: one barrier per tile.
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float *rb = red + par * kUpWaves * R * 256;
+        float *rb = red + layer_exchange_at(par);
         par ^= 1;
 #pragma unroll
         for (int r = 0; r < R; ++r) *(f32x4_t *)(rb + (wave * R + r) * 256 + c * 16 + 4 * g) = acc[r][n];
@@ -568,7 +567,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
 {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     float *red = (float *)lds;
-    const RowsLds s = rows_lds(lds + kUpRedBytes, a);
+    const RowsLds s = rows_lds(lds + kExchangeBytes, a);
     const int T = valid_tokens(a);
     if constexpr (SELF) {
         const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -648,8 +647,7 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
 
 // ---------------------------------------------------------------- down
 
-constexpr int kDownWaves = 4;
-constexpr int kDownRedBytes = 2 * kDownWaves * 4 * 256 * 4;
+constexpr int kDownWaves = kLayerWaves;
 
 // One down task: output columns n0 .. n0 + 16 R - 1 of expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8), written
 // to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3, which
@@ -789,7 +787,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     // the waves' parts meet in LDS as in up_task; two neighbouring columns a thread
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float *rb = red + par * kDownWaves * R * 256;
+        float *rb = red + layer_exchange_at(par);
         par ^= 1;
 #pragma unroll
         for (int r = 0; r < R; ++r) *(f32x4_t *)(rb + (wave * R + r) * 256 + c * 16 + 4 * g) = acc[r][n];
@@ -866,7 +864,7 @@ __device__ __forceinline__ void sum_columns(const LayerArgs &a, int valid, int n
 template <bool Q8, bool TAIL, bool SUM>
 __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
 {
-    __shared__ __attribute__((aligned(16))) char lds[kDownRedBytes];
+    __shared__ __attribute__((aligned(16))) char lds[kExchangeBytes];
     __shared__ int sorted[SUM ? 64 * kDownWaves : 1], last;   // T k <= 32 of sorted are choices
     float *red = (float *)lds;
     const int mine = SUM && (int)threadIdx.x < a.T * a.k ? a.plan.row_of[threadIdx.x] : -1;
@@ -1078,7 +1076,7 @@ int device_cus()
 template <bool Q8>
 hipError_t launch_up(const LayerArgs &a, bool self, int grid, hipStream_t s)
 {
-    const size_t lds = kUpRedBytes + rows_lds_bytes(a.T, a.k, a.E_local);
+    const size_t lds = kExchangeBytes + rows_lds_bytes(a.T, a.k, a.E_local);
     if (self) hipLaunchKernelGGL((k_layer_up<Q8, true>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
     else hipLaunchKernelGGL((k_layer_up<Q8, false>), dim3(grid), dim3(64 * kUpWaves), lds, s, a);
     return hipGetLastError();

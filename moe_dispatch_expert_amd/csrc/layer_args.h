@@ -13,6 +13,16 @@ constexpr int kLayerSelfT = 8;       // tokens up to which the vector router run
 constexpr int kLayerSelfE = 256;     // ... and experts, for the selection
 constexpr int kQ8Group = 128;        // columns (and rows of weights) per scale
 
+// The up and down kernels' exchange of the waves' sums in LDS: per wave at most kLayerTiles tiles of 256 floats, in halves
+// that alternate.  There is one barrier per exchange and none between tasks, so a wave may write the next exchange's sums
+// while others still read this one's: the two must not overlap whatever their tile counts are.  A half therefore starts in
+// one place for every tile count (a 33 to 64 row expert of the 8-bit down kernel has two tiles where others have four).
+constexpr int kLayerWaves = 4;       // per workgroup
+constexpr int kLayerTiles = 4;       // weight tiles per task, at most
+constexpr int kExchangeHalf = kLayerWaves * kLayerTiles * 256;   // floats
+__host__ __device__ constexpr int layer_exchange_at(int par) { return par * kExchangeHalf; }
+constexpr int kExchangeBytes = 2 * kExchangeHalf * 4;
+
 // What the up kernel's first workgroup writes for the later ones: the experts with tokens in ascending order (per expert
 // the tokens ascend, row by row), and the row of every choice.
 struct LayerRec {
