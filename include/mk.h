@@ -376,9 +376,9 @@ mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma,
  *   topk_ids_in, topk_w_in   [T, k] ids and gates routed by the caller (both or
  *               neither; w_router is then not read).  An id outside
  *               [e_begin, e_begin + E_local), a negative one too, adds nothing
- *               (padding rows: all -1); an id given twice for a token counts
- *               with the sum of its gates.  A token without a local choice gets
- *               a zero row.
+ *               (padding rows: all -1); an id given more than once for a token
+ *               counts with the sum of its gates (fp32, in the choices' order).
+ *               A token without a local choice gets a zero row.
  *   w_gate_up   [E_local, 2F, d] bf16 (F gate rows, then F up rows; d contiguous)
  *   w_down      [E_local, d, F] bf16 (F contiguous)
  *   t_valid     NULL, or a device int32: only the first min(T, max(0, *t_valid))

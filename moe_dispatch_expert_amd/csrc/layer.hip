@@ -101,17 +101,16 @@ __device__ __forceinline__ void build_few_rows(const RowsLds &s, const LayerArgs
     int e = l < n ? s.ids[l] - a.e_begin : -1;
     float w = l < n ? s.w[l] : 0.0f;
     if (e < 0 || e >= a.E_local) e = -1;
-    if (a.given) {   // an id given twice for a token: one row, the gates added up
+    if (a.given) {   // an id given more than once for a token: one row, the gates added up one by one as in build_rows
         bool again = false;
-        float more = 0.0f;
+        const int own = __float_as_int(w);
         for (int j = 0; j < n; ++j) {
             const int ej = __builtin_amdgcn_readlane(e, j);
-            const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j));
+            const float wj = __int_as_float(__builtin_amdgcn_readlane(own, j));
             const bool same = ej == e && j / a.k == t;
             again |= same && j < l;
-            more += same && j > l ? wj : 0.0f;
+            w += same && j > l ? wj : 0.0f;
         }
-        w += more;
         if (again) e = -1;
     }
     int row = 0, cnt = 0, hi = 0;
@@ -192,7 +191,7 @@ __device__ __forceinline__ void build_rows(const RowsLds &s, const LayerArgs &a,
         if (e >= 0 && e < a.E_local) {
             bool first = true;
             float w = s.w[i];
-            if (a.given) {   // an id given twice for a token: one row, the gates added up
+            if (a.given) {   // an id given more than once for a token: one row, the gates added up in their order
                 for (int j = t * a.k; j < i; ++j) first &= s.ids[j] != id;
                 for (int j = i + 1; j < (t + 1) * a.k; ++j) w += s.ids[j] == id ? s.w[j] : 0.0f;
             }
