@@ -364,10 +364,12 @@ mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma,
  * this library's reading, as for mk_swiglu and mk_combine:
  *   out[t] = bf16_rne( sum over t's local choices e of
  *              w[t, e] * W_down[e] . ( silu(W_gate[e] . x[t]) * (W_up[e] . x[t]) ) )
- * fp32 sums and activation.  The intermediate w * silu(g) * u is kept in two
- * parts, 16 significant bits (mk_moe_layer_q8: 11), so the output's is the one
- * rounding that shows (g and u are not rounded to bf16, unlike in
- * mk_dispatch_gemm followed by mk_swiglu).  Every sum has a fixed order, which
+ * fp32 sums and activation.  The intermediate w * silu(g) * u keeps 16
+ * significant bits (mk_moe_layer_q8: 11), whatever the size of gates and
+ * activations, so the output's rounding is the one that shows (g and u are not
+ * rounded to bf16, unlike in mk_dispatch_gemm followed by mk_swiglu).  In
+ * mk_moe_layer_q8 intermediates below 2^-100 keep fewer.
+ * Every sum has a fixed order, which
  * does not depend on the other tokens of the call: a token's row has the same
  * bits alone and in any batch.
  *   s           the shape, with N = 2F as for mk_dispatch_gemm_swiglu; T <= 128

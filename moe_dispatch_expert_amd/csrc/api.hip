@@ -482,10 +482,10 @@ void *g_scratch_dev[kMaxDevices];
 
 // ---------------------------------------------------------------- the few-token MoE layer
 
-// Workspace: the plan, router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] in two
-// parts of at most 2 bytes and y [T min(k, E_local), d] fp32.
+// Workspace: the plan, router partial sums [8, T, E] fp32, ids and gates [T, k], h [T min(k, E_local), F] of at most 4 bytes
+// and its binades, and y [T min(k, E_local), d] fp32.
 struct LayerWs {
-    size_t rec, row_of, done, part, ids, w, h, y, total;
+    size_t rec, row_of, done, part, ids, w, h, hx, y, total;
 };
 
 LayerWs layer_ws(const mk_shape *s)
@@ -499,7 +499,8 @@ LayerWs layer_ws(const mk_shape *s)
     L.ids = L.part + align256((size_t)kRouterSegments * s->T * s->E * 4);
     L.w = L.ids + align256(tk * 4);
     L.h = L.w + align256(tk * 4);
-    L.y = L.h + align256(rows * std::max(layer_h_row_bytes(false, s->N / 2), layer_h_row_bytes(true, s->N / 2)));
+    L.hx = L.h + align256(rows * std::max(layer_h_row_bytes(false, s->N / 2), layer_h_row_bytes(true, s->N / 2)));
+    L.y = L.hx + align256(rows * layer_hx_row_bytes(s->N / 2));
     L.total = L.y + align256(rows * s->d * 4) + 256;
     return L;
 }
@@ -558,6 +559,7 @@ mk_status layer_impl(const mk_shape *s, bool q8, const void *x, const void *x_q8
     a.plan.row_of = (int32_t *)(ws + L.row_of);
     a.plan.done = (int32_t *)(ws + L.done);
     a.h = ws + L.h;
+    a.hx = (uint8_t *)ws + L.hx;
     a.y = (float *)(ws + L.y);
     a.out = (uint16_t *)out;
     a.t_valid = t_valid;

@@ -237,6 +237,10 @@ __device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, uint32_t off
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, soff, 0));
 }
+__device__ __forceinline__ uint32_t load_u32(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff)
+{
+    return __builtin_amdgcn_raw_buffer_load_b32(r, off, soff, 0);
+}
 // N consecutive floats (4-byte aligned) in one load.
 template <int N>
 __device__ __forceinline__ void load_floats(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff, float (&f)[N])
@@ -316,29 +320,58 @@ __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, u32x4_t b, f32x4_t c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
 }
-// One K = 128 product of 8-bit operands, e4m3 by e4m3, or (REST) by 2^-8 times e5m2: bytes 0 - 15 of both operands in
-// a0, b0 and 16 - 31 in a1, b1, the same K in the same place of both.  The block scales are powers of two (exponent + 127
-// in every byte).
-template <bool REST>
+// One K = 128 product of e4m3 operands: bytes 0 - 15 of both in a0, b0 and 16 - 31 in a1, b1, the same K in the same place
+// of both.  The block scales are powers of two (exponent + 127 in every byte): 1.
 __device__ __forceinline__ f32x4_t mfma_fp8(u32x4_t a0, u32x4_t a1, u32x4_t b0, u32x4_t b1, f32x4_t c)
 {
     typedef int i32x8_v __attribute__((ext_vector_type(8)));
     const i32x8_v a = {(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
     const i32x8_v b = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, REST ? 1 : 0, 0, 0x7F7F7F7F, 0,
-                                                            REST ? 0x77777777 : 0x7F7F7F7F);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
 }
 
-// Eight e4m3 codes as bf16 (exact).
-__device__ __forceinline__ u32x4_t fp8_to_bf16(uint32_t lo, uint32_t hi)
+typedef _Float16 f16x2_v __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_v __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ f32x4_t mfma_f16(u32x4_t a, u32x4_t b, f32x4_t c)
 {
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_v, a), __builtin_bit_cast(f16x8_v, b), c, 0, 0,
+                                                  0);
+}
+
+// Eight e4m3 codes as fp16 (exact).
+__device__ __forceinline__ u32x4_t fp8_to_f16(uint32_t lo, uint32_t hi)
+{
     u32x4_t o;
-    o.x = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
-    o.y = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
-    o.z = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
-    o.w = __builtin_bit_cast(uint32_t, (bf16x2_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+    o.x = __builtin_bit_cast(uint32_t, (f16x2_v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+    o.y = __builtin_bit_cast(uint32_t, (f16x2_v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+    o.z = __builtin_bit_cast(uint32_t, (f16x2_v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+    o.w = __builtin_bit_cast(uint32_t, (f16x2_v)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
     return o;
+}
+
+// The four groups of h in a lane, from their own binades (x4: a byte each) to the largest of the column's 16 (its four
+// lanes'), which is returned.
+__device__ __forceinline__ int align_groups(uint32_t x4, u32x4_t (&v)[4])
+{
+    int x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (x4 >> 8 * i) & 0xFF;
+    int m = max(max(x[0], x[1]), max(x[2], x[3]));
+    const auto far = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    m = max((int)far[0], (int)far[1]);
+    const auto near = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max((int)near[0], (int)near[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float f = __builtin_amdgcn_ldexpf(1.0f, x[i] - m);   // below 2^-24: 0, and so is then h beside the largest
+        const f16x2_v s = __builtin_bit_cast(f16x2_v, __builtin_amdgcn_cvt_pkrtz(f, f));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t w = v[i][j];
+            v[i][j] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_v, w) * s);
+        }
+    }
+    return m;
 }
 
 // ---------------------------------------------------------------- gate|up
@@ -367,32 +400,42 @@ __device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workg
     return (long)hits * n1 <= (long)few * workgroups && T <= 16 ? 1 : 2;
 }
 
-// h is kept in two parts, so that its rounding does not show beside the output's own (one bf16 part alone made the
-// layer's error 1.4 times a single rounding's): hi = bf16(h), and the rest h - hi, at most 2^-8 |h|, as bf16 for bf16
-// weights and as e5m2 of 2^8 times it (which the matrix core multiplies with e4m3 as it is) for 8-bit ones, leaving 2^-17
-// and 2^-11 |h|.  A rest that is not finite or past e5m2 (|h| > 57344) is left out.  The second part costs 2% of a
-// decode-shaped layer.  A row: the bf16 part, then the rest.  With 8-bit weights the bf16 part's 16-byte pieces of every
-// 128 elements are stored as pieces 0 1 4 5 8 9 12 13, 2 3 6 7 10 11 14 15, so that the lane of weight piece 2 g, 2 g + 1
-// (elements 32 g .. 32 g + 31) finds its four in two loads of whole cache lines.
-constexpr float kRestScale = 256.0f, kRestMax = 57344.0f;
+// h keeps more bits than the output, so that its rounding does not show beside the output's own (one bf16 made the layer's
+// error 1.4 times a single rounding's), whatever the size of gates and activations.
+// With bf16 weights it is in two parts: hi = bf16(h) and bf16(h - hi), leaving 2^-16 |h|; a rest that is not finite is left
+// out.  A row: the first part, then the second.
+// With 8-bit weights it is one fp16 value, 2^(14 - x) h, where 2^x is the binade of the largest of its 8 features, leaving
+// 2^-11 |h| (or 2^-39 of the eight's largest); e4m3 weights are exact in fp16, so the product takes both as they are.  Eight
+// features to a binade, because a task may have no more.  x + 127 is a byte of hx, 16 per block of 128 features.  The
+// 16-byte pieces of every 128 values are stored as pieces 0 1 4 5 8 9 12 13, 2 3 6 7 10 11 14 15, so that the lane of weight
+// piece 2 g, 2 g + 1 (elements 32 g .. 32 g + 31) finds its four in two loads of whole cache lines.
+constexpr uint32_t kTopBinade = 14;                // of a stored fp16
+constexpr uint32_t kLeastBinade = 27;              // 2^-100: smaller values count as that binade's
 
 template <bool Q8>
 __device__ __forceinline__ void store_h(const LayerArgs &a, int row, int f, float h0, float h1)
 {
     char *p = (char *)a.h + (size_t)row * layer_h_row_bytes(Q8, a.F);
-    const int at = Q8 ? (f & ~0x78) | (f & 8) | (f & 0x10) << 2 | (f & 0x60) >> 1 : f;
-    const uint32_t b0 = f32_to_bf16(h0), b1 = f32_to_bf16(h1);
-    const float limit = Q8 ? kRestMax / kRestScale : __builtin_inff();
-    float r0 = h0 - bf16_to_f32(b0), r1 = h1 - bf16_to_f32(b1);
-    r0 = fabsf(r0) < limit ? r0 : 0.0f;
-    r1 = fabsf(r1) < limit ? r1 : 0.0f;
-    *(uint32_t *)(p + 2 * at) = b0 | b1 << 16;
-    p += layer_h_rest(Q8, a.F);
-    if constexpr (Q8)
-        *(uint16_t *)(p + f) =
-            (uint16_t)__builtin_amdgcn_cvt_pk_bf8_f32(r0 * kRestScale, r1 * kRestScale, 0, false);
-    else
-        *(uint32_t *)(p + 2 * f) = (uint32_t)f32_to_bf16(r0) | (uint32_t)f32_to_bf16(r1) << 16;
+    if constexpr (Q8) {
+        typedef float f32x2_t __attribute__((ext_vector_type(2)));
+        typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+        // the 8 features are four neighbouring threads'
+        uint32_t m = max(__float_as_uint(h0) & 0x7FFFFFFFu, __float_as_uint(h1) & 0x7FFFFFFFu);
+        m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, kDppXor1, 0xF, 0xF, true));
+        m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, kDppXor2, 0xF, 0xF, true));
+        const uint32_t x = max(m >> 23, kLeastBinade);
+        const float scale = __uint_as_float((254 + kTopBinade - x) << 23);
+        const int at = (f & ~0x78) | (f & 8) | (f & 0x10) << 2 | (f & 0x60) >> 1;
+        *(f16x2_t *)(p + 2 * at) = __builtin_convertvector((f32x2_t){h0 * scale, h1 * scale}, f16x2_t);
+        if (f % kHGroup == 0) a.hx[(size_t)row * layer_hx_row_bytes(a.F) + f / kHGroup] = (uint8_t)x;
+    } else {
+        const uint32_t b0 = f32_to_bf16(h0), b1 = f32_to_bf16(h1);
+        float r0 = h0 - bf16_to_f32(b0), r1 = h1 - bf16_to_f32(b1);
+        r0 = fabsf(r0) < __builtin_inff() ? r0 : 0.0f;
+        r1 = fabsf(r1) < __builtin_inff() ? r1 : 0.0f;
+        *(uint32_t *)(p + 2 * f) = b0 | b1 << 16;
+        *(uint32_t *)(p + 2 * (a.F + f)) = (uint32_t)f32_to_bf16(r0) | (uint32_t)f32_to_bf16(r1) << 16;
+    }
 }
 
 constexpr int kUpWaves = kLayerWaves;
@@ -505,7 +548,7 @@ __device__ __forceinline__ void up_task(const LayerArgs &a, const RowsLds &s, in
                     for (int n = 0; n < NST; ++n)
 #pragma unroll
                         for (int r = 0; r < R; ++r) {
-                            const f32x4_t p = mfma_fp8<false>(wv[u][r][0], wv[u][r][1], x0[n], x1[n],
+                            const f32x4_t p = mfma_fp8(wv[u][r][0], wv[u][r][1], x0[n], x1[n],
                                                               f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
                             const float f = (R == 1 ? mixed : r < R / 2 ? wg : wu) * fx[u][n];
 #pragma unroll
@@ -649,9 +692,9 @@ __global__ __launch_bounds__(64 * kUpWaves, 2) void k_layer_up(LayerArgs a)
 constexpr int kDownWaves = kLayerWaves;
 
 // One down task: output columns n0 .. n0 + 16 R - 1 of expert e for its rows row0 .. row0 + cnt - 1 (cnt <= 8 N8), written
-// to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, or 128 of K in e4m3, which
-// converted to bf16 (exact) meets h's bf16 part, and as it is h's rest, and is scaled per step.  TAIL: F does not end on a
-// step; pieces past F are zeros on both sides.  red, par: as in up_task.
+// to y in fp32.  The wave sums its share of K in steps of 128 bytes of a weight row: 64 of K, which meets both of h's parts,
+// or 128 of K in e4m3, converted to fp16 (exact), its product scaled by the weights' scale and h's binade.  TAIL: F does not
+// end on a step; pieces past F are zeros on both sides.  red, par: as in up_task.
 template <bool Q8, int R, int N8, bool TAIL, bool SUM = false>
 __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int row0, int cnt, float *red, int &par)
 {
@@ -661,31 +704,31 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
     constexpr int kBytes = Q8 ? 1 : 2;
     // row groups (tiles) whose h is in registers at a time
     constexpr int NS = N8 == 6 ? 2 : N8 < 4 ? N8 : 4, NST = (NS + 1) / 2;
-    constexpr int HL = Q8 ? 3 : 2;               // 128-byte lines of an h row per step: the bf16 part's, then the rest's
     const int lane = threadIdx.x % kWave;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
     const int c = lane & 15, g = lane >> 4;
-    // the lane's piece of a weight row and of the rest of an h row (swap_pairs), in elements, and of h's bf16 part, where
-    // an 8-bit weight piece is two (store_h)
+    // the lane's piece of a weight row (swap_pairs), in elements, and of an h row, where an 8-bit weight piece is two
+    // (store_h)
     const int kp = KP * (2 * g + (c & 1)), kh = Q8 ? 8 * (4 * g + (c & 1)) : kp;
     const int steps = (a.F + KS - 1) / KS, s1 = steps * (wave + 1) / kDownWaves;
-    const uint32_t wbytes = 16 * R * (uint32_t)a.F * kBytes;
+    const uint32_t wbytes = 16 * R * (uint32_t)a.F * kBytes, hrow = layer_h_row_bytes(Q8, a.F);
     const __amdgpu_buffer_rsrc_t w = buffer_of((const char *)a.w_dn + ((size_t)e * a.d + n0) * a.F * kBytes, wbytes);
-    const __amdgpu_buffer_rsrc_t h = buffer_of((const char *)a.h + (size_t)row0 * layer_h_row_bytes(Q8, a.F),
-                                               (uint32_t)cnt * layer_h_row_bytes(Q8, a.F));
+    const __amdgpu_buffer_rsrc_t h = buffer_of((const char *)a.h + (size_t)row0 * hrow, (uint32_t)cnt * hrow);
+    const __amdgpu_buffer_rsrc_t hx = buffer_of(a.hx + (Q8 ? (size_t)row0 * layer_hx_row_bytes(a.F) : 0),
+                                                Q8 ? (uint32_t)cnt * layer_hx_row_bytes(a.F) : 0);
     const __amdgpu_buffer_rsrc_t sw =
         buffer_of(a.s_dn + (Q8 ? ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * steps : 0), Q8 ? steps * 4 : 0);
-    uint32_t wo[R][2], ho[N8], lo[N8];   // lo: of the rest
+    uint32_t wo[R][2], ho[N8], xo[NT];   // xo: of the column's binades
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) wo[r][i] = (uint32_t)((16 * r + (c & 14) + i) * a.F + kp) * kBytes;
 #pragma unroll
-    for (int n = 0; n < N8; ++n) {
-        ho[n] = (uint32_t)min(token_of<N8>(n, c), cnt - 1) * layer_h_row_bytes(Q8, a.F);
-        lo[n] = ho[n] + layer_h_rest(Q8, a.F) + kp * kBytes;
-        ho[n] += 16 * (2 * g + (c & 1));
-    }
+    for (int n = 0; n < N8; ++n)
+        ho[n] = (uint32_t)min(token_of<N8>(n, c), cnt - 1) * hrow + 16 * (2 * g + (c & 1));
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        xo[n] = (uint32_t)min(N8 == 1 ? c >> 1 : 16 * n + c, cnt - 1) * layer_hx_row_bytes(a.F) + 4 * g;
     f32x4_t acc[R][NT];
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -707,19 +750,30 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
         if constexpr (Q8) load_floats<U>(sw, 0, s * 4, fw);
 #pragma unroll
         for (int n0 = 0; n0 < N8; n0 += NS) {
-            u32x4_t hv[U][HL][NS];
+            u32x4_t hv[U][2][NS];   // the two parts, or the two lines of a block
+            uint32_t hb[U][NST];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int l = 0; l < HL; ++l)
+                for (int l = 0; l < 2; ++l)
 #pragma unroll
                     for (int n = 0; n < NS; ++n) {
-                        const bool rest = l == HL - 1;
-                        const int k = rest ? kp : kh + 16 * l;
-                        const uint32_t off = rest ? lo[n0 + n] + 128 * u : ho[n0 + n] + 128 * ((HL - 1) * u + l);
+                        const int k = Q8 ? kh + 16 * l : kp;
+                        const uint32_t off = ho[n0 + n] + (Q8 ? 128 * (2 * u + l) : 128 * u + 2 * a.F * l);
                         hv[u][l][n] = load_x(h, !TAIL || k + (s + u) * KS < a.F ? off : kPastResource,
-                                             rest ? s * 128 : s * 128 * (HL - 1));
+                                             Q8 ? s * 256 : s * 128);
                     }
+            if constexpr (Q8) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int n = 0; n < NST; ++n) {
+                        hb[u][n] = load_u32(hx, xo[n0 / 2 + n] + 16 * u, s * 16);
+                        // F % 16 == 0: a lane's four groups are all inside F, or the first two, or none
+                        const int left = a.F - (s + u) * KS - 32 * g;
+                        if (TAIL && left < 32) hb[u][n] = left > 0 ? hb[u][n] & 0xFFFFu : 0;
+                    }
+            }
             if (n0 == 0) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -728,10 +782,19 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                u32x4_t x[HL][2][NST];
+                u32x4_t x[2][2][NST];
 #pragma unroll
-                for (int l = 0; l < HL; ++l) pair_tokens<NS>(hv[u][l], x[l][0], x[l][1]);
+                for (int l = 0; l < 2; ++l) pair_tokens<NS>(hv[u][l], x[l][0], x[l][1]);
                 if constexpr (Q8) {
+                    u32x4_t xs[NST][4];
+                    float f[NST];
+#pragma unroll
+                    for (int n = 0; n < NST; ++n) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) xs[n][i] = x[i / 2][i & 1][n];
+                        const int binade = align_groups(hb[u][n], xs[n]);
+                        f[n] = __builtin_amdgcn_ldexpf(fw[u], binade - 127 - (int)kTopBinade);
+                    }
                     // RG tiles at a time, so that their chains of products interleave
                     constexpr int RG = NST == 1 && R > 1 ? 2 : 1;
 #pragma unroll
@@ -742,26 +805,24 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const u32x4_t v = wv[u][r0 + r][i];
-                                b[r][2 * i] = fp8_to_bf16(v.x, v.y);
-                                b[r][2 * i + 1] = fp8_to_bf16(v.z, v.w);
+                                b[r][2 * i] = fp8_to_f16(v.x, v.y);
+                                b[r][2 * i + 1] = fp8_to_f16(v.z, v.w);
                             }
 #pragma unroll
                         for (int n = 0; n < NST; ++n) {
                             f32x4_t p[RG];
 #pragma unroll
-                            for (int r = 0; r < RG; ++r)
-                                p[r] = mfma_fp8<true>(wv[u][r0 + r][0], wv[u][r0 + r][1], x[HL - 1][0][n],
-                                                      x[HL - 1][1][n], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+                            for (int r = 0; r < RG; ++r) p[r] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                                for (int r = 0; r < RG; ++r) p[r] = mfma_bf16(b[r][i], x[i / 2][i & 1][n], p[r]);
+                                for (int r = 0; r < RG; ++r) p[r] = mfma_f16(b[r][i], xs[n][i], p[r]);
 #pragma unroll
                             for (int r = 0; r < RG; ++r)
 #pragma unroll
                                 for (int v = 0; v < 4; ++v)
                                     acc[r0 + r][n0 / 2 + n][v] =
-                                        __builtin_fmaf(p[r][v], fw[u], acc[r0 + r][n0 / 2 + n][v]);
+                                        __builtin_fmaf(p[r][v], f[n], acc[r0 + r][n0 / 2 + n][v]);
                         }
                     }
                 } else {

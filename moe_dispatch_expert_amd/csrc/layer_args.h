@@ -12,6 +12,7 @@ constexpr int kLayerMaxT = 128;      // tokens per call (two 64-bit token masks 
 constexpr int kLayerSelfT = 8;       // tokens up to which the vector router runs and the up kernel selects by itself
 constexpr int kLayerSelfE = 256;     // ... and experts, for the selection
 constexpr int kQ8Group = 128;        // columns (and rows of weights) per scale
+constexpr int kHGroup = 8;           // 8-bit form: features of h per binade
 
 // The up and down kernels' exchange of the waves' sums in LDS: per wave at most kLayerTiles tiles of 256 floats, in halves
 // that alternate.  There is one barrier per exchange and none between tasks, so a wave may write the next exchange's sums
@@ -48,7 +49,8 @@ struct LayerArgs {
     float *w_user;
     float *part;                     // [8, T, E] router partial sums
     const float *wr, *bias;          // router
-    void *h;                         // gate * silu(g) * u, rows in expert order, in two parts (layer.hip)
+    void *h;                         // gate * silu(g) * u, rows in expert order (store_h in layer.hip)
+    uint8_t *hx;                     // 8-bit form: the binades of h
     float *y;                        // [T min(k, E_local), d]: the rows' products with W_down
     uint16_t *out;                   // [T, d] bf16
     const int32_t *t_valid;          // NULL or the number of tokens to compute (device)
@@ -66,14 +68,13 @@ __host__ __device__ inline int layer_hits_cap(int T, int k, int E_local) { retur
 constexpr int kFewChoices = 32;
 __host__ __device__ inline bool layer_sums_in_down(int T, int k) { return T <= kLayerSelfT && T * k <= kFewChoices; }
 
-// Bytes of a row of h and where its second part starts (8-bit weights: the first one holds whole blocks of 128).
-__host__ __device__ inline uint32_t layer_h_rest(bool q8, int F)
-{
-    return 2 * (q8 ? (uint32_t)(F + kQ8Group - 1) / kQ8Group * kQ8Group : (uint32_t)F);
-}
+// Bytes of a row of h (store_h in layer.hip): bf16 weights 2 F values twice, 8-bit ones whole blocks of 128 fp16 values, with
+// 16 binades per block in a row of hx.
+__host__ __device__ inline uint32_t layer_h_blocks(int F) { return (uint32_t)(F + kQ8Group - 1) / kQ8Group; }
 __host__ __device__ inline uint32_t layer_h_row_bytes(bool q8, int F)
 {
-    return layer_h_rest(q8, F) + (q8 ? (uint32_t)F : 2 * (uint32_t)F);
+    return q8 ? 2 * kQ8Group * layer_h_blocks(F) : 4 * (uint32_t)F;
 }
+__host__ __device__ inline uint32_t layer_hx_row_bytes(int F) { return kQ8Group / kHGroup * layer_h_blocks(F); }
 
 }  // namespace mk
