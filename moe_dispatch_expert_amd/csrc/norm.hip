@@ -124,11 +124,25 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a)
 
 namespace {
 
+// A launch takes fewer than 2^32 work items (more are not refused, their rows are left out), so more rows than that go
+// to several.
 template <int THREADS, int NP>
-hipError_t launch_norm_as(const NormArgs &a, hipStream_t s)
+hipError_t launch_norm_as(NormArgs a, hipStream_t s)
 {
-    hipLaunchKernelGGL((k_add_rmsnorm<THREADS, NP>), dim3(a.T), dim3(THREADS), 0, s, a);
-    return hipGetLastError();
+    constexpr int kRows = 0x7FFFFFFF / THREADS;
+    for (int left = a.T; left > 0; left -= kRows) {
+        const int n = left < kRows ? left : kRows;
+        const size_t e = (size_t)n * a.d;
+        hipLaunchKernelGGL((k_add_rmsnorm<THREADS, NP>), dim3(n), dim3(THREADS), 0, s, a);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        a.x += e;
+        if (a.res) a.res += e;
+        if (a.res_out) a.res_out += e;
+        if (a.y) a.y += e;
+        if (a.q) a.q += e, a.qs += e / 128;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
