@@ -341,7 +341,8 @@ mk_status mk_grouped_gemm_swiglu(const void *a, const int32_t *expert_offsets, i
  *   y_q8[t, i]    = e4m3_rne( y[t, i] / y_scale[t, i / 128] ).
  * fp32 arithmetic; every output is rounded once, from the fp32 values (the sum
  * of squares from the unrounded h, y_q8 from the unrounded y).  Sums of squares
- * past the fp32 range give y = 0; a NaN or an infinity in a row of x or the
+ * past the fp32 range give y = 0 (smaller ones than it holds are summed scaled,
+ * which matters with eps = 0); a row of zeros with eps = 0 gives NaN; a NaN or an infinity in a row of x or the
  * residual gives that row the values the formula has (a NaN is left out of the
  * maximum, so it reaches its own column's code and not the group's scale).
  * The pages (zubnet.ai, paragraph 2) start at the routing of token rows; the

@@ -27,6 +27,9 @@ namespace {
 
 constexpr float kAmaxFloor = 0x1p-40f;   // keeps 448 / amax finite in a group of zeros
 constexpr float kE4m3Max = 448.0f;
+// Rows of a mean square + eps below 2^-90 (only with an eps below that) are summed up again at 2^96 times their size, where
+// the smallest bf16's square is 2^-74 and the largest such row's sum 2^117.
+constexpr float kTinyMean = 0x1p-90f, kTinyScale = 0x1p96f;
 
 // Maximum over the 16 lanes of a DPP row; every lane of the row receives it.
 __device__ __forceinline__ float row16_max(float v)
@@ -46,6 +49,19 @@ __device__ __forceinline__ u32x4_t pack8(const float (&f)[8])
     for (int i = 0; i < 4; ++i)
         o[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){f[2 * i], f[2 * i + 1]}, bf16x2_t));
     return o;
+}
+
+// Sum over the workgroup; red: LDS of its own.
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float v, float *red)
+{
+    v = wave_sum_f32(v);
+    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave; ++w) v += red[w];
+    return v;
 }
 
 }  // namespace
@@ -82,20 +98,33 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a)
         for (int j = 0; j < 8; ++j) part = __builtin_fmaf(h[i][j], h[i][j], part);
         ss += ti + i * THREADS < pieces ? part : 0.0f;
     }
-    ss = wave_sum_f32(ss);
-    __shared__ float red[THREADS / kWave];
-    if (ti % kWave == 0) red[ti / kWave] = ss;
-    __syncthreads();
-    ss = 0.0f;
+    __shared__ float red[2][THREADS / kWave];
+    float mean = block_sum<THREADS>(ss, red[0]) / (float)a.d + a.eps;
+    if (a.res_out) {
 #pragma unroll
-    for (int w = 0; w < THREADS / kWave; ++w) ss += red[w];
-    const float inv = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+        for (int i = 0; i < NP; ++i)
+            if (ti + i * THREADS < pieces) *(u32x4_t *)(a.res_out + row + 8 * (ti + i * THREADS)) = pack8(h[i]);
+    }
+    if (mean < kTinyMean) {   // the whole row: its squares may be below fp32's range, those of 2^96 h are not
+        ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            float part = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                h[i][j] *= kTinyScale;
+                part = __builtin_fmaf(h[i][j], h[i][j], part);
+            }
+            ss += ti + i * THREADS < pieces ? part : 0.0f;
+        }
+        mean = block_sum<THREADS>(ss, red[1]) / (float)a.d + a.eps * kTinyScale * kTinyScale;
+    }
+    const float inv = 1.0f / sqrtf(mean);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         const int p = ti + i * THREADS;
         const bool in = p < pieces;
         const int pc = min(p, pieces - 1);
-        if (a.res_out && in) *(u32x4_t *)(a.res_out + row + 8 * p) = pack8(h[i]);
         float g[8], y[8];
         unpack8(*(const u32x4_t *)(a.gamma + 8 * pc), g);
 #pragma unroll

@@ -1,4 +1,4 @@
-"""mk_add_rmsnorm at the ends of its range: more rows than one launch's grid holds.  Formula and tolerances as in
+"""mk_add_rmsnorm at the ends of its range: more rows than one launch's grid holds, and eps = 0.  Formula and tolerances as in
 test_gpu_norm.py."""
 import pytest
 import torch
@@ -26,3 +26,27 @@ def test_norm_of_more_rows_than_a_grid(T, d, q8):
     y = out["y"].float()
     ms = (y / gamma.cuda().float()).square().mean(1)
     assert ((ms - 1).abs() < 0.02).all()
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("d", [8, 1024, 16384])
+def test_norm_of_tiny_rows_without_eps(d, residual):
+    """Squares that fp32 cannot hold: with eps = 0 (or as tiny) the formula's values are still of ordinary size."""
+    x, r, gamma = _inputs(6, d, residual, 12)
+    scale = torch.tensor([0, -40, -66, -80, -110, -120])[:, None].double()
+    x = (x.double() * 2.0 ** scale).to(torch.bfloat16)
+    r = None if r is None else (r.double() * 2.0 ** scale).to(torch.bfloat16)
+    dx, dr = x.cuda(), None if r is None else r.cuda()
+    for eps in (0.0, 1e-38, 1e-30):
+        out = mk.mk_add_rmsnorm(dx, gamma.cuda(), dr, eps=eps, q8=d % 128 == 0)
+        _check(out, x, r, gamma, eps=float(torch.tensor(eps, dtype=torch.float32)))
+
+
+def test_norm_of_zero_rows_without_eps():
+    """0 / 0 in the formula: NaN in that row only."""
+    x, _, gamma = _inputs(3, 256, False, 13)
+    x[1] = 0
+    y = mk.mk_add_rmsnorm(x.cuda(), gamma.cuda(), eps=0.0)["y"].float().cpu()
+    assert torch.isnan(y[1]).all() and torch.isfinite(y[[0, 2]]).all()
+    y = mk.mk_add_rmsnorm(x.cuda(), gamma.cuda(), eps=1e-38)["y"].float().cpu()
+    assert (y[1] == 0).all()
