@@ -5,6 +5,9 @@ libmk.so.  PyTorch provides device memory and the current stream.  There is no
 CPU fallback: loading fails loudly when the library is missing, and the calls
 require CUDA (HIP) tensors.
 
+A call given a `stream` allocates what it was not given as that stream's memory; the caller orders the streams (inputs
+before the call, the use of outputs after it).
+
 Names follow the C ABI: mk_route_topk, mk_dispatch_gemm,
 mk_dispatch_gemm_workspace_bytes, mk_route_topk_workspace_bytes,
 mk_select_tuning, mk_poll_error, mk_status_str; for a serving step of a few
@@ -13,6 +16,7 @@ mk_moe_layer_workspace_bytes.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -139,6 +143,26 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _memory_of(stream):
+    """A context whose allocations are `stream`'s memory: a call on another stream than the current one must not take the
+    current one's, where work queued earlier may still use it and later work may be given it while the call runs."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
+
+
+def _hand_over(stream, *made) -> None:
+    """The outputs allocated for a call on `stream` go to the caller's current stream: it may read them until it drops
+    them (after it has waited for `stream`)."""
+    if stream is not None:
+        cur = torch.cuda.current_stream(stream.device)
+        if cur != stream:
+            for t in made:
+                if t is not None:
+                    t.record_stream(cur)
+
+
 def _check(status: int, what: str):
     if status != MK_OK:
         raise MkError(status, what)
@@ -177,15 +201,20 @@ def mk_route_topk(x: torch.Tensor, w_router: torch.Tensor, k: int, bias: Optiona
     T, d = x.shape
     E = w_router.shape[1]
     dev = x.device
-    if topk_ids is None:
-        topk_ids = torch.empty(T, k, dtype=torch.int32, device=dev)
-    if topk_w is None:
-        topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(mk_route_topk_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
+    made = []
+    with _memory_of(stream):
+        if topk_ids is None:
+            topk_ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+            made.append(topk_ids)
+        if topk_w is None:
+            topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+            made.append(topk_w)
+        if workspace is None:
+            workspace = torch.empty(mk_route_topk_workspace_bytes(T, E), dtype=torch.uint8, device=dev)
     st = lib.mk_route_topk(_ptr(x), _ptr(w_router), _ptr(bias), T, d, E, k, _ptr(topk_ids), _ptr(topk_w),
                            _ptr(logits), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "mk_route_topk")
+    _hand_over(stream, *made)
     return topk_ids, topk_w
 
 
@@ -283,12 +312,20 @@ def mk_dispatch_gemm(x, w_experts: torch.Tensor, k: int, *, w_router: Optional[t
     dev = w_experts.device
     r_cap = T * min(k, E_local)
     o = {} if out is None else dict(out)
-    o.setdefault("y_perm", torch.empty(max(r_cap, 1), N // 2 if swiglu else N, dtype=torch.bfloat16, device=dev))
-    o.setdefault("slot_of", torch.empty(T, k, dtype=torch.int32, device=dev))
-    o.setdefault("expert_offsets", torch.empty(E_local + 1, dtype=torch.int32, device=dev))
-    o.setdefault("topk_ids", torch.empty(T, k, dtype=torch.int32, device=dev))
-    o.setdefault("topk_w", torch.empty(T, k, dtype=torch.float32, device=dev))
-    o.setdefault("row_token", torch.empty(max(r_cap, 1), dtype=torch.int32, device=dev))
+    made = []
+
+    def output(name, *of, dtype=torch.int32):
+        if name not in o:
+            o[name] = torch.empty(*of, dtype=dtype, device=dev)
+            made.append(o[name])
+
+    with _memory_of(stream):
+        output("y_perm", max(r_cap, 1), N // 2 if swiglu else N, dtype=torch.bfloat16)
+        output("slot_of", T, k)
+        output("expert_offsets", E_local + 1)
+        output("topk_ids", T, k)
+        output("topk_w", T, k, dtype=torch.float32)
+        output("row_token", max(r_cap, 1))
     shape = _shape(T, d, E, k, e_begin, E_local, N)
     srcs = _Sources(xs, chunk_rows, chunk_ready, epoch, sim_delay_us, sim_payload)
     tu = _tuning(tune)
@@ -297,7 +334,9 @@ def mk_dispatch_gemm(x, w_experts: torch.Tensor, k: int, *, w_router: Optional[t
                                                           None if tu is None else ctypes.byref(tu)))
         if nbytes == 0:
             _check(MK_EINVAL, "mk_dispatch_gemm_workspace_bytes")
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        with _memory_of(stream):
+            workspace = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        made.append(workspace)
     fn = lib.mk_dispatch_gemm_swiglu if swiglu else lib.mk_dispatch_gemm
     st = fn(ctypes.byref(shape), ctypes.byref(srcs.c), _ptr(w_router), _ptr(bias),
             _ptr(topk_ids_in), _ptr(w_experts), _ptr(o["y_perm"]), _ptr(o["slot_of"]),
@@ -305,6 +344,7 @@ def mk_dispatch_gemm(x, w_experts: torch.Tensor, k: int, *, w_router: Optional[t
             _ptr(o["row_token"]), _ptr(workspace), workspace.numel(),
             None if tu is None else ctypes.byref(tu), _stream(stream))
     _check(st, "mk_dispatch_gemm_swiglu" if swiglu else "mk_dispatch_gemm")
+    _hand_over(stream, *made)
     o["workspace"] = workspace
     o["_sources"] = srcs
     return o
@@ -341,11 +381,14 @@ def mk_combine(y_perm: torch.Tensor, slot_of: torch.Tensor, topk_w: torch.Tensor
     N = y_perm.shape[1]
     if rows is None:
         rows = y_perm.shape[0]
+    made = None
     if out is None:
-        out = torch.empty(T, N, dtype=torch.bfloat16, device=slot_of.device)
+        with _memory_of(stream):
+            out = made = torch.empty(T, N, dtype=torch.bfloat16, device=slot_of.device)
     st = load().mk_combine(_ptr(y_perm), int(rows), _ptr(slot_of), _ptr(topk_w), T, k, N, _ptr(out),
                            _stream(stream))
     _check(st, "mk_combine")
+    _hand_over(stream, made)
     return out
 
 
@@ -356,9 +399,12 @@ def mk_swiglu(gate_up: torch.Tensor, rows: Optional[int] = None, out: Optional[t
     F = F2 // 2
     if rows is None:
         rows = R2
+    made = None
     if out is None:
-        out = torch.empty(R2, F, dtype=torch.bfloat16, device=gate_up.device)
+        with _memory_of(stream):
+            out = made = torch.empty(R2, F, dtype=torch.bfloat16, device=gate_up.device)
     _check(load().mk_swiglu(_ptr(gate_up), int(rows), F, _ptr(out), _stream(stream)), "mk_swiglu")
+    _hand_over(stream, made)
     return out
 
 
@@ -367,12 +413,15 @@ def mk_grouped_gemm(a: torch.Tensor, expert_offsets: torch.Tensor, w: torch.Tens
                     stream=None) -> torch.Tensor:
     """y[r] = bf16(a[r] . W[e]^T) for the rows r of each expert e of the layout (mk_grouped_gemm)."""
     E_local, N, K = w.shape
-    if out is None:
-        out = torch.empty(a.shape[0], N, dtype=torch.bfloat16, device=a.device)
-    if workspace is None:
-        workspace = torch.empty(mk_grouped_gemm_workspace_bytes(E_local), dtype=torch.uint8, device=a.device)
+    made = None
+    with _memory_of(stream):
+        if out is None:
+            out = made = torch.empty(a.shape[0], N, dtype=torch.bfloat16, device=a.device)
+        if workspace is None:
+            workspace = torch.empty(mk_grouped_gemm_workspace_bytes(E_local), dtype=torch.uint8, device=a.device)
     _check(load().mk_grouped_gemm(_ptr(a), _ptr(expert_offsets), E_local, _ptr(w), K, N, _ptr(out),
                                   _ptr(workspace), workspace.numel(), _stream(stream)), "mk_grouped_gemm")
+    _hand_over(stream, made)
     return out
 
 
@@ -383,13 +432,16 @@ def mk_grouped_gemm_swiglu(a: torch.Tensor, expert_offsets: torch.Tensor, w_gate
     (mk_grouped_gemm_swiglu)."""
     E_local, two_f, K = w_gate_up.shape
     F = two_f // 2
-    if out is None:
-        out = torch.empty(a.shape[0], F, dtype=torch.bfloat16, device=a.device)
-    if workspace is None:
-        workspace = torch.empty(mk_grouped_gemm_workspace_bytes(E_local), dtype=torch.uint8, device=a.device)
+    made = None
+    with _memory_of(stream):
+        if out is None:
+            out = made = torch.empty(a.shape[0], F, dtype=torch.bfloat16, device=a.device)
+        if workspace is None:
+            workspace = torch.empty(mk_grouped_gemm_workspace_bytes(E_local), dtype=torch.uint8, device=a.device)
     _check(load().mk_grouped_gemm_swiglu(_ptr(a), _ptr(expert_offsets), E_local, _ptr(w_gate_up), K, F,
                                          _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "mk_grouped_gemm_swiglu")
+    _hand_over(stream, made)
     return out
 
 
@@ -439,11 +491,13 @@ def mk_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torc
     dev = x.device
     o = {}
     given = out or o
+    made = []
 
     def output(name, dtype, of):
         t = given.get(name)
         if t is None:
             t = torch.empty_like(x) if dtype is _BF16 else torch.empty(of, dtype=dtype, device=dev)
+            made.append(t)
             p = t.data_ptr()
         else:
             p = _need(what, name, t, dev, dtype, of)
@@ -453,15 +507,17 @@ def mk_add_rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torc
     px = _need(what, "x", x, dev, _BF16, shape)
     pg = _need(what, "gamma", gamma, dev, _BF16, (d,))
     pr = po = py = pq = ps = None
-    if residual is not None:
-        pr = _need(what, "residual", residual, dev, _BF16, shape)
-        po = output("residual", _BF16, shape)
-    if bf16:
-        py = output("y", _BF16, shape)
-    if q8:
-        pq = output("q8", _FP8, shape)
-        ps = output("q8_scale", _F32, (T, d // 128))
+    with _memory_of(stream):
+        if residual is not None:
+            pr = _need(what, "residual", residual, dev, _BF16, shape)
+            po = output("residual", _BF16, shape)
+        if bf16:
+            py = output("y", _BF16, shape)
+        if q8:
+            pq = output("q8", _FP8, shape)
+            ps = output("q8_scale", _F32, (T, d // 128))
     _call_on(dev, stream, (_lib or load()).mk_add_rmsnorm, what, px, pr, pg, T, d, eps, po, py, pq, ps)
+    _hand_over(stream, *made)
     return o
 
 
@@ -483,16 +539,20 @@ def _moe_layer(what, x, x_q8, x_scale, w_gate_up, gate_up_scale, w_down, down_sc
         E = w_router.shape[1] if w_router is not None else E_local
     given = out or {}
     y, ids, gates = given.get("out"), given.get("topk_ids"), given.get("topk_w")
-    if y is None:
-        y = torch.empty((T, d), dtype=_BF16, device=dev)
-        py = y.data_ptr()
-    else:
-        py = _need(what, "out", y, dev, _BF16, (T, d))
     lib = _lib or load()
     shape = _shape(T, d, E, k, e_begin, E_local, two_f)
-    if workspace is None:   # (for a shape that the call refuses the size is 0, and the call names the reason)
-        workspace = torch.empty(max(256, lib.mk_moe_layer_workspace_bytes(ctypes.byref(shape))), dtype=torch.uint8,
-                                device=dev)
+    made = ()
+    with _memory_of(stream):
+        if y is None:
+            y = torch.empty((T, d), dtype=_BF16, device=dev)
+            made = (y,)
+            py = y.data_ptr()
+        else:
+            py = _need(what, "out", y, dev, _BF16, (T, d))
+        if workspace is None:   # (for a shape that the call refuses the size is 0, and the call names the reason)
+            workspace = torch.empty(max(256, lib.mk_moe_layer_workspace_bytes(ctypes.byref(shape))), dtype=torch.uint8,
+                                    device=dev)
+            made += (workspace,)
     routing = (_may(what, "w_router", w_router, dev, _F32, (d, E)), _may(what, "bias", bias, dev, _F32, (E,)),
                _may(what, "topk_ids_in", topk_ids_in, dev, _I32, (T, k)),
                _may(what, "topk_w_in", topk_w_in, dev, _F32, (T, k)))
@@ -512,6 +572,7 @@ def _moe_layer(what, x, x_q8, x_scale, w_gate_up, gate_up_scale, w_down, down_sc
         _call_on(dev, stream, lib.mk_moe_layer, what, ctypes.byref(shape), px, *routing,
                  _need(what, "w_gate_up", w_gate_up, dev, _BF16, (E_local, two_f, d)),
                  _need(what, "w_down", w_down, dev, _BF16, (E_local, d, F)), *outs)
+    _hand_over(stream, *made)
     return {"out": y, "topk_ids": ids, "topk_w": gates, "workspace": workspace}
 
 
