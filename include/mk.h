@@ -369,10 +369,9 @@ mk_status mk_add_rmsnorm(const void *x, const void *residual, const void *gamma,
  * significant bits (mk_moe_layer_q8: 11), whatever the size of gates and
  * activations, so the output's rounding is the one that shows (g and u are not
  * rounded to bf16, unlike in mk_dispatch_gemm followed by mk_swiglu).  In
- * mk_moe_layer_q8 intermediates below 2^-100 keep fewer.
- * Every sum has a fixed order, which
- * does not depend on the other tokens of the call: a token's row has the same
- * bits alone and in any batch.
+ * mk_moe_layer_q8 intermediates below 2^-100, alone or times down_scale, keep
+ * fewer.  Every sum has a fixed order, which does not depend on the other tokens
+ * of the call: a token's row has the same bits alone and in any batch.
  *   s           the shape, with N = 2F as for mk_dispatch_gemm_swiglu; T <= 128
  *   w_router, bias   routing inside the call, ids and gates bit for bit those of
  *               mk_route_topk; or

@@ -718,14 +718,17 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
                                                 Q8 ? (uint32_t)cnt * layer_hx_row_bytes(a.F) : 0);
     const __amdgpu_buffer_rsrc_t sw =
         buffer_of(a.s_dn + (Q8 ? ((size_t)e * (a.d / kQ8Group) + n0 / kQ8Group) * steps : 0), Q8 ? steps * 4 : 0);
-    uint32_t wo[R][2], ho[N8], xo[NT];   // xo: of the column's binades
+    uint32_t wo[R][2], ho[N8], lo[N8], xo[NT];   // lo: of the second part or line; xo: of the column's binades
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) wo[r][i] = (uint32_t)((16 * r + (c & 14) + i) * a.F + kp) * kBytes;
 #pragma unroll
-    for (int n = 0; n < N8; ++n)
-        ho[n] = (uint32_t)min(token_of<N8>(n, c), cnt - 1) * hrow + 16 * (2 * g + (c & 1));
+    for (int n = 0; n < N8; ++n) {
+        ho[n] = (uint32_t)min(token_of<N8>(n, c), cnt - 1) * hrow;
+        lo[n] = ho[n] + (Q8 ? 128 : 2 * a.F) + 16 * (2 * g + (c & 1));
+        ho[n] += 16 * (2 * g + (c & 1));
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
         xo[n] = (uint32_t)min(N8 == 1 ? c >> 1 : 16 * n + c, cnt - 1) * layer_hx_row_bytes(a.F) + 4 * g;
@@ -759,7 +762,7 @@ __device__ __forceinline__ void down_task(const LayerArgs &a, int e, int n0, int
 #pragma unroll
                     for (int n = 0; n < NS; ++n) {
                         const int k = Q8 ? kh + 16 * l : kp;
-                        const uint32_t off = ho[n0 + n] + (Q8 ? 128 * (2 * u + l) : 128 * u + 2 * a.F * l);
+                        const uint32_t off = (l == 0 ? ho[n0 + n] : lo[n0 + n]) + (Q8 ? 256 : 128) * u;
                         hv[u][l][n] = load_x(h, !TAIL || k + (s + u) * KS < a.F ? off : kPastResource,
                                              Q8 ? s * 256 : s * 128);
                     }

@@ -120,3 +120,33 @@ def test_many_calls_on_another_stream_without_a_workspace():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want)
+
+
+@pytest.mark.gpu
+def test_captured_on_a_forked_stream():
+    """A capture whose calls run on a second stream and allocate for themselves, replayed between eager calls."""
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(40, 256, generator=g).to(BF16).cuda()
+    w = (torch.randn(8, 256, 256, generator=g) / 16).to(BF16).cuda()
+    dn = (torch.randn(8, 256, 128, generator=g) / 11).to(BF16).cuda()
+    wr, gamma = (torch.randn(256, 8, generator=g) / 16).cuda(), torch.ones(256, dtype=BF16, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step(s):
+        n = mk.mk_add_rmsnorm(x, gamma, stream=s)["y"]
+        return mk.mk_moe_layer(n, w, dn, 2, w_router=wr, stream=s)["out"]
+
+    step(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = step(side)
+        torch.cuda.current_stream().wait_stream(side)
+    for i in range(4):
+        x.mul_(1.25)
+        out.zero_()
+        graph.replay()
+        want = step(None)
+        assert torch.equal(out, want), i
+        torch.cuda.synchronize()
