@@ -21,10 +21,11 @@
 // token's rows up in expert order, and "sum", which does that for more.
 //
 // Bound by memory; a kernel that only reads reaches 7.0 - 7.1 TB/s here.  Kernel times, bf16 / e4m3:
-//   128 tokens, 32 of 256 experts, d = 7168, F = 2048:   router 18.5, selection 4.7, up 275 - 289 / 144 - 149
-//                                                        (6.5 - 6.8 / 6.3 - 6.5 TB/s), down 142 - 148 / 79 - 82, sum 4.8 us
-//   1 token, 2 of 8 experts, d = 4096, F = 14336, bf16:  router 5.8, up 73 (6.4 TB/s), down with the sum 39 us
-//   128 tokens, 2 of 8 experts, same sizes (32 rows each): up 340 - 352 / 210, down 220 / 172 us
+//   128 tokens, 32 of 256 experts, d = 7168, F = 2048:   router 18.7, selection 4.8, up 288 / 148 (6.5 / 6.3 TB/s), down
+//                                                        148 / 79 (6.3 / 6.0), sum 4.9 us
+//   1 token, 2 of 8 experts, d = 4096, F = 14336, bf16:  router 6.0, up 74 (6.4 TB/s), down with the sum 39 us
+//   64 tokens, 2 of 8 experts, same sizes (16 rows each): up 301 / 168, down 158 / 88 us
+//   128 tokens (32 rows each):                           up 354 / 211, down 221 / 168 us
 // With 32 rows an expert the tokens' and h's loads weigh as much as the weights', and a wave's loads and products no
 // longer overlap as well.
 #include <hip/hip_runtime.h>
@@ -391,7 +392,7 @@ struct IntC {
 // tiles where the workgroups get at least four tasks each or come out nearly even (8 experts of 32 rows: up 352 us, with
 // two tiles 405).  One tile (built for 16 tokens at most) where that gives a workgroup `few` tasks or fewer: up, few = 4
 // (1 expert of 2048 features, d = 7168: 15 us, with two tiles 23), and down, whose tasks are shorter, few = 1 (6 experts
-// of e4m3, d = 2048, twice as many tasks as workgroups: 8.4 us, with two tiles 7.0).
+// of e4m3, d = 2048, 768 tasks of one tile for 512 workgroups: the whole call 28.6 us, with two tiles 25.6).
 __device__ __forceinline__ int tiles_per_task(int hits, int n1, int T, int workgroups, int few)
 {
     const long t4 = (long)hits * ((n1 + 3) / 4);
@@ -973,7 +974,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 2) void k_layer_down(LayerArgs a)
                 if (m <= 8) down_task<Q8, R, 1, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else if (m <= 16) down_task<Q8, R, 2, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else if (m <= 32) down_task<Q8, R, 4, TAIL>(a, e, n0, row0 + r, m, red, par);
-                else if (!Q8 && m <= 48)   // 256 choices over 8 experts, 14336 features: 220 us, without this form 246
+                else if (!Q8 && m <= 48)   // 256 choices over 8 experts, 14336 features: 221 us, without this form 247
                     down_task<Q8, R, Q8 ? 8 : 6, TAIL>(a, e, n0, row0 + r, m, red, par);
                 else   // four e4m3 tiles by four token tiles would not fit the registers
                     for (int i = 0; i < (Q8 ? R / 2 : 1); ++i)

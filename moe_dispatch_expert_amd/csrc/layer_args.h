@@ -61,10 +61,10 @@ struct LayerArgs {
 __host__ __device__ inline int layer_rows_cap(int T, int k, int E_local) { return T * (k < E_local ? k : E_local); }
 __host__ __device__ inline int layer_hits_cap(int T, int k, int E_local) { return E_local < T * k ? E_local : T * k; }
 
-// A few choices: the down kernel adds the rows up itself, one launch fewer (whole calls back to back: one token at 6 experts
-// of e4m3 27.7 -> 26.5 us, a Mixtral-shaped token 120.1 -> 119.4, where the host is slower than the kernels 20 -> 17).  With
-// more the wait for other workgroups' rows costs as much or more (8 tokens, 64 choices: 92.2 -> 92.9, 16 tokens, 128
-// choices: 211.5 -> 214.5).
+// A few choices: the down kernel adds the rows up itself, one launch fewer (whole calls in a captured graph, the sum in a
+// kernel of its own against in the down kernel: one token at 6 experts of e4m3 26.3 -> 25.6 us, d = F = 512 14.8 -> 14.4, a
+// Mixtral-shaped token 118.8 -> 118.6).  With more the wait for other workgroups' rows costs more than the launch (8 tokens
+// with 64 choices of 32 experts: 109.8 -> 111.9 us, with 48 of 64 small ones 107.7 -> 109.6, of e4m3 68.9 -> 71.1).
 constexpr int kFewChoices = 32;
 __host__ __device__ inline bool layer_sums_in_down(int T, int k) { return T <= kLayerSelfT && T * k <= kFewChoices; }
 
