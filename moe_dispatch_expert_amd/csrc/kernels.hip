@@ -14,12 +14,12 @@
 
 namespace mk {
 
-// Router partial sums: one wave task per wave, four per workgroup.
-__global__ __launch_bounds__(256) void k_router(RouterArgs a)
+// Router partial sums: one wave task per wave, four per workgroup, from task q0.
+__global__ __launch_bounds__(256) void k_router(RouterArgs a, int q0)
 {
     __shared__ __attribute__((aligned(16))) char lds[4 * kRtLdsPerWave];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
-    const int q = (int)blockIdx.x * 4 + wave;
+    const int q = q0 + (int)blockIdx.x * 4 + wave;
     if (q < router_tasks(a.T, a.E)) router_task(a, q, (lds_byte_t *)(lds + wave * kRtLdsPerWave));
 }
 
@@ -193,16 +193,26 @@ hipError_t launch_zero(void *p, size_t bytes, hipStream_t s)
     return hipGetLastError();
 }
 
+// Workgroups of 256 threads per launch: one launch takes fewer than 2^32 work items, and the rest of more is not refused
+// but left out.
+constexpr int kMostWorkgroups = 1 << 23;
+
 hipError_t launch_router(const RouterArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_router, dim3((router_tasks(a.T, a.E) + 3) / 4), dim3(256), 0, s, a);
-    return hipGetLastError();
+    const int tasks = router_tasks(a.T, a.E);
+    for (long q0 = 0; q0 < tasks; q0 += 4L * kMostWorkgroups) {
+        const int grid = (int)std::min<long>((tasks - q0 + 3) / 4, kMostWorkgroups);
+        hipLaunchKernelGGL(k_router, dim3(grid), dim3(256), 0, s, a, (int)q0);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_topk(const TopkArgs &ta, const CountArgs &ca, bool do_count, hipStream_t s)
 {
     // token-parallel selection, then the per-block histogram from the ids it wrote
-    hipLaunchKernelGGL(k_topk_wave, dim3(topk_wave_units(ta.T, 4)), dim3(256), 0, s, ta);
+    hipLaunchKernelGGL(k_topk_wave, dim3(std::min(topk_wave_units(ta.T, 4), kMostWorkgroups)), dim3(256), 0, s, ta);
     if (!do_count) return hipGetLastError();
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
