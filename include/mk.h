@@ -420,6 +420,134 @@ mk_status mk_moe_layer_q8(const mk_shape *s, const void *x, const void *x_q8, co
                           int32_t *topk_ids_out, float *topk_w_out, void *workspace, size_t workspace_bytes,
                           void *stream);
 
+/* The expert layout of given choices, as the dispatch makes it, without a
+ * product: for callers that route first and run the grouped products below on
+ * their own rows.  The pages name the routing of tokens to experts (zubnet.ai,
+ * paragraph 2; lefilia.fr, paragraph 3); slots in ascending token order are
+ * this library's reading, as for mk_dispatch_gemm.
+ *   e'          = topk_ids[t, j] - e_begin, local if 0 <= e' < E_local
+ *   offsets     = exclusive prefix sum of the local experts' choices; R = offsets[E_local]
+ *   slot_of[t,j]= offsets[e'] + #{local choices (t', j') of e' before (t, j)},
+ *                 by token, then by j;  -1 if not local (a negative id too)
+ *   row_token[slot_of[t, j]] = t
+ * A token that names an expert twice gets two rows.
+ *   topk_ids [T, k] int32     slot_of [T, k] int32 (out)
+ *   expert_offsets [E_local + 1] int32 (out)
+ *   row_token NULL or [T * k] int32 (out; entries >= R are not written)
+ *   workspace mk_expert_layout_workspace_bytes(T, k, E_local) bytes, any
+ *             contents; two calls in flight must not share one.
+ * Requires T >= 0, k >= 1, T * k < 2^31, E_local >= 1, e_begin >= 0; k <= 32,
+ * E_local <= 1024 (else MK_EUNSUPPORTED).  T == 0 gives offsets of 0. */
+size_t mk_expert_layout_workspace_bytes(int32_t T, int32_t k, int32_t E_local);
+mk_status mk_expert_layout(const int32_t *topk_ids, int32_t T, int32_t k, int32_t e_begin, int32_t E_local,
+                           int32_t *slot_of, int32_t *expert_offsets, int32_t *row_token, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Backward pass of the expert FFN.  The pages name the MoE Dispatch+GEMM kernel
+ * for training too (zubnet.ai, paragraph 1); the gradients are those of
+ * mk_combine, mk_swiglu and mk_grouped_gemm as this header defines them.  The
+ * dispatch's own gradient, dx[t] = sum over t's slots of da[slot], is mk_combine
+ * with gates of one.
+ *
+ * mk_combine_backward:
+ *   dy[slot_of[t, j], n] = bf16_rne( topk_w[t, j] * dout[t, n] )
+ *   dtopk_w[t, j]        = sum_n dout[t, n] * y_perm[slot_of[t, j], n]
+ * for 0 <= slot_of[t, j] < rows; otherwise dtopk_w[t, j] = 0.  fp32, the sum in a
+ * fixed order.  A slot that one token names more than once gets the sum of its
+ * gates; different tokens name different slots (as the dispatch makes them).
+ * Rows of dy that no choice names are left as they were.
+ *   dout [T, N] bf16     y_perm [rows, N] bf16 (may be NULL without dtopk_w)
+ *   slot_of [T, k] int32     topk_w [T, k] fp32
+ *   dy [rows, N] bf16 (out; may be y_perm)     dtopk_w NULL or [T, k] fp32 (out)
+ * Requires T >= 0, 1 <= k <= 32, rows >= 0, N > 0, N % 8 == 0. */
+mk_status mk_combine_backward(const void *dout, const void *y_perm, int32_t rows, const int32_t *slot_of,
+                              const float *topk_w, int32_t T, int32_t k, int32_t N, void *dy, float *dtopk_w,
+                              void *stream);
+
+/* Gradient of mk_swiglu over [g | u] rows, with s = 1 / (1 + e^-g):
+ *   dgate_up[r, f]     = bf16_rne( dh[r, f] * u * s * (1 + g * (1 - s)) )
+ *   dgate_up[r, F + f] = bf16_rne( dh[r, f] * g * s )
+ * fp32; and, if asked for, h[r, f] as mk_swiglu gives it, bit for bit (what the
+ * gradient of the down-projection's weights reads).
+ *   gate_up [rows, 2F] bf16     dh [rows, F] bf16
+ *   rows_valid NULL, or a device int32 (4-byte aligned; expert_offsets + E_local
+ *              is one): only the first min(rows, max(0, *rows_valid)) rows are
+ *              computed, the others of every output are left as they were
+ *   dgate_up [rows, 2F] bf16 (out; may be gate_up)     h NULL or [rows, F] bf16 (out; may be dh)
+ * Requires rows >= 0, F > 0, F % 8 == 0. */
+mk_status mk_swiglu_backward(const void *gate_up, const void *dh, int32_t rows, int32_t F, const int32_t *rows_valid,
+                             void *dgate_up, void *h, void *stream);
+
+/* Gradient of mk_grouped_gemm (y[r] = W[e] . a[r]) for its rows:
+ *   da[r, i] = bf16_rne( sum_n dy[r, n] * w[e, n, i] ),  fp32 accumulation,
+ * for every row r of expert e, offsets[e] <= r < offsets[e + 1].  The sum's order
+ * does not depend on other rows.
+ *   dy [rows, N] bf16     expert_offsets [E_local + 1] int32 (non-decreasing, offsets[0] = 0; read on the device,
+ *                         values past `rows` are taken as `rows`)
+ *   w [E_local, N, K] bf16 (as for mk_grouped_gemm)
+ *   da [rows, K] bf16 (out; rows >= offsets[E_local] untouched)
+ * Requires rows >= 0, 1 <= E_local <= 1024, N > 0, K > 0, N % 8 == 0, K % 8 == 0;
+ * N, K <= 2^20 (else MK_EUNSUPPORTED).  rows == 0 is a no-op.  No workspace. */
+mk_status mk_grouped_gemm_dgrad(const void *dy, int32_t rows, const int32_t *expert_offsets, int32_t E_local,
+                                const void *w, int32_t K, int32_t N, void *da, void *stream);
+
+/* Gradient of mk_grouped_gemm for the experts' weights:
+ *   dw[e, n, i] (+)= sum over e's rows r of dy[r, n] * a[t(r), i],  fp32 accumulation,
+ * t(r) = r, or row_token[r] where the product read its rows in place
+ * (mk_dispatch_gemm: a is then the token matrix).  An expert without rows gets
+ * zeros.  The sum's order is fixed.
+ *   dy [rows, N] bf16     expert_offsets as for mk_grouped_gemm_dgrad
+ *   row_token NULL, or [rows] int32; a is then [a_rows, K], and a value outside
+ *             [0, a_rows) reads a row of zeros
+ *   a [rows, K] bf16 (row_token NULL; a_rows is ignored) or [a_rows, K]
+ *   dw [E_local, N, K] (out): fp32 with dw_fp32 = 1, bf16 (one rounding) with 0
+ *   accumulate 1: added to what dw holds (fp32 only, else MK_EINVAL); 0: dw is overwritten
+ * Requires what mk_grouped_gemm_dgrad does; with row_token, a_rows >= 0 and
+ * a_rows * K * 2 <= 2^32 - 512 (else MK_EUNSUPPORTED).  rows == 0 gives zeros
+ * (nothing to add with accumulate).  No workspace. */
+mk_status mk_grouped_gemm_wgrad(const void *dy, const void *a, int32_t rows, const int32_t *expert_offsets,
+                                int32_t E_local, const int32_t *row_token, int32_t a_rows, int32_t K, int32_t N,
+                                void *dw, int32_t dw_fp32, int32_t accumulate, void *stream);
+
+/* The grouped product in 8-bit integers, with a scale for every row (token) and
+ * every output channel; the pages name the expert GEMM (zubnet.ai, paragraph 2),
+ * its 8-bit form is this library's.
+ *
+ * mk_quant_i8: rows of codes,
+ *   m = max |x[r, :]|,  scale[r] = m / 127,  q[r, i] = round( 127 * x[r, i] / m )
+ * (ties to even).  A row of zeros has scale 0 and codes 0; a row with an infinity
+ * or a NaN has scale NaN and codes 0, so that what is computed from it is NaN.  A
+ * scale below 2^-126 (m below 2^-119) has fewer bits.
+ *   x [rows, d] bf16     rows_valid as for mk_swiglu_backward
+ *   q [rows, d] int8 (out)     scale [rows] fp32 (out)
+ * mk_swiglu_i8: the same of h = silu(g) * u (fp32, not rounded in between) of
+ * [g | u] rows: gate_up [rows, 2F] bf16, q [rows, F], scale [rows].
+ * Require rows >= 0, d (F) > 0, d % 8 == 0; d <= 32768 (else MK_EUNSUPPORTED). */
+mk_status mk_quant_i8(const void *x, int32_t rows, int32_t d, const int32_t *rows_valid, void *q, float *scale,
+                      void *stream);
+mk_status mk_swiglu_i8(const void *gate_up, int32_t rows, int32_t F, const int32_t *rows_valid, void *q, float *scale,
+                       void *stream);
+
+/* mk_grouped_gemm_i8:
+ *   y[r, n] = bf16_rne( a_scale[t(r)] * w_scale[e, n] * sum_i a[t(r), i] * w[e, n, i] )
+ * for every row r of expert e; t(r) = r, or row_token[r] (rows of tokens quantised
+ * once and read in place by every expert that the token chose).  The sum is exact
+ * (int32), so y has the same bits whatever the batch; it is converted to fp32,
+ * scaled by w_scale, then by a_scale.  A plain product is E_local = 1.
+ *   a [rows, K] int8 and a_scale [rows] fp32 (row_token NULL; a_rows is ignored),
+ *     or [a_rows, K] and [a_rows] with row_token [rows] (a value outside
+ *     [0, a_rows) gives a row of zeros)
+ *   expert_offsets as for mk_grouped_gemm_dgrad
+ *   w [E_local, N, K] int8 (K contiguous)     w_scale [E_local, N] fp32
+ *   y [rows, N] bf16 (out; rows >= offsets[E_local] untouched)
+ * Requires rows >= 0, 1 <= E_local <= 1024, N > 0, K > 0, N % 8 == 0, K % 16 == 0;
+ * K < 2^17 (int32 sums), N <= 2^20 and, with row_token, a_rows >= 0,
+ * a_rows * K <= 2^32 - 512 (else MK_EUNSUPPORTED).  rows == 0 is a no-op.  No
+ * workspace. */
+mk_status mk_grouped_gemm_i8(const void *a, const float *a_scale, int32_t rows, const int32_t *expert_offsets,
+                             int32_t E_local, const int32_t *row_token, int32_t a_rows, const void *w,
+                             const float *w_scale, int32_t K, int32_t N, void *y, void *stream);
+
 /* Synchronous: reads the device error word of a dispatch workspace (the caller
  * must have synchronised the stream).  Returns MK_OK, MK_ETIMEOUT or MK_EINVAL;
  * *detail (if non-NULL) receives which wait or id failed.  Clears the word. */

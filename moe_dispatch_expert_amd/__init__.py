@@ -12,7 +12,10 @@ Names follow the C ABI: mk_route_topk, mk_dispatch_gemm,
 mk_dispatch_gemm_workspace_bytes, mk_route_topk_workspace_bytes,
 mk_select_tuning, mk_poll_error, mk_status_str; for a serving step of a few
 tokens mk_add_rmsnorm, mk_moe_layer, mk_moe_layer_q8,
-mk_moe_layer_workspace_bytes.
+mk_moe_layer_workspace_bytes; for training mk_combine_backward,
+mk_swiglu_backward, mk_grouped_gemm_dgrad, mk_grouped_gemm_wgrad; in 8-bit
+integers mk_quant_i8, mk_swiglu_i8, mk_grouped_gemm_i8; mk_expert_layout,
+mk_expert_layout_workspace_bytes.
 """
 from __future__ import annotations
 
@@ -120,6 +123,19 @@ def load() -> ctypes.CDLL:
     lib.mk_moe_layer.restype = _c_i32
     lib.mk_moe_layer_q8.argtypes = [P(MkShape)] + [_vp] * 16 + [ctypes.c_size_t, _vp]
     lib.mk_moe_layer_q8.restype = _c_i32
+    size, i = ctypes.c_size_t, _c_i32
+    for name, args in (("mk_expert_layout", [_vp, i, i, i, i, _vp, _vp, _vp, _vp, size, _vp]),
+                       ("mk_combine_backward", [_vp, _vp, i, _vp, _vp, i, i, i, _vp, _vp, _vp]),
+                       ("mk_swiglu_backward", [_vp, _vp, i, i, _vp, _vp, _vp, _vp]),
+                       ("mk_grouped_gemm_dgrad", [_vp, i, _vp, i, _vp, i, i, _vp, _vp]),
+                       ("mk_grouped_gemm_wgrad", [_vp, _vp, i, _vp, i, _vp, i, i, i, _vp, i, i, _vp]),
+                       ("mk_quant_i8", [_vp, i, i, _vp, _vp, _vp, _vp]),
+                       ("mk_swiglu_i8", [_vp, i, i, _vp, _vp, _vp, _vp]),
+                       ("mk_grouped_gemm_i8", [_vp, _vp, i, _vp, i, _vp, i, _vp, _vp, i, i, _vp, _vp])):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = i
+    lib.mk_expert_layout_workspace_bytes.argtypes = [i, i, i]
+    lib.mk_expert_layout_workspace_bytes.restype = size
     _lib = lib
     return lib
 
@@ -604,3 +620,198 @@ def mk_moe_layer_q8(x_q8: torch.Tensor, x_scale: torch.Tensor, w_gate_up: torch.
     x [T, d] bf16 is the router's input, needed with w_router."""
     return _moe_layer("mk_moe_layer_q8", x, x_q8, x_scale, w_gate_up, gate_up_scale, w_down, down_scale, k, w_router,
                       bias, topk_ids_in, topk_w_in, E, e_begin, t_valid, workspace, out, stream)
+
+
+_I8 = torch.int8
+
+
+def _outputs(what, given, dev, stream, wanted):
+    """The output tensors of a call by name, those of `given` checked, the others allocated: (dict, made).  wanted: name ->
+    (dtype, shape)."""
+    o, made = {}, []
+    with _memory_of(stream):
+        for name, (dtype, shape) in wanted.items():
+            t = None if given is None else given.get(name)
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=dev)
+                made.append(t)
+            else:
+                _need(what, name, t, dev, dtype, shape)
+            o[name] = t
+    return o, made
+
+
+def mk_expert_layout_workspace_bytes(T: int, k: int, E_local: int) -> int:
+    return int(load().mk_expert_layout_workspace_bytes(T, k, E_local))
+
+
+def mk_expert_layout(topk_ids: torch.Tensor, E_local: int, e_begin: int = 0, *, out: Optional[dict] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """The expert layout of the choices topk_ids [T, k] int32 (mk_expert_layout), without a product.
+
+    Returns dict(expert_offsets [E_local + 1], slot_of [T, k] (-1: not a local expert), row_token [T * k] of which the
+    first expert_offsets[E_local] are written, workspace); tensors given in `out` under these names receive them."""
+    what = "mk_expert_layout"
+    T, k = topk_ids.shape
+    dev = topk_ids.device
+    lib = _lib or load()
+    pi = _need(what, "topk_ids", topk_ids, dev, _I32, (T, k))
+    o, made = _outputs(what, out, dev, stream, {"expert_offsets": (_I32, (E_local + 1,)), "slot_of": (_I32, (T, k)),
+                                                "row_token": (_I32, (T * k,))})
+    if workspace is None:   # (for a shape that the call refuses the size is 0, and the call names the reason)
+        with _memory_of(stream):
+            workspace = torch.empty(max(256, lib.mk_expert_layout_workspace_bytes(T, k, E_local)), dtype=torch.uint8,
+                                    device=dev)
+        made.append(workspace)
+    pw = _need(what, "workspace", workspace, dev, torch.uint8, workspace.shape)
+    _call_on(dev, stream, lib.mk_expert_layout, what, pi, T, k, e_begin, E_local, o["slot_of"].data_ptr(),
+             o["expert_offsets"].data_ptr(), o["row_token"].data_ptr(), pw, workspace.numel())
+    _hand_over(stream, *made)
+    o["workspace"] = workspace
+    return o
+
+
+def mk_combine_backward(dout: torch.Tensor, y_perm: torch.Tensor, slot_of: torch.Tensor, topk_w: torch.Tensor, *,
+                        gates: bool = True, out: Optional[dict] = None, stream=None) -> dict:
+    """Gradient of mk_combine (mk_combine_backward) for dout [T, N] bf16: dict(dy_perm, like y_perm [rows, N]; with
+    gates=True dtopk_w [T, k] fp32).  Rows of dy_perm that no choice names are left as they were (not initialised if
+    allocated here).  Tensors given in `out` under these names receive them (dy_perm may be y_perm itself)."""
+    what = "mk_combine_backward"
+    T, N = dout.shape
+    k = slot_of.shape[1]
+    rows = y_perm.shape[0]
+    dev = dout.device
+    pd = _need(what, "dout", dout, dev, _BF16, (T, N))
+    py = _need(what, "y_perm", y_perm, dev, _BF16, (rows, N))
+    ps = _need(what, "slot_of", slot_of, dev, _I32, (T, k))
+    pw = _need(what, "topk_w", topk_w, dev, _F32, (T, k))
+    wanted = {"dy_perm": (_BF16, (rows, N))}
+    if gates:
+        wanted["dtopk_w"] = (_F32, (T, k))
+    o, made = _outputs(what, out, dev, stream, wanted)
+    _call_on(dev, stream, (_lib or load()).mk_combine_backward, what, pd, py, rows, ps, pw, T, k, N,
+             o["dy_perm"].data_ptr(), o["dtopk_w"].data_ptr() if gates else None)
+    _hand_over(stream, *made)
+    return o
+
+
+def mk_swiglu_backward(gate_up: torch.Tensor, dh: torch.Tensor, *, h: bool = False,
+                       rows_valid: Optional[torch.Tensor] = None, out: Optional[dict] = None, stream=None) -> dict:
+    """Gradient of mk_swiglu (mk_swiglu_backward) over gate_up [rows, 2F] for dh [rows, F] bf16: dict(dgate_up; with
+    h=True also h, as mk_swiglu gives it).
+
+    rows_valid: int32 tensor of one element (expert_offsets[E_local:] is one), the rows to compute (the others stay as
+    they are).  Tensors given in `out` receive the outputs (dgate_up may be gate_up, h may be dh)."""
+    what = "mk_swiglu_backward"
+    rows, F = dh.shape
+    dev = dh.device
+    pg = _need(what, "gate_up", gate_up, dev, _BF16, (rows, 2 * F))
+    pd = _need(what, "dh", dh, dev, _BF16, (rows, F))
+    pv = _may(what, "rows_valid", rows_valid, dev, _I32, (1,))
+    wanted = {"dgate_up": (_BF16, (rows, 2 * F))}
+    if h:
+        wanted["h"] = (_BF16, (rows, F))
+    o, made = _outputs(what, out, dev, stream, wanted)
+    _call_on(dev, stream, (_lib or load()).mk_swiglu_backward, what, pg, pd, rows, F, pv, o["dgate_up"].data_ptr(),
+             o["h"].data_ptr() if h else None)
+    _hand_over(stream, *made)
+    return o
+
+
+def mk_grouped_gemm_dgrad(dy: torch.Tensor, expert_offsets: torch.Tensor, w: torch.Tensor,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of mk_grouped_gemm for its rows (mk_grouped_gemm_dgrad): da[r] = bf16(W[e]^T . dy[r]) for dy [rows, N]
+    and w [E_local, N, K] bf16.  Returns da [rows, K]; rows past the last expert's are left as they were."""
+    what = "mk_grouped_gemm_dgrad"
+    E_local, N, K = w.shape
+    rows = dy.shape[0]
+    dev = dy.device
+    pd = _need(what, "dy", dy, dev, _BF16, (rows, N))
+    po = _need(what, "expert_offsets", expert_offsets, dev, _I32, (E_local + 1,))
+    pw = _need(what, "w", w, dev, _BF16, (E_local, N, K))
+    o, made = _outputs(what, {"out": out}, dev, stream, {"out": (_BF16, (rows, K))})
+    _call_on(dev, stream, (_lib or load()).mk_grouped_gemm_dgrad, what, pd, rows, po, E_local, pw, K, N,
+             o["out"].data_ptr())
+    _hand_over(stream, *made)
+    return o["out"]
+
+
+def mk_grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, expert_offsets: torch.Tensor, *,
+                          row_token: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
+                          out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Gradient of mk_grouped_gemm for the experts' weights (mk_grouped_gemm_wgrad): dw[e] = sum over e's rows of
+    dy[r]^T a[r], in fp32 or bf16.  dy [rows, N], a [rows, K] bf16, or a [T, K] with row_token [rows] int32 (the rows that
+    the dispatch read in place).  accumulate: added to `out` (fp32).  Returns dw [E_local, N, K]."""
+    what = "mk_grouped_gemm_wgrad"
+    rows, N = dy.shape
+    a_rows, K = a.shape
+    dev = dy.device
+    E_local = expert_offsets.shape[0] - 1
+    if dtype is not _F32 and dtype is not _BF16:
+        raise ValueError(f"{what}: dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+    if accumulate and out is None:
+        raise ValueError(f"{what}: accumulate needs an out to add to")
+    pd = _need(what, "dy", dy, dev, _BF16, (rows, N))
+    pa = _need(what, "a", a, dev, _BF16, (a_rows if row_token is not None else rows, K))
+    po = _need(what, "expert_offsets", expert_offsets, dev, _I32, (E_local + 1,))
+    pt = _may(what, "row_token", row_token, dev, _I32, (rows,))
+    o, made = _outputs(what, {"out": out}, dev, stream, {"out": (dtype, (E_local, N, K))})
+    _call_on(dev, stream, (_lib or load()).mk_grouped_gemm_wgrad, what, pd, pa, rows, po, E_local, pt, a_rows, K, N,
+             o["out"].data_ptr(), int(dtype is _F32), int(accumulate))
+    _hand_over(stream, *made)
+    return o["out"]
+
+
+def _quant_i8(what, x, rows, d, rows_valid, out, stream) -> dict:
+    dev = x.device
+    px = _need(what, "x" if what == "mk_quant_i8" else "gate_up", x, dev, _BF16, x.shape)
+    pv = _may(what, "rows_valid", rows_valid, dev, _I32, (1,))
+    o, made = _outputs(what, out, dev, stream, {"q": (_I8, (rows, d)), "scale": (_F32, (rows,))})
+    _call_on(dev, stream, getattr(_lib or load(), what), what, px, rows, d, pv, o["q"].data_ptr(),
+             o["scale"].data_ptr())
+    _hand_over(stream, *made)
+    return o
+
+
+def mk_quant_i8(x: torch.Tensor, *, rows_valid: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                stream=None) -> dict:
+    """Rows of 8-bit integers (mk_quant_i8) of x [rows, d] bf16: dict(q [rows, d] int8, scale [rows] fp32), x = q * scale.
+
+    rows_valid as for mk_swiglu_backward.  Tensors given in `out` under these names receive the outputs."""
+    rows, d = x.shape
+    return _quant_i8("mk_quant_i8", x, rows, d, rows_valid, out, stream)
+
+
+def mk_swiglu_i8(gate_up: torch.Tensor, *, rows_valid: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                 stream=None) -> dict:
+    """mk_quant_i8 of h = silu(g) * u of [g | u] rows [rows, 2F] bf16, h in fp32 (mk_swiglu_i8): dict(q [rows, F] int8,
+    scale [rows] fp32)."""
+    rows, F2 = gate_up.shape
+    if F2 % 2:
+        raise ValueError("mk_swiglu_i8: gate_up must have 2F columns")
+    return _quant_i8("mk_swiglu_i8", gate_up, rows, F2 // 2, rows_valid, out, stream)
+
+
+def mk_grouped_gemm_i8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: torch.Tensor, w: torch.Tensor,
+                       w_scale: torch.Tensor, *, row_token: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The grouped product of 8-bit integers (mk_grouped_gemm_i8): y[r] = bf16(a_scale * w_scale * (W[e] . a)) for the rows
+    of expert e; a [rows, K] int8 with a_scale [rows] fp32, or [T, K] and [T] with row_token [rows] int32; w
+    [E_local, N, K] int8, w_scale [E_local, N] fp32.  Returns y [rows, N] bf16; rows past the last expert's are left as
+    they were."""
+    what = "mk_grouped_gemm_i8"
+    E_local, N, K = w.shape
+    a_rows = a.shape[0]
+    rows = a_rows if row_token is None else row_token.shape[0]
+    dev = a.device
+    pa = _need(what, "a", a, dev, _I8, (a_rows, K))
+    ps = _need(what, "a_scale", a_scale, dev, _F32, (a_rows,))
+    po = _need(what, "expert_offsets", expert_offsets, dev, _I32, (E_local + 1,))
+    pw = _need(what, "w", w, dev, _I8, (E_local, N, K))
+    pc = _need(what, "w_scale", w_scale, dev, _F32, (E_local, N))
+    pt = _may(what, "row_token", row_token, dev, _I32, (rows,))
+    o, made = _outputs(what, {"out": out}, dev, stream, {"out": (_BF16, (rows, N))})
+    _call_on(dev, stream, (_lib or load()).mk_grouped_gemm_i8, what, pa, ps, rows, po, E_local, pt, a_rows, pw, pc, K,
+             N, o["out"].data_ptr())
+    _hand_over(stream, *made)
+    return o["out"]

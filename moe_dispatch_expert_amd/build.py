@@ -13,7 +13,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build", "mk")
 LIB = os.path.join(HERE, "libmk.so")
-SOURCES = ["kernels.hip", "kernels_w4.hip", "norm.hip", "layer.hip", "api.hip"]
+SOURCES = ["kernels.hip", "kernels_w4.hip", "norm.hip", "layer.hip", "grouped.hip", "backward.hip", "quant.hip",
+           "expert_layout.hip", "api.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

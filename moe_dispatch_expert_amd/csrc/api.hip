@@ -5,11 +5,13 @@
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/mk.h"
 #include "fused_dev.h"
 #include "gemm_dev.h"
+#include "grouped_args.h"
 #include "layer_args.h"
 #include "layout_dev.h"
 #include "mk_args.h"
@@ -602,6 +604,78 @@ mk_status layer_impl(const mk_shape *s, bool q8, const void *x, const void *x_q8
     return launch_layer(a, q8, self, hs) == hipSuccess ? MK_OK : MK_EHIP;
 }
 
+bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+// Whether any of the outputs (NULL ones apart) is in the place of another output or of one of the inputs.
+bool collides(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins)
+{
+    for (const void *const *o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void *const *p = outs.begin(); p != o; ++p)
+            if (*o == *p) return true;
+        for (const void *i : ins)
+            if (*o == i) return true;
+    }
+    return false;
+}
+
+bool all_aligned16(std::initializer_list<const void *> ps)
+{
+    for (const void *p : ps)
+        if (!aligned16(p)) return false;
+    return true;
+}
+
+// The chunks of mk_expert_layout: as few choices as one pass of a workgroup takes, and at most kLayoutChunks chunks.
+void layout_chunks(int64_t n, int32_t &chunk, int32_t &chunks)
+{
+    const int64_t passes = (n + 1023) / 1024;
+    chunk = (int32_t)((passes + kLayoutChunks - 1) / kLayoutChunks * 1024);
+    chunks = chunk > 0 ? (int32_t)((n + chunk - 1) / chunk) : 0;
+}
+
+mk_status check_layout_shape(int32_t T, int32_t k, int32_t e_begin, int32_t E_local)
+{
+    if (T < 0 || k < 1 || e_begin < 0 || E_local < 1) return MK_EINVAL;
+    if (k > kMaxK || E_local > kGroupedMaxE) return MK_EUNSUPPORTED;
+    if ((int64_t)T * k > 0x7FFFFFFF) return MK_EINVAL;
+    return MK_OK;
+}
+
+// The shape of a grouped product below: step is what K has to be a multiple of.
+mk_status check_grouped_shape(int32_t rows, int32_t E_local, int32_t K, int32_t N, int32_t step)
+{
+    if (rows < 0 || E_local < 1 || K <= 0 || N <= 0 || K % step != 0 || N % 8 != 0) return MK_EINVAL;
+    if (E_local > kGroupedMaxE || K > kGroupedMaxDim || N > kGroupedMaxDim) return MK_EUNSUPPORTED;
+    return MK_OK;
+}
+
+// Rows read through row_token lie in one buffer resource: their offsets have 32 bits, and the last ones mean "past it".
+mk_status check_gather(const int32_t *row_token, int32_t a_rows, int64_t row_bytes)
+{
+    if (!row_token) return MK_OK;
+    if (a_rows < 0) return MK_EINVAL;
+    return (int64_t)a_rows * row_bytes > ((int64_t)1 << 32) - 512 ? MK_EUNSUPPORTED : MK_OK;
+}
+
+mk_status quant_impl(bool swiglu, const void *x, int32_t rows, int32_t d, const int32_t *rows_valid, void *q,
+                     float *scale, void *stream)
+{
+    if (rows < 0 || d <= 0 || d % 8 != 0) return MK_EINVAL;
+    if (d > kQuantMaxD) return MK_EUNSUPPORTED;
+    if (rows == 0) return MK_OK;
+    if (!x || !q || !scale || !all_aligned16({x, q, scale}) || !aligned4(rows_valid)) return MK_EINVAL;
+    if (collides({q, scale}, {x, rows_valid})) return MK_EINVAL;
+    QuantArgs a{};
+    a.x = (const uint16_t *)x;
+    a.rows_valid = rows_valid;
+    a.q = (int8_t *)q;
+    a.scale = scale;
+    a.rows = rows;
+    a.d = d;
+    return launch_quant_i8(a, swiglu, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
 }  // namespace
 
 extern "C" {
@@ -909,6 +983,171 @@ mk_status mk_moe_layer_q8(const mk_shape *s, const void *x, const void *x_q8, co
     return layer_impl(s, true, x, x_q8, x_scale, w_router, bias, topk_ids_in, topk_w_in, w_gate_up_q8, gate_up_scale,
                       w_down_q8, down_scale, t_valid, out, topk_ids_out, topk_w_out, workspace, workspace_bytes,
                       stream);
+}
+
+size_t mk_expert_layout_workspace_bytes(int32_t T, int32_t k, int32_t E_local)
+{
+    if (check_layout_shape(T, k, 0, E_local) != MK_OK) return 0;
+    int32_t chunk, chunks;
+    layout_chunks((int64_t)T * k, chunk, chunks);
+    return align256((size_t)chunks * E_local * 4) + 256;
+}
+
+mk_status mk_expert_layout(const int32_t *topk_ids, int32_t T, int32_t k, int32_t e_begin, int32_t E_local,
+                           int32_t *slot_of, int32_t *expert_offsets, int32_t *row_token, void *workspace,
+                           size_t workspace_bytes, void *stream)
+{
+    const mk_status st = check_layout_shape(T, k, e_begin, E_local);
+    if (st != MK_OK) return st;
+    if (!expert_offsets || !workspace || (T > 0 && (!topk_ids || !slot_of))) return MK_EINVAL;
+    if (!all_aligned16({topk_ids, slot_of, expert_offsets, row_token, workspace})) return MK_EINVAL;
+    if (collides({slot_of, expert_offsets, row_token, workspace}, {topk_ids})) return MK_EINVAL;
+    if (workspace_bytes < mk_expert_layout_workspace_bytes(T, k, E_local)) return MK_EWORKSPACE;
+    LayoutArgs a{};
+    a.ids = topk_ids;
+    a.counts = (int32_t *)workspace;
+    a.offsets = expert_offsets;
+    a.slot_of = slot_of;
+    a.row_token = row_token;
+    a.n = T * k;
+    a.k = k;
+    a.e_begin = e_begin;
+    a.E = E_local;
+    layout_chunks(a.n, a.chunk, a.chunks);
+    if (a.chunks == 0) a.chunks = 1;   // no choices: the offsets alone
+    return launch_expert_layout(a, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
+mk_status mk_combine_backward(const void *dout, const void *y_perm, int32_t rows, const int32_t *slot_of,
+                              const float *topk_w, int32_t T, int32_t k, int32_t N, void *dy, float *dtopk_w,
+                              void *stream)
+{
+    if (T < 0 || k < 1 || k > kMaxK || rows < 0 || N <= 0 || N % 8 != 0) return MK_EINVAL;
+    if (T == 0) return MK_OK;
+    if (!dout || !slot_of || !topk_w || (rows > 0 && (!dy || (dtopk_w && !y_perm)))) return MK_EINVAL;
+    if (!all_aligned16({dout, y_perm, slot_of, topk_w, dy, dtopk_w})) return MK_EINVAL;
+    if (collides({dy, dtopk_w}, {dout, slot_of, topk_w}) || (dtopk_w && dtopk_w == y_perm)) return MK_EINVAL;
+    CombineBackwardArgs a{};
+    a.dout = (const uint16_t *)dout;
+    a.y = (const uint16_t *)y_perm;
+    a.slot_of = slot_of;
+    a.gate = topk_w;
+    a.dy = (uint16_t *)dy;
+    a.dgate = dtopk_w;
+    a.T = T;
+    a.k = k;
+    a.N = N;
+    a.rows = rows;
+    return launch_combine_backward(a, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
+mk_status mk_swiglu_backward(const void *gate_up, const void *dh, int32_t rows, int32_t F, const int32_t *rows_valid,
+                             void *dgate_up, void *h, void *stream)
+{
+    if (rows < 0 || F <= 0 || F % 8 != 0) return MK_EINVAL;
+    if (rows == 0) return MK_OK;
+    if (!gate_up || !dh || !dgate_up || !all_aligned16({gate_up, dh, dgate_up, h}) || !aligned4(rows_valid))
+        return MK_EINVAL;
+    if (collides({dgate_up, h}, {rows_valid}) || dgate_up == dh || (h && h == gate_up)) return MK_EINVAL;
+    SwigluBackwardArgs a{};
+    a.gu = (const uint16_t *)gate_up;
+    a.dh = (const uint16_t *)dh;
+    a.rows_valid = rows_valid;
+    a.dgu = (uint16_t *)dgate_up;
+    a.h = (uint16_t *)h;
+    a.rows = rows;
+    a.F = F;
+    return launch_swiglu_backward(a, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
+mk_status mk_grouped_gemm_dgrad(const void *dy, int32_t rows, const int32_t *expert_offsets, int32_t E_local,
+                                const void *w, int32_t K, int32_t N, void *da, void *stream)
+{
+    const mk_status st = check_grouped_shape(rows, E_local, K, N, 8);
+    if (st != MK_OK) return st;
+    if (rows == 0) return MK_OK;
+    if (!dy || !expert_offsets || !w || !da || !all_aligned16({dy, expert_offsets, w, da})) return MK_EINVAL;
+    if (collides({da}, {dy, expert_offsets, w})) return MK_EINVAL;
+    GroupedArgs a{};
+    a.dy = (const uint16_t *)dy;
+    a.rows = rows;
+    a.offsets = expert_offsets;
+    a.E = E_local;
+    a.w = w;
+    a.K = K;
+    a.N = N;
+    a.out = da;
+    return launch_grouped_dgrad(a, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
+mk_status mk_grouped_gemm_wgrad(const void *dy, const void *a, int32_t rows, const int32_t *expert_offsets,
+                                int32_t E_local, const int32_t *row_token, int32_t a_rows, int32_t K, int32_t N,
+                                void *dw, int32_t dw_fp32, int32_t accumulate, void *stream)
+{
+    mk_status st = check_grouped_shape(rows, E_local, K, N, 8);
+    if (st != MK_OK) return st;
+    if (dw_fp32 < 0 || dw_fp32 > 1 || accumulate < 0 || accumulate > 1 || (accumulate && !dw_fp32)) return MK_EINVAL;
+    st = check_gather(row_token, a_rows, (int64_t)K * 2);
+    if (st != MK_OK) return st;
+    if (!expert_offsets || !dw || (rows > 0 && (!dy || (!a && !(row_token && a_rows == 0))))) return MK_EINVAL;
+    if (!all_aligned16({dy, a, expert_offsets, row_token, dw})) return MK_EINVAL;
+    if (collides({dw}, {dy, a, expert_offsets, row_token})) return MK_EINVAL;
+    GroupedArgs g{};
+    g.dy = (const uint16_t *)dy;
+    g.a = a;
+    g.rows = rows;
+    g.offsets = expert_offsets;
+    g.E = E_local;
+    g.row_token = row_token;
+    g.a_rows = row_token ? a_rows : rows;
+    g.K = K;
+    g.N = N;
+    g.out = dw;
+    g.out_f32 = dw_fp32;
+    g.accumulate = accumulate;
+    return launch_grouped_wgrad(g, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
+}
+
+mk_status mk_quant_i8(const void *x, int32_t rows, int32_t d, const int32_t *rows_valid, void *q, float *scale,
+                      void *stream)
+{
+    return quant_impl(false, x, rows, d, rows_valid, q, scale, stream);
+}
+
+mk_status mk_swiglu_i8(const void *gate_up, int32_t rows, int32_t F, const int32_t *rows_valid, void *q, float *scale,
+                       void *stream)
+{
+    return quant_impl(true, gate_up, rows, F, rows_valid, q, scale, stream);
+}
+
+mk_status mk_grouped_gemm_i8(const void *a, const float *a_scale, int32_t rows, const int32_t *expert_offsets,
+                             int32_t E_local, const int32_t *row_token, int32_t a_rows, const void *w,
+                             const float *w_scale, int32_t K, int32_t N, void *y, void *stream)
+{
+    mk_status st = check_grouped_shape(rows, E_local, K, N, 16);
+    if (st != MK_OK) return st;
+    if (K >= kI8MaxK) return MK_EUNSUPPORTED;
+    st = check_gather(row_token, a_rows, K);
+    if (st != MK_OK) return st;
+    if (rows == 0) return MK_OK;
+    const bool none = row_token && a_rows == 0;
+    if (!expert_offsets || !w || !w_scale || !y || (!none && (!a || !a_scale))) return MK_EINVAL;
+    if (!all_aligned16({a, a_scale, expert_offsets, row_token, w, w_scale, y})) return MK_EINVAL;
+    if (collides({y}, {a, a_scale, expert_offsets, row_token, w, w_scale})) return MK_EINVAL;
+    GroupedArgs g{};
+    g.a = a;
+    g.a_scale = a_scale;
+    g.rows = rows;
+    g.offsets = expert_offsets;
+    g.E = E_local;
+    g.row_token = row_token;
+    g.a_rows = row_token ? a_rows : rows;
+    g.w = w;
+    g.w_scale = w_scale;
+    g.K = K;
+    g.N = N;
+    g.out = y;
+    return launch_grouped_i8(g, (hipStream_t)stream) == hipSuccess ? MK_OK : MK_EHIP;
 }
 
 mk_status mk_poll_error(void *workspace, int32_t *detail)

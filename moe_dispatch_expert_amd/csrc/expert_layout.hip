@@ -1,0 +1,133 @@
+// expert_layout.hip -- the expert layout of given choices: a stable counting sort by expert.
+//
+//   offsets[e] = choices of experts before e,   slot(t, j) = offsets[e] + earlier choices (t', j') < (t, j) of the same e
+//
+// Two launches over chunks of choices, one workgroup each (one launch if there is one chunk): the first counts each
+// chunk's choices by expert; in the second every workgroup sums the counts up (totals for the offsets, earlier chunks for
+// its base) and ranks its own choices, 64 at a time per wave: the lanes of a wave that hold the same expert find one
+// another by one ballot per bit of the expert's number.  Bound by latency: a few thousand choices are a few KB.
+#include <hip/hip_runtime.h>
+
+#include "grouped_args.h"
+#include "mk_device.h"
+#include "mk_launch.h"
+
+namespace mk {
+
+namespace {
+
+constexpr int kLayoutThreads = 1024, kLayoutWaves = kLayoutThreads / kWave;
+
+// The local expert of choice i, or -1.
+__device__ __forceinline__ int local_expert(const LayoutArgs &a, int64_t i, int64_t end)
+{
+    if (i >= end) return -1;
+    const int64_t e = (int64_t)a.ids[i] - a.e_begin;
+    return e >= 0 && e < a.E ? (int)e : -1;
+}
+
+}  // namespace
+
+__global__ __launch_bounds__(kLayoutThreads) void k_layout_count(LayoutArgs a)
+{
+    __shared__ int32_t cnt[kGroupedMaxE];
+    for (int e = (int)threadIdx.x; e < a.E; e += kLayoutThreads) cnt[e] = 0;
+    __syncthreads();
+    const int64_t i0 = (int64_t)blockIdx.x * a.chunk, end = min(i0 + a.chunk, (int64_t)a.n);
+    for (int64_t i = i0 + threadIdx.x; i < end; i += kLayoutThreads) {
+        const int e = local_expert(a, i, end);
+        if (e >= 0) atomicAdd(&cnt[e], 1);
+    }
+    __syncthreads();
+    for (int e = (int)threadIdx.x; e < a.E; e += kLayoutThreads) a.counts[(size_t)blockIdx.x * a.E + e] = cnt[e];
+}
+
+__global__ __launch_bounds__(kLayoutThreads) void k_layout_slots(LayoutArgs a)
+{
+    __shared__ int32_t next[kGroupedMaxE];                        // next slot of every expert
+    __shared__ int32_t scan[kGroupedMaxE];
+    __shared__ uint8_t wcnt[kLayoutWaves][kGroupedMaxE];          // choices of each wave's 64 by expert (at most 64)
+    const int ti = (int)threadIdx.x, lane = ti % kWave, wave = ti / kWave;
+    const int chunk = (int)blockIdx.x;
+    const int64_t i0 = (int64_t)chunk * a.chunk, end = min(i0 + a.chunk, (int64_t)a.n);
+    // totals and what earlier chunks hold of expert ti
+    int total = 0, before = 0;
+    if (a.chunks == 1) {
+        scan[ti] = 0;
+        __syncthreads();
+        for (int64_t i = i0 + ti; i < end; i += kLayoutThreads) {
+            const int e = local_expert(a, i, end);
+            if (e >= 0) atomicAdd(&scan[e], 1);
+        }
+        __syncthreads();
+        total = scan[ti];
+        __syncthreads();
+    } else if (ti < a.E) {
+        constexpr int kB = 16;   // loads in flight
+        for (int c0 = 0; c0 < a.chunks; c0 += kB) {
+            int v[kB];
+#pragma unroll
+            for (int j = 0; j < kB; ++j) v[j] = c0 + j < a.chunks ? a.counts[(size_t)(c0 + j) * a.E + ti] : 0;
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+                total += v[j];
+                before += c0 + j < chunk ? v[j] : 0;
+            }
+        }
+    }
+    scan[ti] = total;
+    __syncthreads();
+    for (int off = 1; off < kLayoutThreads; off <<= 1) {
+        const int v = ti >= off ? scan[ti - off] : 0;
+        __syncthreads();
+        scan[ti] += v;
+        __syncthreads();
+    }
+    if (ti < a.E) {
+        next[ti] = scan[ti] - total + before;
+        if (chunk == 0) {
+            a.offsets[ti + 1] = scan[ti];
+            if (ti == 0) a.offsets[0] = 0;
+        }
+    }
+    const int bits = a.E > 1 ? 32 - __clz(a.E - 1) : 0;
+    for (int64_t b = i0; b < end; b += kLayoutThreads) {
+        for (int i = ti; i < kLayoutWaves * kGroupedMaxE / 4; i += kLayoutThreads) ((uint32_t *)wcnt)[i] = 0u;
+        __syncthreads();
+        const int64_t i = b + ti;
+        const int e = local_expert(a, i, end);
+        uint64_t same = __ballot(e >= 0);
+        for (int bit = 0; bit < bits; ++bit) {
+            const bool one = (e >> bit) & 1;
+            const uint64_t m = __ballot(one);
+            same &= one ? m : ~m;
+        }
+        const int rank = __popcll(same & lanemask_lt());
+        if (e >= 0 && rank == 0) wcnt[wave][e] = (uint8_t)__popcll(same);
+        __syncthreads();
+        int slot = -1;
+        if (e >= 0) {
+            slot = next[e] + rank;
+            for (int w = 0; w < wave; ++w) slot += wcnt[w][e];
+            if (a.row_token) a.row_token[slot] = (int32_t)(i / a.k);
+        }
+        if (i < end) a.slot_of[i] = slot;
+        __syncthreads();
+        if (ti < a.E)
+            for (int w = 0; w < kLayoutWaves; ++w) next[ti] += wcnt[w][ti];
+        __syncthreads();
+    }
+}
+
+hipError_t launch_expert_layout(const LayoutArgs &a, hipStream_t s)
+{
+    if (a.chunks > 1) {
+        hipLaunchKernelGGL(k_layout_count, dim3(a.chunks), dim3(kLayoutThreads), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(k_layout_slots, dim3(a.chunks), dim3(kLayoutThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace mk

@@ -17,6 +17,11 @@ struct FusedArgs;
 struct WsHeader;
 struct NormArgs;
 struct LayerArgs;
+struct GroupedArgs;
+struct CombineBackwardArgs;
+struct SwigluBackwardArgs;
+struct QuantArgs;
+struct LayoutArgs;
 
 // Router partial sums, one wave task per wave (router_tasks).
 hipError_t launch_router(const RouterArgs &a, hipStream_t s);
@@ -58,5 +63,15 @@ hipError_t launch_add_rmsnorm(const NormArgs &a, hipStream_t s);
 // the experts from the router's partial sums).
 hipError_t launch_layer_router(const LayerArgs &a, hipStream_t s);
 hipError_t launch_layer(const LayerArgs &a, bool q8, bool self, hipStream_t s);
+// The grouped product's gradients and its form of 8-bit integers.
+hipError_t launch_grouped_dgrad(const GroupedArgs &a, hipStream_t s);
+hipError_t launch_grouped_wgrad(const GroupedArgs &a, hipStream_t s);
+hipError_t launch_grouped_i8(const GroupedArgs &a, hipStream_t s);
+// The gradients of the combine and the SwiGLU; 8-bit rows (swiglu: of the SwiGLU of gate|up rows; d <= kQuantMaxD); the
+// expert layout of given choices.
+hipError_t launch_combine_backward(const CombineBackwardArgs &a, hipStream_t s);
+hipError_t launch_swiglu_backward(const SwigluBackwardArgs &a, hipStream_t s);
+hipError_t launch_quant_i8(const QuantArgs &a, bool swiglu, hipStream_t s);
+hipError_t launch_expert_layout(const LayoutArgs &a, hipStream_t s);
 
 }  // namespace mk
