@@ -1,0 +1,518 @@
+// grouped_dev.h -- the tile of the grouped product's gradients (bf16) and of its 8-bit form, on gfx950 matrix cores.
+//
+// A workgroup of eight waves computes BM rows x 256 columns of
+//   out[m, n] = sum_l Q[m, l] P[n, l]
+// P is the matrix instructions' A operand, so a lane ends with four neighbouring columns of a row.  The three products
+// differ in which index of an operand is contiguous in memory:
+//   dgrad  out = da,    P[i, n] = W[e, n, i] (rows along the contraction),  Q[r, n] = dy[r, n] (contraction contiguous)
+//   wgrad  out = dW[e], P[i, r] = a[r, i] and Q[n, r] = dy[r, n] (rows along the contraction both)
+//   8-bit  out = y,     P[n, i] = w[e, n, i] and Q[r, i] = a[r, i] (contraction contiguous both)
+// The contraction runs in slabs of 128 bytes of an operand's row (64 bf16, 128 int8), straight from memory into LDS
+// (buffer_load ... lds, 1 KiB a load), two slabs in flight; four matrix instruction steps a slab, the fragments of step
+// s + 1 read during the products of step s, one barrier a slab, before its last step.
+//   - Contraction contiguous: LDS rows of 128 bytes, 16-byte chunk c of row r at c ^ ((r >> 1) & 7); a fragment is one
+//     16-byte read.
+//   - Rows along the contraction: 64 LDS rows of 2 C bytes, 16-byte unit u of row r at u ^ 4 (r & 3); a fragment is two
+//     transposing reads (ds_read_b64_tr_b16: 16 lanes hold 4 rows x 16 columns and each gets a column's 4 values), whose
+//     4 rows x 64 bytes then lie on different banks.
+// Every load is checked lane by lane against the tile's rows or columns and the slab's rest of the contraction: a lane
+// outside gets an offset past the resource, which reads zeros without a memory access, so ragged ends add exact zeros
+// whatever lies behind them.
+#pragma once
+
+#include "gemm_dev.h"
+#include "grouped_args.h"
+
+namespace mk {
+
+enum { kDgrad = 0, kWgrad = 1, kI8 = 2 };
+
+typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
+typedef int32_t i32x16_t __attribute__((ext_vector_type(16)));
+typedef int16_t i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef __attribute__((address_space(3))) const i32x4_t lds_ci32x4_t;
+
+constexpr int kGroupedThreads = 512, kGroupedWaves = 8;
+constexpr int kStageBytes = 32768;                  // one operand's slab
+constexpr int kGroupedStages = 4 * kStageBytes;     // P of both stages, then Q of both
+constexpr int kPlainRecords = (int)0x80000000u;     // of resources whose offsets all lie below 2 GiB
+
+// The tile: BM rows by 256 columns, the waves WN along the columns and 8 / WN along the rows.
+template <int KIND_, int BM_>
+struct GTile {
+    static constexpr int KIND = KIND_, BM = BM_, BN = 256;
+    static constexpr int WN = BM >= 128 ? 2 : (BM == 64 ? 4 : 8), WM = kGroupedWaves / WN;
+    static constexpr int NI = BN / WN / 32, MI = BM / WM / 32;
+    static constexpr bool PKR = KIND != kI8, QKR = KIND == kWgrad;   // rows along the contraction
+    static constexpr int ESZ = KIND == kI8 ? 1 : 2;                  // bytes of an element
+    static constexpr int L = 128 / ESZ;                              // contraction per slab
+    static_assert(NI >= 1 && MI >= 1, "tile shape");
+};
+
+// The lane as a value of its own: what a tile computes from it stays in the tile, or in its epilogue.  (Otherwise the compiler
+// keeps the offsets of every tile height in registers throughout the task loop, and spills the tile's.)
+__device__ __forceinline__ int fresh_lane(int lane)
+{
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// One operand of a tile: C rows (or columns) of it, and this lane's part of its loads.
+template <bool KR, int C>
+struct Side {
+    static constexpr int RB = 2 * C;                         // KR: bytes of an LDS row
+    static constexpr int RPL = 1024 / RB;                    // KR: rows a load
+    static constexpr int SLOTS = KR ? 64 / RPL / kGroupedWaves : (C / 8 + kGroupedWaves - 1) / kGroupedWaves;
+    uint32_t off[SLOTS];   // byte offsets in the resource (kPastResource: nothing to read)
+    int pos;               // place in the slab: KR the row of slot 0, else the byte
+    uint64_t base;         // KR: of the next slab to load
+    uint64_t step;         // KR: bytes between slabs
+    rsrc4_t rs;            // not KR: the resource
+};
+
+// Contraction contiguous: LDS block b = wave + 8 slot holds rows 8 b .. 8 b + 7; row(i) gives the byte offset of the
+// operand's row i, or kPastResource.
+template <class S, class F>
+__device__ __forceinline__ void side_rows(S &s, rsrc4_t rs, int wave, int lane, F &&row)
+{
+    const uint32_t c = dma_chunk_bytes(wave, lane);
+#pragma unroll
+    for (int i = 0; i < S::SLOTS; ++i) {
+        const uint32_t o = row((wave + kGroupedWaves * i) * 8 + (lane >> 3));
+        s.off[i] = o == kPastResource ? o : o + c;
+    }
+    s.pos = (int)c;
+    s.rs = rs;
+}
+
+// Rows along the contraction: LDS block b = wave + 8 slot holds rows b RPL ..; base: the tile's first column of row 0,
+// ld: bytes between rows, cols: columns there are.  (gather: off holds the column's part alone.)
+template <class S>
+__device__ __forceinline__ void side_columns(S &s, const void *base, uint64_t ld, int cols, bool gather, int wave, int lane)
+{
+    constexpr int UPR = S::RB / 16;
+    const int r0 = lane / UPR;   // row of the block
+    const int u = (lane % UPR) ^ (((S::RPL * wave + r0) & 3) << 2);   // (8 RPL is a multiple of 4: the same in every slot)
+#pragma unroll
+    for (int i = 0; i < S::SLOTS; ++i) {
+        const int row = (wave + kGroupedWaves * i) * S::RPL + r0;
+        s.off[i] = u * 8 < cols ? (gather ? 0u : (uint32_t)row * (uint32_t)ld) + (uint32_t)u * 16u : kPastResource;
+    }
+    s.pos = wave * S::RPL + r0;
+    s.base = (uint64_t)base;
+    s.step = 64 * ld;
+}
+
+__device__ __forceinline__ rsrc4_t slab_rsrc(uint64_t base, uint32_t records)
+{
+    return rsrc4_t{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)base),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(base >> 32) & 0xFFFFu), records, 0x00020000u};
+}
+
+// Load slot i of a slab into the stage at `lds`; rest: what is left of the contraction from the slab's start (rows of KR,
+// else bytes; <= 0: nothing).  tok (GATHER): this lane's row of `a`.
+template <bool GATHER, bool KR, int C>
+__device__ __forceinline__ void side_load(const Side<KR, C> &s, rsrc4_t rs, int i, int slab, int rest, int tok,
+                                          uint32_t row_bytes, lds_char_t *lds, int wave)
+{
+    typedef Side<KR, C> S;
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds + (wave + kGroupedWaves * i) * 1024));
+    if constexpr (KR) {
+        uint32_t o = s.off[i];
+        bool ok = s.pos + kGroupedWaves * S::RPL * i < rest;
+        if constexpr (GATHER) {
+            ok = ok & (tok >= 0) & (o != kPastResource);
+            o += (uint32_t)tok * row_bytes;
+        }
+        lds_load16(rs, at, ok ? o : kPastResource, 0u);
+    } else {
+        lds_load16(rs, at, s.pos < rest ? s.off[i] : kPastResource,
+                   __builtin_amdgcn_readfirstlane((uint32_t)slab * 128u));
+    }
+}
+
+// Where this lane's fragments start in a stage.  Contraction contiguous: by step of the slab; rows along it: by block of
+// 32 columns (block q of the operand: q0 + index).
+template <bool KR, int C, int NB>
+__device__ __forceinline__ void frag_bases(lds_char_t *stage, int q0, int lane, lds_char_t *(&b)[4])
+{
+    b[0] = b[1] = b[2] = b[3] = stage;
+    if constexpr (KR) {
+        constexpr int RB = 2 * C;
+        const int i = lane & 15;
+        const int row = 8 * (lane >> 5) + (i >> 2);
+        const int low = (2 * ((lane >> 4) & 1) + ((i & 3) >> 1)) * 16 + 8 * (i & 1);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const int q = q0 + n;
+            int o = row * RB + ((q & ~3) << 6) + (((q & 3) ^ (i >> 2)) << 6) + low;
+            asm volatile("" : "+v"(o));   // computed once, kept in a register
+            b[n] = stage + o;
+        }
+    } else {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            int o = (lane & 31) * 128 + (((2 * kk + (lane >> 5)) ^ (((lane & 31) >> 1) & 7)) << 4);
+            asm volatile("" : "+v"(o));
+            b[kk] = stage + q0 * 32 * 128 + o;
+        }
+    }
+}
+
+// Half t of fragment n of step kk from the stage that b points into (t = 0 alone with the contraction contiguous).
+template <bool KR, int C>
+__device__ __forceinline__ void read_half(lds_char_t *const (&b)[4], int n, int t, int kk, i32x4_t &f)
+{
+    if constexpr (KR) {
+        const i16x4_t v =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(b[n] + (16 * kk + 4 * t) * 2 * C));
+        const u32x2_t w = __builtin_bit_cast(u32x2_t, v);
+        f[2 * t] = (int32_t)w[0];
+        f[2 * t + 1] = (int32_t)w[1];
+    } else {
+        f = *(lds_ci32x4_t *)(b[kk] + n * 32 * 128);
+    }
+}
+
+template <int KIND>
+struct Acc {
+    typedef f32x16_t type;
+};
+template <>
+struct Acc<kI8> {
+    typedef i32x16_t type;
+};
+
+__device__ __forceinline__ void product(i32x4_t p, i32x4_t q, f32x16_t &acc)
+{
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, p), __builtin_bit_cast(bf16x8_t, q), acc,
+                                                  0, 0, 0);
+}
+__device__ __forceinline__ void product(i32x4_t p, i32x4_t q, i32x16_t &acc)
+{
+    acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(p, q, acc, 0, 0, 0);
+}
+
+// The sums of a tile: acc[i][j], lane: column 32 i + 8 (v / 4) + 4 (lane / 32) + v % 4 of the wave's columns, row
+// 32 j + lane % 32 of its rows.  len: the contraction's length in elements.  toks(slab, ids): the rows of `a` that this lane
+// loads of a slab (wgrad with a gather; null otherwise).
+template <class T, bool GATHER, class SP, class SQ, class TOK>
+__device__ __forceinline__ void tile_sums(SP &sp, SQ &sq, int len, uint32_t records_p, uint32_t row_bytes,
+                                          TOK &&toks, lds_char_t *lds, int wave, int lane,
+                                          typename Acc<T::KIND>::type (&acc)[T::NI][T::MI])
+{
+    constexpr int CP = T::BN, CQ = T::BM;
+    constexpr int NH = T::PKR ? 2 : 1, MH = T::QKR ? 2 : 1;    // reads a fragment
+    constexpr int NR = T::NI * NH + T::MI * MH;                // reads a step
+    constexpr int NM = T::NI * T::MI;                          // products a step
+    constexpr int NL = SP::SLOTS + SQ::SLOTS;                  // loads a slab
+    const int wn = wave % T::WN, wm = wave / T::WN;
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::MI; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    const int KK = __builtin_amdgcn_readfirstlane((len + T::L - 1) / T::L);
+    if (KK == 0) return;
+    lds_char_t *bp[4], *bq[4];
+    frag_bases<T::PKR, CP, T::NI>(lds, wn * T::NI, lane, bp);
+    frag_bases<T::QKR, CQ, T::MI>(lds + 2 * kStageBytes, wm * T::MI, lane, bq);
+    int ids[SP::SLOTS];
+    rsrc4_t rp, rq;
+    // the resources of the next slab (in order: 0, 1, ...)
+    auto next_slab = [&]() {
+        if constexpr (T::PKR) {
+            rp = slab_rsrc(sp.base, records_p);
+            if constexpr (!GATHER) sp.base += sp.step;
+        } else {
+            rp = sp.rs;
+        }
+        if constexpr (T::QKR) {
+            rq = slab_rsrc(sq.base, kPlainRecords);
+            sq.base += sq.step;
+        } else {
+            rq = sq.rs;
+        }
+    };
+    auto load = [&](int i, int slab, int st) {
+        const int restp = T::PKR ? len - slab * 64 : (len - slab * T::L) * T::ESZ;
+        const int restq = T::QKR ? len - slab * 64 : (len - slab * T::L) * T::ESZ;
+        if (i < SP::SLOTS) side_load<GATHER>(sp, rp, i, slab, restp, GATHER ? ids[i] : 0, row_bytes, lds + st, wave);
+        else side_load<false>(sq, rq, i - SP::SLOTS, slab, restq, 0, 0u, lds + 2 * kStageBytes + st, wave);
+    };
+    for (int s = 0; s < 2; ++s) {
+        toks(s, ids);
+        next_slab();
+#pragma unroll
+        for (int i = 0; i < NL; ++i) load(i, s, s * kStageBytes);
+    }
+    toks(2, ids);
+    wait_vmem_all();
+    __syncthreads();
+
+    i32x4_t fp0[T::NI], fq0[T::MI], fp1[T::NI], fq1[T::MI];
+    // read r of a step, in the order in which the products need them: P 0, the Q, the other P
+    auto rd = [&](int r, int kk, i32x4_t (&fp)[T::NI], i32x4_t (&fq)[T::MI]) {
+        if (r < NH) read_half<T::PKR, CP>(bp, 0, r, kk, fp[0]);
+        else if (r < NH + T::MI * MH) read_half<T::QKR, CQ>(bq, (r - NH) / MH, (r - NH) % MH, kk, fq[(r - NH) / MH]);
+        else {
+            const int n = (r - T::MI * MH) / NH;
+            read_half<T::PKR, CP>(bp, n, (r - T::MI * MH) % NH, kk, fp[n]);
+        }
+    };
+    // the products of a step on (fp, fq), with the reads of the next one and a slab's loads spread over them
+    auto step = [&](const i32x4_t (&fp)[T::NI], const i32x4_t (&fq)[T::MI], auto &&reads, int nld, auto &&loads) {
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            product(fp[q / T::MI], fq[q % T::MI], acc[q / T::MI][q % T::MI]);
+#pragma unroll
+            for (int i = q * nld / NM; i < (q + 1) * nld / NM; ++i) loads(i);
+#pragma unroll
+            for (int r = q * NR / NM; r < (q + 1) * NR / NM; ++r) reads(r);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < NR; ++r) rd(r, 0, fp0, fq0);
+    auto none = [](int) {};
+    // Slab j in stage j % 2; slab j + 2 goes into the stage during the last step.  After the last slab the same steps read a
+    // stage that nothing was loaded into, and their loads have nothing left to read: cheaper than forms of their own, whose
+    // different exits cost copies of the sums.
+    int flip = kStageBytes;   // from this stage to the other one
+    int cur = 0;
+    for (int j = 0; j < KK; ++j) {
+        step(fp0, fq0, [&](int r) { rd(r, 1, fp1, fq1); }, 0, none);
+        step(fp1, fq1, [&](int r) { rd(r, 2, fp0, fq0); }, 0, none);
+        step(fp0, fq0, [&](int r) { rd(r, 3, fp1, fq1); }, 0, none);
+        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0): slab j + 1 and the last step's fragments are here
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            bp[n] += flip;
+            bq[n] += flip;
+        }
+        next_slab();
+        step(fp1, fq1, [&](int r) { rd(r, 0, fp0, fq0); }, NL, [&](int i) { load(i, j + 2, cur); });
+        toks(j + 3, ids);
+        cur = __builtin_amdgcn_readfirstlane(cur + flip);
+        flip = -flip;
+    }
+    // A distance between the last product and the first read of its sums that does not depend on the schedule (see
+    // gemm_tile_big); no load may still be on its way into LDS.
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7");
+#pragma unroll
+    for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+        for (int k = 0; k < T::MI; ++k) asm volatile("" : "+a"(acc[i][k]));
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmem_all();
+}
+
+// Stores a wave's rows through its own 16 KiB of LDS (every wave is done with the stages), so that memory sees whole
+// segments: 64 NI bytes of bf16 a row, ...
+template <class T, class F>
+__device__ __forceinline__ void store_bf16(F &&value, uint16_t *out, int64_t ldc, int rows, int cols, lds_char_t *lds,
+                                           int wave, int lane)
+{
+    constexpr int RB = 64 * T::NI, CH = RB / 16;          // bytes and 16-byte chunks of a wave's row
+    constexpr int RPI = 64 / CH;                          // rows an instruction
+    lds_char_t *mine = lds + wave * 16384;
+    lane = fresh_lane(lane);
+#pragma unroll
+    for (int j = 0; j < T::MI; ++j) {
+        const int m = j * 32 + (lane & 31);
+#pragma unroll
+        for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                typedef __attribute__((address_space(3))) u32x2_t lds_u32x2_t;
+                *(lds_u32x2_t *)(mine + m * RB + (((4 * i + g) ^ (m & (CH - 1))) << 4) + ((lane >> 5) << 3)) =
+                    u32x2_t{pack_bf16x2(value(i, j, 4 * g), value(i, j, 4 * g + 1)),
+                            pack_bf16x2(value(i, j, 4 * g + 2), value(i, j, 4 * g + 3))};
+            }
+    }
+    const int wn = wave % T::WN, wm = wave / T::WN;
+    const int c = lane % CH, n = wn * (T::BN / T::WN) + 8 * c, m0 = wm * (T::BM / T::WM);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(out, (size_t)0x80000000u);
+#pragma unroll
+    for (int r = 0; r < 32 * T::MI; r += RPI) {
+        const int m = r + lane / CH;
+        const v4i_t v = *(__attribute__((address_space(3))) const v4i_t *)(mine + m * RB + ((c ^ (m & (CH - 1))) << 4));
+        if (m0 + m < rows && n < cols)
+            __builtin_amdgcn_raw_buffer_store_b128(v, rs, (uint32_t)(m0 + m) * (uint32_t)(ldc * 2) + n * 2, 0, kStoreNT);
+    }
+}
+
+// ... or 128 NI bytes of fp32, 32 rows at a time, added to what is there where add is set.
+template <class T, class F>
+__device__ __forceinline__ void store_f32(F &&value, float *out, int64_t ldc, int rows, int cols, bool add,
+                                          lds_char_t *lds, int wave, int lane)
+{
+    constexpr int RB = 128 * T::NI, CH = RB / 16, RPI = 64 / CH;
+    lds_char_t *mine = lds + wave * 16384;
+    lane = fresh_lane(lane);
+    const int wn = wave % T::WN, wm = wave / T::WN;
+    const int c = lane % CH, n = wn * (T::BN / T::WN) + 4 * c;
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(out, (size_t)0xFFFFFFF0u);
+#pragma unroll
+    for (int j = 0; j < T::MI; ++j) {
+        const int w = lane & 31;
+#pragma unroll
+        for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                typedef __attribute__((address_space(3))) f32x4_t lds_f32x4_t;
+                *(lds_f32x4_t *)(mine + w * RB + (((8 * i + 2 * g + (lane >> 5)) ^ (w & (CH - 1))) << 4)) =
+                    f32x4_t{value(i, j, 4 * g), value(i, j, 4 * g + 1), value(i, j, 4 * g + 2), value(i, j, 4 * g + 3)};
+            }
+        const int m0 = wm * (T::BM / T::WM) + 32 * j;
+        constexpr int BATCH = 32 / RPI < 8 ? 32 / RPI : 8;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += RPI * BATCH) {
+            f32x4_t v[BATCH], o[BATCH];
+            uint32_t at[BATCH];
+            bool ok[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const int m = r0 + b * RPI + lane / CH;
+                ok[b] = m0 + m < rows && n < cols;
+                at[b] = (uint32_t)(m0 + m) * (uint32_t)(ldc * 4) + (uint32_t)n * 4u;
+                v[b] = *(__attribute__((address_space(3))) const f32x4_t *)(mine + m * RB + ((c ^ (m & (CH - 1))) << 4));
+                if (add)
+                    o[b] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                           rs, ok[b] ? at[b] : 0xFFFFFFF8u, 0, kStoreNT));
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                if (add) v[b] += o[b];
+                if (ok[b]) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i_t, v[b]), rs, at[b], 0, kStoreNT);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------ which tiles there are
+
+// Tables of a launch, in LDS behind the stages.  Every workgroup makes them from the offsets.
+struct GroupedTables {
+    int32_t off[kGroupedMaxE + 1];     // clamped offsets
+    int32_t tall[kGroupedMaxE + 1];    // rows of tiles: how many of more than 128 rows lie before expert e ...
+    int32_t low[kGroupedMaxE + 1];     // ... and how many short ones (the rest of an expert, if 128 rows or fewer);
+                                       // wgrad: low[i] = the expert with the i-th most rows
+    int32_t wave_sum[2][kGroupedWaves];
+};
+static_assert(kGroupedStages + sizeof(GroupedTables) <= 160 * 1024, "LDS");
+
+__device__ __forceinline__ void tables_offsets(const GroupedArgs &a, GroupedTables &t)
+{
+    for (int e = (int)threadIdx.x; e <= a.E; e += kGroupedThreads) t.off[e] = min(max(a.offsets[e], 0), a.rows);
+    __syncthreads();
+}
+
+// Rows of expert e (offsets that do not ascend, which the caller must not give, count as no rows).
+__device__ __forceinline__ int table_count(const GroupedTables &t, int e) { return max(t.off[e + 1] - t.off[e], 0); }
+
+__device__ __forceinline__ void tables_rows(const GroupedArgs &a, GroupedTables &t)
+{
+    tables_offsets(a, t);
+    const int ti = (int)threadIdx.x, lane = ti % kWave, wave = ti / kWave;
+    int n[2][2];   // thread: experts 2 ti and 2 ti + 1
+    int sum[2] = {0, 0};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = 2 * ti + h;
+        const int cnt = e < a.E ? table_count(t, e) : 0, rest = cnt % 256;
+        n[h][0] = cnt / 256 + (rest > 128);
+        n[h][1] = rest > 0 && rest <= 128;
+        sum[0] += n[h][0];
+        sum[1] += n[h][1];
+    }
+    int inc[2] = {sum[0], sum[1]};
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int v = __shfl_up(inc[k], d);
+            if (lane >= d) inc[k] += v;
+        }
+    }
+    if (lane == kWave - 1) {
+        t.wave_sum[0][wave] = inc[0];
+        t.wave_sum[1][wave] = inc[1];
+    }
+    __syncthreads();
+    int at[2] = {inc[0] - sum[0], inc[1] - sum[1]};
+    for (int w = 0; w < wave; ++w) {
+        at[0] += t.wave_sum[0][w];
+        at[1] += t.wave_sum[1][w];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = 2 * ti + h;
+        if (e < a.E) {
+            t.tall[e] = at[0];
+            t.low[e] = at[1];
+            if (e == a.E - 1) {
+                t.tall[a.E] = at[0] + n[h][0];
+                t.low[a.E] = at[1] + n[h][1];
+            }
+        }
+        at[0] += n[h][0];
+        at[1] += n[h][1];
+    }
+    __syncthreads();
+}
+
+// The expert of tile row q of a prefix table (the last e with pre[e] <= q).
+__device__ __forceinline__ int table_expert(const int32_t *pre, int E, int64_t q)
+{
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= q) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+struct GroupedJob {
+    int e, row0, rows, col0;
+};
+
+// Task q of the rows' products: tall tiles first, expert by expert, in groups of up to 8 row tiles that go through the
+// columns together (the 32 workgroups of an XCD then share 8 row tiles and 4 column tiles in its L2); the short ones after
+// all of them, so that the last round is made of short tasks.
+__device__ __forceinline__ GroupedJob rows_job(const GroupedArgs &a, const GroupedTables &t, int cols, int64_t q)
+{
+    GroupedJob j;
+    const int64_t tall = (int64_t)t.tall[a.E] * cols;
+    if (q < tall) {
+        j.e = table_expert(t.tall, a.E, q / cols);
+        const int64_t r = q - (int64_t)t.tall[j.e] * cols;
+        const int n = t.tall[j.e + 1] - t.tall[j.e];
+        const int group = (int)(r / (8 * cols)), in = (int)(r - (int64_t)group * 8 * cols);
+        const int size = min(8, n - 8 * group);
+        j.col0 = in / size * 256;
+        j.row0 = (8 * group + in % size) * 256;
+    } else {
+        const int64_t r = q - tall;
+        j.e = table_expert(t.low, a.E, r / cols);
+        j.col0 = (int)(r - (int64_t)t.low[j.e] * cols) * 256;
+        j.row0 = (t.tall[j.e + 1] - t.tall[j.e]) * 256;
+    }
+    j.rows = min(table_count(t, j.e) - j.row0, 256);
+    j.row0 += t.off[j.e];
+    j.e = __builtin_amdgcn_readfirstlane(j.e);
+    j.row0 = __builtin_amdgcn_readfirstlane(j.row0);
+    j.rows = __builtin_amdgcn_readfirstlane(j.rows);
+    j.col0 = __builtin_amdgcn_readfirstlane(j.col0);
+    return j;
+}
+
+// Place of workgroup w among G (a multiple of 8): the workgroups of one XCD (w % 8) take neighbouring tasks.
+__device__ __forceinline__ int xcd_place(int w, int G) { return (w % 8) * (G / 8) + w / 8; }
+
+}  // namespace mk
