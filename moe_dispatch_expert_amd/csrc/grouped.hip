@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "grouped_dev.h"
+#include "grouped_few.h"
 #include "mk_device.h"
 #include "mk_launch.h"
 
@@ -126,16 +127,11 @@ __device__ __forceinline__ void wgrad_tile(const GroupedArgs &a, const GroupedTa
 
 // Rows' products (dgrad, 8-bit): the last rows of an expert run as a tile of 128, 64 or 32 rows.
 template <int KIND>
-__global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_rows(GroupedArgs a)
+__device__ __forceinline__ void rows_tiles(const GroupedArgs &a, const GroupedTables &t, lds_char_t *lds, int wave, int lane)
 {
-    __shared__ __attribute__((aligned(1024))) char stages[kGroupedStages];
-    __shared__ GroupedTables t;
-    lds_char_t *lds = (lds_char_t *)stages;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
-    tables_rows(a, t);
     const int cols = ((KIND == kI8 ? a.N : a.K) + 255) / 256;
-    const int64_t tasks = (int64_t)(t.tall[a.E] + t.low[a.E]) * cols;
-    for (int64_t q = xcd_place((int)blockIdx.x, (int)gridDim.x); q < tasks; q += gridDim.x) {
+    const int tasks = (t.tall[a.E] + t.low[a.E]) * cols;   // (outputs that fit the device have fewer than 2^31 tiles)
+    for (int q = xcd_place((int)blockIdx.x, (int)gridDim.x); q < tasks; q += gridDim.x) {
         const GroupedJob j = rows_job(a, t, cols, q);
         if constexpr (KIND == kDgrad) {
             if (j.rows > 128) dgrad_tile<256>(a, j, lds, wave, lane);
@@ -148,6 +144,44 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_rows(GroupedArgs
             else if (j.rows > 32) i8_tile<64>(a, j, lds, wave, lane);
             else i8_tile<32>(a, j, lds, wave, lane);
         }
+    }
+}
+
+__global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_dgrad(GroupedArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) char stages[kGroupedStages];
+    __shared__ GroupedTables t;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
+    tables_rows(a, t);
+    rows_tiles<kDgrad>(a, t, (lds_char_t *)stages, wave, lane);
+}
+
+__global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a)
+{
+    __shared__ __attribute__((aligned(1024))) union {
+        struct {
+            char stages[kGroupedStages];
+            GroupedTables t;
+        } tile;
+        struct {
+            char ring[kGroupedWaves * kFewRing];
+            FewTables t;
+        } few;
+    } m;
+    static_assert(sizeof(m) <= 160 * 1024 && kGroupedStages + sizeof(GroupedTables) <= kGroupedWaves * kFewRing,
+                  "LDS; the few rows' tables are made from the others");
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
+    const int2 hits = tables_rows(a, m.tile.t);
+    const int R = __builtin_amdgcn_readfirstlane(m.tile.t.off[a.E]), H = __builtin_amdgcn_readfirstlane(hits.y);
+    if (R <= kFewRows && R <= kFewGroup * H) {
+        few_tables(a, m.tile.t, m.few.t, hits.x);
+        // The width of a weight tile: 32, or 16 where that leaves the workgroup with the most tasks less to read.
+        const int G = (int)gridDim.x;
+        const int w32 = (H * ((a.N + 31) / 32) + G - 1) / G * 32, w16 = (H * ((a.N + 15) / 16) + G - 1) / G * 16;
+        if (w16 < w32) few_rows<16>(a, m.few.t, H, (lds_char_t *)m.few.ring, wave, lane);
+        else few_rows<32>(a, m.few.t, H, (lds_char_t *)m.few.ring, wave, lane);
+    } else {
+        rows_tiles<kI8>(a, m.tile.t, (lds_char_t *)m.tile.stages, wave, lane);
     }
 }
 
@@ -210,7 +244,7 @@ hipError_t launch_grouped_dgrad(const GroupedArgs &a, hipStream_t s)
 {
     const int grid = persistent_grid();
     if (grid <= 0) return hipErrorInvalidDevice;
-    hipLaunchKernelGGL(k_grouped_rows<kDgrad>, dim3(grid), dim3(kGroupedThreads), 0, s, a);
+    hipLaunchKernelGGL(k_grouped_dgrad, dim3(grid), dim3(kGroupedThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -227,7 +261,7 @@ hipError_t launch_grouped_i8(const GroupedArgs &a, hipStream_t s)
 {
     const int grid = persistent_grid();
     if (grid <= 0) return hipErrorInvalidDevice;
-    hipLaunchKernelGGL(k_grouped_rows<kI8>, dim3(grid), dim3(kGroupedThreads), 0, s, a);
+    hipLaunchKernelGGL(k_grouped_i8, dim3(grid), dim3(kGroupedThreads), 0, s, a);
     return hipGetLastError();
 }
 

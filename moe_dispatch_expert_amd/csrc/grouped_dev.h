@@ -402,7 +402,7 @@ struct GroupedTables {
     int32_t tall[kGroupedMaxE + 1];    // rows of tiles: how many of more than 128 rows lie before expert e ...
     int32_t low[kGroupedMaxE + 1];     // ... and how many short ones (the rest of an expert, if 128 rows or fewer);
                                        // wgrad: low[i] = the expert with the i-th most rows
-    int32_t wave_sum[2][kGroupedWaves];
+    uint64_t wave_sum[kGroupedWaves];
 };
 static_assert(kGroupedStages + sizeof(GroupedTables) <= 160 * 1024, "LDS");
 
@@ -415,59 +415,56 @@ __device__ __forceinline__ void tables_offsets(const GroupedArgs &a, GroupedTabl
 // Rows of expert e (offsets that do not ascend, which the caller must not give, count as no rows).
 __device__ __forceinline__ int table_count(const GroupedTables &t, int e) { return max(t.off[e + 1] - t.off[e], 0); }
 
-__device__ __forceinline__ void tables_rows(const GroupedArgs &a, GroupedTables &t)
+// Tall and short row tiles of every expert.  Returns the experts with rows: those before the thread's two (experts 2 ti and
+// 2 ti + 1), and all of them.
+__device__ __forceinline__ int2 tables_rows(const GroupedArgs &a, GroupedTables &t)
 {
     tables_offsets(a, t);
     const int ti = (int)threadIdx.x, lane = ti % kWave, wave = ti / kWave;
-    int n[2][2];   // thread: experts 2 ti and 2 ti + 1
-    int sum[2] = {0, 0};
+    // one scan of three sums in a word: short tiles (16 bits), experts with rows (16), tall tiles (32)
+    uint64_t n[2], sum = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int e = 2 * ti + h;
         const int cnt = e < a.E ? table_count(t, e) : 0, rest = cnt % 256;
-        n[h][0] = cnt / 256 + (rest > 128);
-        n[h][1] = rest > 0 && rest <= 128;
-        sum[0] += n[h][0];
-        sum[1] += n[h][1];
+        n[h] = ((uint64_t)(uint32_t)(cnt / 256 + (rest > 128)) << 32) | ((uint32_t)(cnt > 0) << 16) |
+               (uint32_t)(rest > 0 && rest <= 128);
+        sum += n[h];
     }
-    int inc[2] = {sum[0], sum[1]};
+    uint64_t inc = sum;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int v = __shfl_up(inc[k], d);
-            if (lane >= d) inc[k] += v;
-        }
+        const uint64_t v = __shfl_up((unsigned long long)inc, d);
+        if (lane >= d) inc += v;
     }
-    if (lane == kWave - 1) {
-        t.wave_sum[0][wave] = inc[0];
-        t.wave_sum[1][wave] = inc[1];
-    }
+    if (lane == kWave - 1) t.wave_sum[wave] = inc;
     __syncthreads();
-    int at[2] = {inc[0] - sum[0], inc[1] - sum[1]};
-    for (int w = 0; w < wave; ++w) {
-        at[0] += t.wave_sum[0][w];
-        at[1] += t.wave_sum[1][w];
+    uint64_t at = inc - sum, all = 0;
+    for (int w = 0; w < kGroupedWaves; ++w) {
+        const uint64_t v = t.wave_sum[w];
+        at += w < wave ? v : 0;
+        all += v;
     }
+    const int before = (int)((uint32_t)at >> 16);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int e = 2 * ti + h;
         if (e < a.E) {
-            t.tall[e] = at[0];
-            t.low[e] = at[1];
-            if (e == a.E - 1) {
-                t.tall[a.E] = at[0] + n[h][0];
-                t.low[a.E] = at[1] + n[h][1];
-            }
+            t.tall[e] = (int32_t)(at >> 32);
+            t.low[e] = (int32_t)((uint32_t)at & 0xFFFFu);
         }
-        at[0] += n[h][0];
-        at[1] += n[h][1];
+        at += n[h];
+    }
+    if (ti == 0) {
+        t.tall[a.E] = (int32_t)(all >> 32);
+        t.low[a.E] = (int32_t)((uint32_t)all & 0xFFFFu);
     }
     __syncthreads();
+    return make_int2(before, (int)((uint32_t)all >> 16));
 }
 
 // The expert of tile row q of a prefix table (the last e with pre[e] <= q).
-__device__ __forceinline__ int table_expert(const int32_t *pre, int E, int64_t q)
+__device__ __forceinline__ int table_expert(const int32_t *pre, int E, int q)
 {
     int lo = 0, hi = E;
     while (hi - lo > 1) {
@@ -485,22 +482,22 @@ struct GroupedJob {
 // Task q of the rows' products: tall tiles first, expert by expert, in groups of up to 8 row tiles that go through the
 // columns together (the 32 workgroups of an XCD then share 8 row tiles and 4 column tiles in its L2); the short ones after
 // all of them, so that the last round is made of short tasks.
-__device__ __forceinline__ GroupedJob rows_job(const GroupedArgs &a, const GroupedTables &t, int cols, int64_t q)
+__device__ __forceinline__ GroupedJob rows_job(const GroupedArgs &a, const GroupedTables &t, int cols, int q)
 {
     GroupedJob j;
-    const int64_t tall = (int64_t)t.tall[a.E] * cols;
+    const int tall = t.tall[a.E] * cols;
     if (q < tall) {
-        j.e = table_expert(t.tall, a.E, q / cols);
-        const int64_t r = q - (int64_t)t.tall[j.e] * cols;
+        j.e = table_expert(t.tall, a.E, (int)((uint32_t)q / (uint32_t)cols));
+        const int r = q - t.tall[j.e] * cols;
         const int n = t.tall[j.e + 1] - t.tall[j.e];
-        const int group = (int)(r / (8 * cols)), in = (int)(r - (int64_t)group * 8 * cols);
+        const int group = r / (8 * cols), in = r - group * 8 * cols;
         const int size = min(8, n - 8 * group);
         j.col0 = in / size * 256;
         j.row0 = (8 * group + in % size) * 256;
     } else {
-        const int64_t r = q - tall;
-        j.e = table_expert(t.low, a.E, r / cols);
-        j.col0 = (int)(r - (int64_t)t.low[j.e] * cols) * 256;
+        const int r = q - tall;
+        j.e = table_expert(t.low, a.E, (int)((uint32_t)r / (uint32_t)cols));
+        j.col0 = (r - t.low[j.e] * cols) * 256;
         j.row0 = (t.tall[j.e + 1] - t.tall[j.e]) * 256;
     }
     j.rows = min(table_count(t, j.e) - j.row0, 256);
