@@ -20,140 +20,278 @@ struct NoTokens {
     __device__ __forceinline__ void operator()(int, int *) const {}
 };
 
-template <int BM>
-__device__ __forceinline__ void dgrad_tile(const GroupedArgs &a, const GroupedJob &j, lds_char_t *lds, int wave, int lane)
+// The row products' tiles q, q + G, ... < n of one shape (BM = 256: of the tall tiles, else of the short ones), cols columns
+// of tiles from column first_col; returns the first q past n.
+template <int KIND, int BM, int BN>
+__device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t, int q, int n, int cols, int first_col,
+                                          lds_char_t *lds, int wave, int lane0)
 {
-    typedef GTile<kDgrad, BM> T;
-    lane = fresh_lane(lane);
-    Side<true, 256> sp;
-    Side<false, BM> sq;
-    side_columns(sp, (const uint16_t *)a.w + (size_t)j.e * a.N * a.K + j.col0, (uint64_t)a.K * 2, a.K - j.col0, false,
-                 wave, lane);
-    const uint32_t rb = (uint32_t)a.N * 2;
-    side_rows(sq, make_rsrc4(a.dy + (size_t)j.row0 * a.N, (size_t)0x80000000u), wave, lane,
-              [&](int m) { return m < j.rows ? (uint32_t)m * rb : kPastResource; });
-    f32x16_t acc[T::NI][T::MI];
-    tile_sums<T, false>(sp, sq, a.N, kPlainRecords, 0u, NoTokens{}, lds, wave, lane, acc);
-    __syncthreads();
-    store_bf16<T>([&](int i, int k, int v) { return acc[i][k][v]; }, (uint16_t *)a.out + (size_t)j.row0 * a.K + j.col0,
-                  a.K, j.rows, a.K - j.col0, lds, wave, lane);
-    __syncthreads();
-}
-
-template <int BM>
-__device__ __forceinline__ void i8_tile(const GroupedArgs &a, const GroupedJob &j, lds_char_t *lds, int wave, int lane)
-{
-    typedef GTile<kI8, BM> T;
-    lane = fresh_lane(lane);
-    Side<false, 256> sp;
-    Side<false, BM> sq;
-    side_rows(sp, make_rsrc4((const int8_t *)a.w + ((size_t)j.e * a.N + j.col0) * a.K, (size_t)0x80000000u), wave, lane,
-              [&](int n) { return j.col0 + n < a.N ? (uint32_t)n * (uint32_t)a.K : kPastResource; });
-    if (a.row_token) {
-        side_rows(sq, make_rsrc4(a.a, (size_t)a.a_rows * a.K), wave, lane, [&](int m) {
-            if (m >= j.rows) return kPastResource;
-            const int t = a.row_token[j.row0 + m];
-            return t >= 0 && t < a.a_rows ? (uint32_t)t * (uint32_t)a.K : kPastResource;
-        });
-    } else {
-        side_rows(sq, make_rsrc4((const int8_t *)a.a + (size_t)j.row0 * a.K, (size_t)0x80000000u), wave, lane,
-                  [&](int m) { return m < j.rows ? (uint32_t)m * (uint32_t)a.K : kPastResource; });
-    }
-    i32x16_t acc[T::NI][T::MI];
-    tile_sums<T, false>(sp, sq, a.K, kPlainRecords, 0u, NoTokens{}, lds, wave, lane, acc);
-    // the scales of the lane's rows and of its columns, four neighbours at a time
-    lane = fresh_lane(lane);
-    const int wn = wave % T::WN, wm = wave / T::WN;
-    float sa[T::MI];
-#pragma unroll
-    for (int k = 0; k < T::MI; ++k) {
-        const int m = wm * (T::BM / T::WM) + 32 * k + (lane & 31);
-        const int r = j.row0 + min(m, j.rows - 1);
-        const int t = a.row_token ? a.row_token[r] : r;
-        sa[k] = t >= 0 && t < a.a_rows ? a.a_scale[t] : 0.0f;
-    }
-    const float *ws = a.w_scale + (size_t)j.e * a.N;
-    f32x4_t sw[T::NI][4];
-#pragma unroll
-    for (int i = 0; i < T::NI; ++i)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int n = j.col0 + wn * (T::BN / T::WN) + 32 * i + 8 * g + 4 * (lane >> 5);
-            sw[i][g] = *(const f32x4_t *)(ws + min(n, a.N - 4));
+    typedef GTile<KIND, BM, BN> T;
+    typedef TileLoads<T, false> TL;
+    constexpr int STORES = 2 * T::NI * T::MI;
+    if (q >= n) return q;
+    const int G = (int)gridDim.x;
+    int lane = fresh_lane(lane0);
+    auto job_of = [&](int i) {
+        GroupedJob j = BM == 256 ? tall_job(a, t, cols, BN, i) : low_job(a, t, cols, BN, i);
+        j.col0 += first_col;
+        return j;
+    };
+    // 8-bit with a gather: the tokens of a tile's rows, into LDS (waves 0 to 3, 64 each), and token m of them, or -1.
+    const bool gather = KIND == kI8 && a.row_token;
+    auto tokens = [&](const GroupedJob &j) {
+        if (gather && wave < 4)
+            lds_load4(make_rsrc4(a.row_token + j.row0, (size_t)j.rows * 4),
+                      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char_t *)&t.tok[64 * wave]),
+                      (uint32_t)(64 * wave + lane) * 4u);
+    };
+    auto token = [&](const GroupedJob &j, int m) {
+        const int v = t.tok[m & 255];
+        return m < j.rows && v >= 0 && v < a.a_rows ? v : -1;
+    };
+    // The loads of a tile's scales (8-bit) and of its first slab.
+    auto begin = [&](const GroupedJob &j, TL &tl, int buf) {
+        if constexpr (KIND == kDgrad) {
+            side_columns(tl.p, (const uint16_t *)a.w + (size_t)j.e * a.N * a.K + j.col0, (uint64_t)a.K * 2, a.K - j.col0,
+                         false, wave, lane);
+            const uint32_t rb = (uint32_t)a.N * 2;
+            side_rows(tl.q, make_rsrc4(a.dy + (size_t)j.row0 * a.N, (size_t)0x80000000u), wave, lane,
+                      [&](int m, int) { return m < j.rows ? (uint32_t)m * rb : kPastResource; });
+            tl.len = a.N;
+        } else {
+            const uint32_t rb = (uint32_t)a.K;
+            side_rows(tl.p, make_rsrc4((const int8_t *)a.w + ((size_t)j.e * a.N + j.col0) * a.K, (size_t)0x80000000u),
+                      wave, lane, [&](int c, int) { return j.col0 + c < a.N ? (uint32_t)c * rb : kPastResource; });
+            if (gather)
+                side_rows(tl.q, make_rsrc4(a.a, (size_t)a.a_rows * a.K), wave, lane, [&](int m, int) {
+                    const int v = token(j, m);
+                    return v >= 0 ? (uint32_t)v * rb : kPastResource;
+                });
+            else
+                side_rows(tl.q, make_rsrc4((const int8_t *)a.a + (size_t)j.row0 * a.K, (size_t)0x80000000u), wave, lane,
+                          [&](int m, int) { return m < j.rows ? (uint32_t)m * rb : kPastResource; });
+            tl.len = a.K;
+            // waves 0 to 3: 64 rows' scales each; the others: 64 columns'
+            const int i = 64 * (wave & 3) + lane;
+            const bool rows = wave < 4;
+            uint32_t o = kPastResource;
+            if (rows) {
+                const int v = gather ? token(j, i) : (i < j.rows ? i : -1);
+                if (v >= 0) o = (uint32_t)v * 4u;
+            } else if (i < BN && j.col0 + i < a.N) {
+                o = (uint32_t)i * 4u;
+            }
+            const float *from = rows ? a.a_scale + (gather ? 0 : (size_t)j.row0) : a.w_scale + (size_t)j.e * a.N + j.col0;
+            lds_load4(make_rsrc4(from, (size_t)0x80000000u),
+                      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char_t *)&t.scale[buf][rows ? 0 : 1][64 * (wave & 3)]),
+                      o);
         }
+        tl.records_p = kPlainRecords;
+        tl.load_slab(0);
+    };
+    GroupedJob job = job_of(q);
+    tokens(job);
+    wait_vmem_all();
     __syncthreads();
-    store_bf16<T>([&](int i, int k, int v) { return (float)acc[i][k][v] * sw[i][v / 4][v % 4] * sa[k]; },
-                  (uint16_t *)a.out + (size_t)j.row0 * a.N + j.col0, a.N, j.rows, a.N - j.col0, lds, wave, lane);
-    __syncthreads();
+    TL tl;
+    tl.dst = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + (uint32_t)wave * 1024u);
+    int buf = 0;
+    begin(job, tl, buf);
+    for (bool first = true;; first = false) {
+        const bool more = q + G < n;
+        GroupedJob next = job;
+        if (more) {
+            next = job_of(q + G);
+            tokens(next);
+        }
+        typename Acc<KIND>::type acc[T::NI][T::MI];
+        tile_sums<T, false, STORES>(tl, !first, NoTokens{}, lds, wave, lane, acc);
+        __syncthreads();   // every wave is done with the stages
+        lane = fresh_lane(lane0);
+        if (more) begin(next, tl, buf ^ 1);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        const int el = fresh_lane(lane0);
+        if constexpr (KIND == kDgrad) {
+            store_bf16<T>([&](int i, int k, int v) { return acc[i][k][v]; },
+                          (uint16_t *)a.out + (size_t)job.row0 * a.K + job.col0, a.K, job.rows, a.K - job.col0, lds, wave, el);
+        } else {
+            const int wn = wave % T::WN, wm = wave / T::WN % T::WM;
+            float sa[T::MI];
+#pragma unroll
+            for (int k = 0; k < T::MI; ++k) sa[k] = t.scale[buf][0][wm * (T::BM / T::WM) + 32 * k + (el & 31)];
+            const float *sw = &t.scale[buf][1][wn * (T::BN / T::WN) + 4 * (el >> 5)];
+            store_bf16<T>([&](int i, int k, int v) { return (float)acc[i][k][v] * sw[32 * i + 8 * (v / 4) + v % 4] * sa[k]; },
+                          (uint16_t *)a.out + (size_t)job.row0 * a.N + job.col0, a.N, job.rows, a.N - job.col0, lds, wave,
+                          el);
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();   // the outputs have left the stages
+        q += G;
+        if (!more) break;
+        job = next;
+        buf ^= 1;
+    }
+    wait_vmem_all();
+    return q;
 }
 
-template <int BM, bool GATHER>
-__device__ __forceinline__ void wgrad_tile(const GroupedArgs &a, const GroupedTables &t, int e, int n0, int k0,
-                                           lds_char_t *lds, int wave, int lane)
+// How many workgroups' worth of time n tiles of each of `rows` row tiles take, in rounds.
+__device__ __forceinline__ int rounds(int rows, int columns, int width, int G)
 {
-    typedef GTile<kWgrad, BM> T;
-    lane = fresh_lane(lane);
-    Side<true, 256> sp;
-    Side<true, BM> sq;
-    const int row0 = __builtin_amdgcn_readfirstlane(t.off[e]);
-    const int cnt = __builtin_amdgcn_readfirstlane(table_count(t, e));
-    const uint64_t ld = (uint64_t)a.K * 2;
-    side_columns(sp, (const uint16_t *)a.a + (GATHER ? 0 : (size_t)row0 * a.K) + k0, ld, a.K - k0, GATHER, wave, lane);
-    side_columns(sq, a.dy + (size_t)row0 * a.N + n0, (uint64_t)a.N * 2, a.N - n0, false, wave, lane);
-    f32x16_t acc[T::NI][T::MI];
-    auto toks = [&](int slab, int *ids) {
-        if constexpr (!GATHER) return;
+    return (rows * ((columns + width - 1) / width) + G - 1) / G;
+}
+
+// Row products (dgrad, 8-bit): tall tiles (more than 128 rows), then the experts' last rows.
+//   - Tall tiles are 256 columns wide (the last 128 or fewer: 128), or all 128 (which takes 0.56 of the time) where that
+//     leaves fewer rounds' time.
+//   - The short ones read the weights for few rows: their time goes with the width, so the width is the one of 256, 128
+//     and 64 with the least rounds x width: half as wide a tile is half as long a task for twice as many CUs.
+template <int KIND>
+__device__ __forceinline__ void rows_all(const GroupedArgs &a, GroupedTables &t, bool long_tails, lds_char_t *lds, int wave,
+                                         int lane)
+{
+    const int G = (int)gridDim.x, C = KIND == kI8 ? a.N : a.K;
+    const int tall = __builtin_amdgcn_readfirstlane(t.tall[a.E]), low = __builtin_amdgcn_readfirstlane(t.low[a.E]);
+    // The phases' tiles are numbered on, so that workgroups without a tile in one's last round come first in the next.
+    // (Outputs that fit the device have fewer than 2^31 tiles.)
+    int q = xcd_place((int)blockIdx.x, G), n;
+    if (tall > 0) {
+        const int full = C / 256, rest = C - full * 256;
+        if (rounds(tall, C, 128, G) * 56 < rounds(tall, C, 256, G) * 97) {
+            n = tall * ((C + 127) / 128);
+            q = rows_tiles<KIND, 256, 128>(a, t, q, n, (C + 127) / 128, 0, lds, wave, lane) - n;
+        } else {
+            const int wide = full + (rest > 128);
+            n = tall * wide;
+            q = rows_tiles<KIND, 256, 256>(a, t, q, n, wide, 0, lds, wave, lane) - n;
+            if (rest > 0 && rest <= 128)
+                q = rows_tiles<KIND, 256, 128>(a, t, q, tall, 1, full * 256, lds, wave, lane) - tall;
+        }
+    }
+    if (low == 0) return;
+    const int c256 = rounds(low, C, 256, G) * 4, c128 = rounds(low, C, 128, G) * 2, c64 = rounds(low, C, 64, G);
+    const int width = c256 <= c128 && c256 <= c64 ? 256 : (c128 <= c64 ? 128 : 64);
+    n = low * ((C + width - 1) / width);
+    if (long_tails) {
+        if (width == 256) rows_tiles<KIND, 128, 256>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
+        else if (width == 128) rows_tiles<KIND, 128, 128>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
+        else rows_tiles<KIND, 128, 64>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
+    } else {
+        if (width == 256) rows_tiles<KIND, 32, 256>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
+        else if (width == 128) rows_tiles<KIND, 32, 128>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
+        else rows_tiles<KIND, 32, 64>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
+    }
+}
+
+// The weights' gradient, tiles q, q + G, ... < n of one shape: BM = 256: the full tiles of N (ns of them an expert), 128: the
+// last 128 or fewer.
+template <int BM, bool GATHER, bool F32>
+__device__ __forceinline__ void wgrad_tiles(const GroupedArgs &a, const GroupedTables &t, int experts, int ns, int first_n,
+                                            lds_char_t *lds, int wave, int lane0)
+{
+    typedef GTile<kWgrad, BM, 256> T;
+    typedef TileLoads<T, GATHER> TL;
+    constexpr int STORES = (F32 ? 4 : 2) * T::NI * T::MI;
+    const int G = (int)gridDim.x, place = xcd_place((int)blockIdx.x, G);
+    const int nk = (a.K + 255) / 256, per = nk * ns;
+    const int n = experts * per;
+    const int64_t ld = (int64_t)a.K * 2;
+    int lane = fresh_lane(lane0);
+    struct Job {
+        int e, n0, k0, row0, cnt;
+    };
+    // Experts with the most rows first; every other round goes through the workgroups backwards, so that those with a long
+    // task get a short one next.
+    auto task_of = [&](int r) { return r * G + ((r & 1) ? G - 1 - place : place); };
+    auto job_of = [&](int q) {
+        const int i = q / per, r = q - i * per;
+        const int group = r / (8 * nk), in = r - group * 8 * nk, size = min(8, ns - 8 * group);
+        Job j;
+        j.e = __builtin_amdgcn_readfirstlane(t.low[i]);
+        j.k0 = __builtin_amdgcn_readfirstlane(in / size * 256);
+        j.n0 = __builtin_amdgcn_readfirstlane(first_n + (8 * group + in % size) * 256);
+        j.row0 = __builtin_amdgcn_readfirstlane(t.off[j.e]);
+        j.cnt = __builtin_amdgcn_readfirstlane(table_count(t, j.e));
+        return j;
+    };
+    auto toks_of = [&](const Job &j, const TL &tl, int slab, int *ids) {
+        if constexpr (GATHER) {
+            if (j.cnt == 0) return;   // (uniform)
 #pragma unroll
-        for (int i = 0; i < Side<true, 256>::SLOTS; ++i) {
-            const int r = slab * 64 + sp.pos + kGroupedWaves * Side<true, 256>::RPL * i;
-            const int v = a.row_token[row0 + min(r, cnt - 1)];
-            ids[i] = v < a.a_rows ? v : -1;
+            for (int i = 0; i < TL::SP::SLOTS; ++i) {
+                const int r = slab * 64 + tl.p.pos + kGroupedWaves * TL::SP::RPL * i;
+                const int v = a.row_token[j.row0 + min(r, j.cnt - 1)];
+                ids[i] = v < a.a_rows ? v : -1;
+            }
         }
     };
-    // with a gather the rows' offsets run through all of `a` (and nothing is read of no rows)
-    const uint32_t records =
-        GATHER ? (a.a_rows > 0 ? (uint32_t)((size_t)a.a_rows * a.K * 2 - (size_t)k0 * 2) : 0u) : (uint32_t)kPlainRecords;
-    tile_sums<T, GATHER>(sp, sq, cnt, records, (uint32_t)ld, toks, lds, wave, lane, acc);
-    __syncthreads();
-    const size_t o = ((size_t)e * a.N + n0) * a.K + k0;
-    auto value = [&](int i, int k, int v) { return acc[i][k][v]; };
-    if (a.out_f32)
-        store_f32<T>(value, (float *)a.out + o, a.K, a.N - n0, a.K - k0, a.accumulate, lds, wave, lane);
-    else store_bf16<T>(value, (uint16_t *)a.out + o, a.K, a.N - n0, a.K - k0, lds, wave, lane);
-    __syncthreads();
+    auto begin = [&](const Job &j, TL &tl) {
+        side_columns(tl.p, (const uint16_t *)a.a + (GATHER ? 0 : (size_t)j.row0 * a.K) + j.k0, (uint64_t)ld, a.K - j.k0,
+                     GATHER, wave, lane);
+        side_columns(tl.q, a.dy + (size_t)j.row0 * a.N + j.n0, (uint64_t)a.N * 2, a.N - j.n0, false, wave, lane);
+        tl.len = j.cnt;
+        // with a gather the rows' offsets run through all of `a` (and nothing is read of no rows)
+        tl.records_p =
+            GATHER ? (a.a_rows > 0 ? (uint32_t)((size_t)a.a_rows * a.K * 2 - (size_t)j.k0 * 2) : 0u) : (uint32_t)kPlainRecords;
+        tl.row_bytes = (uint32_t)ld;
+        tl.load_slab(0);
+        toks_of(j, tl, 1, tl.ids);
+    };
+    if (place >= n) return;
+    Job job = job_of(place);
+    TL tl;
+    tl.dst = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + (uint32_t)wave * 1024u);
+    tl.p.pos = wave * TL::SP::RPL + lane / (TL::SP::RB / 16);   // (the same for every tile)
+    int ids[GATHER ? TL::SP::SLOTS : 1];
+    toks_of(job, tl, 0, tl.ids);
+    begin(job, tl);
+    for (int round = 1;; ++round) {
+        const int nq = task_of(round);
+        const bool more = nq < n;
+        Job next = job;
+        if (more) {
+            next = job_of(nq);
+            toks_of(next, tl, 0, ids);
+        }
+        f32x16_t acc[T::NI][T::MI];
+        tile_sums<T, GATHER, STORES>(tl, !GATHER && round > 1, [&](int slab, int *to) { toks_of(job, tl, slab, to); }, lds, wave, lane, acc);
+        __syncthreads();   // every wave is done with the stages
+        lane = fresh_lane(lane0);
+        if (more) {
+            if constexpr (GATHER) {
+#pragma unroll
+                for (int i = 0; i < TL::SP::SLOTS; ++i) tl.ids[i] = ids[i];
+            }
+            begin(next, tl);
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        const size_t o = ((size_t)job.e * a.N + job.n0) * a.K + job.k0;
+        auto value = [&](int i, int k, int v) { return acc[i][k][v]; };
+        const int el = fresh_lane(lane0);
+        if constexpr (F32)
+            store_f32<T>(value, (float *)a.out + o, a.K, a.N - job.n0, a.K - job.k0, a.accumulate, lds, wave, el);
+        else store_bf16<T>(value, (uint16_t *)a.out + o, a.K, a.N - job.n0, a.K - job.k0, lds, wave, el);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();   // the outputs have left the stages
+        if (!more) break;   // (no later round has a task either)
+        job = next;
+    }
+    wait_vmem_all();
 }
 
 }  // namespace
-
-// Rows' products (dgrad, 8-bit): the last rows of an expert run as a tile of 128, 64 or 32 rows.
-template <int KIND>
-__device__ __forceinline__ void rows_tiles(const GroupedArgs &a, const GroupedTables &t, lds_char_t *lds, int wave, int lane)
-{
-    const int cols = ((KIND == kI8 ? a.N : a.K) + 255) / 256;
-    const int tasks = (t.tall[a.E] + t.low[a.E]) * cols;   // (outputs that fit the device have fewer than 2^31 tiles)
-    for (int q = xcd_place((int)blockIdx.x, (int)gridDim.x); q < tasks; q += gridDim.x) {
-        const GroupedJob j = rows_job(a, t, cols, q);
-        if constexpr (KIND == kDgrad) {
-            if (j.rows > 128) dgrad_tile<256>(a, j, lds, wave, lane);
-            else if (j.rows > 64) dgrad_tile<128>(a, j, lds, wave, lane);
-            else if (j.rows > 32) dgrad_tile<64>(a, j, lds, wave, lane);
-            else dgrad_tile<32>(a, j, lds, wave, lane);
-        } else {
-            if (j.rows > 128) i8_tile<256>(a, j, lds, wave, lane);
-            else if (j.rows > 64) i8_tile<128>(a, j, lds, wave, lane);
-            else if (j.rows > 32) i8_tile<64>(a, j, lds, wave, lane);
-            else i8_tile<32>(a, j, lds, wave, lane);
-        }
-    }
-}
 
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_dgrad(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(1024))) char stages[kGroupedStages];
     __shared__ GroupedTables t;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
-    tables_rows(a, t);
-    rows_tiles<kDgrad>(a, t, (lds_char_t *)stages, wave, lane);
+    const TableTotals n = tables_rows(a, t);
+    rows_all<kDgrad>(a, t, n.long_tails, (lds_char_t *)stages, wave, lane);
 }
 
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a)
@@ -168,26 +306,26 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a
             FewTables t;
         } few;
     } m;
-    static_assert(sizeof(m) <= 160 * 1024 && kGroupedStages + sizeof(GroupedTables) <= kGroupedWaves * kFewRing,
-                  "LDS; the few rows' tables are made from the others");
+    static_assert(sizeof(m) <= 160 * 1024, "LDS");
+    static_assert(kGroupedStages + offsetof(GroupedTables, scale) <= kGroupedWaves * kFewRing,
+                  "the few rows' tables are made from the others");
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
-    const int2 hits = tables_rows(a, m.tile.t);
-    const int R = __builtin_amdgcn_readfirstlane(m.tile.t.off[a.E]), H = __builtin_amdgcn_readfirstlane(hits.y);
+    const TableTotals n = tables_rows(a, m.tile.t);
+    const int R = __builtin_amdgcn_readfirstlane(m.tile.t.off[a.E]), H = __builtin_amdgcn_readfirstlane(n.hits);
     if (R <= kFewRows && R <= kFewGroup * H) {
-        few_tables(a, m.tile.t, m.few.t, hits.x);
+        few_tables(a, m.tile.t, m.few.t, n.before);
         // The width of a weight tile: 32, or 16 where that leaves the workgroup with the most tasks less to read.
         const int G = (int)gridDim.x;
         const int w32 = (H * ((a.N + 31) / 32) + G - 1) / G * 32, w16 = (H * ((a.N + 15) / 16) + G - 1) / G * 16;
         if (w16 < w32) few_rows<16>(a, m.few.t, H, (lds_char_t *)m.few.ring, wave, lane);
         else few_rows<32>(a, m.few.t, H, (lds_char_t *)m.few.ring, wave, lane);
     } else {
-        rows_tiles<kI8>(a, m.tile.t, (lds_char_t *)m.tile.stages, wave, lane);
+        rows_all<kI8>(a, m.tile.t, n.long_tails, (lds_char_t *)m.tile.stages, wave, lane);
     }
 }
 
-// The weights' gradient: tiles of 256 x 256 (the last 128 or fewer of the N: 128 x 256), experts with the most rows
-// first; every other round goes through the workgroups backwards, so that those with a long task get a short one next.
-template <bool GATHER>
+// The weights' gradient: full tiles of 256 x 256 of all experts, then (N % 256 in 1 .. 128) tiles of 128 x 256.
+template <bool GATHER, bool F32>
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_wgrad(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(1024))) char stages[kGroupedStages];
@@ -195,31 +333,31 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_wgrad(GroupedArg
     lds_char_t *lds = (lds_char_t *)stages;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
     tables_offsets(a, t);
+    // The experts in the order of their rows, most first.
+    const int padded = (a.E + 3) & ~3;
+    int experts = 0;
+    for (int e0 = 0; e0 < padded; e0 += kGroupedThreads) {
+        const int e = e0 + (int)threadIdx.x;
+        const int c = e < a.E ? table_count(t, e) : -1;
+        if (e < padded) t.tall[e] = c;
+        experts += __syncthreads_count(c > 0);
+    }
     for (int e = (int)threadIdx.x; e < a.E; e += kGroupedThreads) {
-        const int c = table_count(t, e);
+        const int c = t.tall[e];
         int rank = 0;
-        for (int f = 0; f < a.E; ++f) {
-            const int d = table_count(t, f);
-            rank += d > c || (d == c && f < e);
+#pragma unroll 4
+        for (int f = 0; f < padded; f += 4) {
+            const int4 d = *(const int4 *)&t.tall[f];
+            rank += (d.x > c || (d.x == c && f < e)) + (d.y > c || (d.y == c && f + 1 < e)) +
+                    (d.z > c || (d.z == c && f + 2 < e)) + (d.w > c || (d.w == c && f + 3 < e));
         }
         t.low[rank] = e;
     }
     __syncthreads();
-    const int nk = (a.K + 255) / 256, nn = (a.N + 255) / 256, per = nk * nn;
-    const int64_t tasks = (int64_t)a.E * per;
-    const int G = (int)gridDim.x, place = xcd_place((int)blockIdx.x, G);
-    for (int64_t round = 0; round * G < tasks; ++round) {
-        const int64_t q = round * G + ((round & 1) ? G - 1 - place : place);
-        if (q >= tasks) continue;
-        const int i = (int)(q / per), r = (int)(q - (int64_t)i * per);
-        const int e = __builtin_amdgcn_readfirstlane(t.low[i]);
-        if (a.accumulate && table_count(t, e) == 0) continue;   // nothing to add (uniform)
-        const int group = r / (8 * nk), in = r - group * 8 * nk, size = min(8, nn - 8 * group);
-        const int k0 = __builtin_amdgcn_readfirstlane(in / size * 256);
-        const int n0 = __builtin_amdgcn_readfirstlane((8 * group + in % size) * 256);
-        if (a.N - n0 > 128) wgrad_tile<256, GATHER>(a, t, e, n0, k0, lds, wave, lane);
-        else wgrad_tile<128, GATHER>(a, t, e, n0, k0, lds, wave, lane);
-    }
+    if (!a.accumulate) experts = a.E;   // (those without rows have nothing to add)
+    const int full = a.N / 256 + (a.N % 256 > 128), half = a.N % 256 > 0 && a.N % 256 <= 128;
+    if (full) wgrad_tiles<256, GATHER, F32>(a, t, experts, full, 0, lds, wave, lane);
+    if (half) wgrad_tiles<128, GATHER, F32>(a, t, experts, 1, full * 256, lds, wave, lane);
 }
 
 namespace {
@@ -252,8 +390,9 @@ hipError_t launch_grouped_wgrad(const GroupedArgs &a, hipStream_t s)
 {
     const int grid = persistent_grid();
     if (grid <= 0) return hipErrorInvalidDevice;
-    if (a.row_token) hipLaunchKernelGGL(k_grouped_wgrad<true>, dim3(grid), dim3(kGroupedThreads), 0, s, a);
-    else hipLaunchKernelGGL(k_grouped_wgrad<false>, dim3(grid), dim3(kGroupedThreads), 0, s, a);
+    void (*k)(GroupedArgs) = a.row_token ? (a.out_f32 ? k_grouped_wgrad<true, true> : k_grouped_wgrad<true, false>)
+                                         : (a.out_f32 ? k_grouped_wgrad<false, true> : k_grouped_wgrad<false, false>);
+    hipLaunchKernelGGL(k, dim3(grid), dim3(kGroupedThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -30,11 +30,6 @@ struct FewTables {
 
 typedef int32_t few_acc_t __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ void lds_load4(rsrc4_t rsrc, uint32_t lds_addr, uint32_t voff)
-{
-    asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "{m0}"(lds_addr));
-}
-
 // A place in a workgroup's stream: task q (weight tile q % tiles of the (q / tiles)-th hit expert), group g of 16 of its
 // rows; item counts the groups passed.
 struct FewPlace {
@@ -198,21 +193,22 @@ __device__ __forceinline__ void few_rows(const GroupedArgs &a, FewTables &t, int
     wait_vmem_all();   // no load may land in this memory once the workgroup is gone
 }
 
-// The tables of this form: rows' tokens and scales, experts with rows (hits of them, before: how many before the thread's
-// two), sums of zero.  g: the offsets.
+// The tables of this form: rows' tokens and scales, experts with rows (before: how many lie before the thread's two), sums of
+// zero.  g: the offsets, whose place the tables may take.
 __device__ __forceinline__ void few_tables(const GroupedArgs &a, const GroupedTables &g, FewTables &t, int before)
 {
-    const int ti = (int)threadIdx.x;
+    const int ti = (int)threadIdx.x, e = 2 * ti, R = g.off[a.E];
+    int off[3];
+#pragma unroll
+    for (int h = 0; h < 3; ++h) off[h] = g.off[min(e + h, a.E)];
+    __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int e = 2 * ti + h;
-        if (e < a.E) {
-            t.off[e] = (uint16_t)g.off[e];
-            if (e == a.E - 1) t.off[a.E] = (uint16_t)g.off[a.E];
-            if (table_count(g, e) > 0) t.hit[before++] = (uint16_t)e;
-        }
+        if (e + h <= a.E) t.off[e + h] = (uint16_t)off[h];
+        if (e + h < a.E && off[h + 1] > off[h]) t.hit[before++] = (uint16_t)(e + h);
     }
-    for (int r = ti; r < g.off[a.E]; r += kGroupedThreads) {
+    if (e + 2 == a.E) t.off[a.E] = (uint16_t)off[2];
+    for (int r = ti; r < R; r += kGroupedThreads) {
         const int v = a.row_token ? a.row_token[r] : r;
         const bool ok = v >= 0 && v < a.a_rows;
         t.tok[r] = ok ? v : -1;
