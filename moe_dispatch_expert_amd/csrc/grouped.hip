@@ -185,46 +185,55 @@ __device__ __forceinline__ void rows_all(const GroupedArgs &a, GroupedTables &t,
     }
 }
 
-// The weights' gradient, tiles q, q + G, ... < n of one shape: BM = 256: the full tiles of N (ns of them an expert), 128: the
-// last 128 or fewer.
+// The tasks of the weights' gradient: every expert's full tiles (256 x 256; full of them along N), then its tiles of the last
+// 128 or fewer of N (128 x 256; half: 1 if there are any).  Experts with the most rows first; every other round goes through
+// the workgroups backwards, so that those with a long task get a short one next.
+struct WgradTasks {
+    int nk, full, half, per, n;   // tiles along K; tasks an expert, and all of them
+    int G, place;
+
+    __device__ __forceinline__ int task(int round) const { return round * G + ((round & 1) ? G - 1 - place : place); }
+    __device__ __forceinline__ bool is_half(int q) const { return q % per >= nk * full; }
+};
+
+// The workgroup's tasks from `round` on, as long as they are tiles of BM rows; returns the first round that is not.
 template <int BM, bool GATHER, bool F32>
-__device__ __forceinline__ void wgrad_tiles(const GroupedArgs &a, const GroupedTables &t, int experts, int ns, int first_n,
-                                            lds_char_t *lds, int wave, int lane0)
+__device__ __forceinline__ int wgrad_tiles(const GroupedArgs &a, const GroupedTables &t, const WgradTasks &w, int round,
+                                           lds_char_t *lds, int wave, int lane0)
 {
     typedef GTile<kWgrad, BM, 256> T;
     typedef TileLoads<T, GATHER> TL;
     constexpr int STORES = (F32 ? 4 : 2) * T::NI * T::MI;
-    const int G = (int)gridDim.x, place = xcd_place((int)blockIdx.x, G);
-    const int nk = (a.K + 255) / 256, per = nk * ns;
-    const int n = experts * per;
     const int64_t ld = (int64_t)a.K * 2;
     int lane = fresh_lane(lane0);
     struct Job {
         int e, n0, k0, row0, cnt;
     };
-    // Experts with the most rows first; every other round goes through the workgroups backwards, so that those with a long
-    // task get a short one next.
-    auto task_of = [&](int r) { return r * G + ((r & 1) ? G - 1 - place : place); };
     auto job_of = [&](int q) {
-        const int i = q / per, r = q - i * per;
-        const int group = r / (8 * nk), in = r - group * 8 * nk, size = min(8, ns - 8 * group);
+        const int i = q / w.per, r = q - i * w.per;
         Job j;
+        if constexpr (BM == 256) {
+            const int group = r / (8 * w.nk), in = r - group * 8 * w.nk, size = min(8, w.full - 8 * group);
+            j.k0 = __builtin_amdgcn_readfirstlane(in / size * 256);
+            j.n0 = __builtin_amdgcn_readfirstlane((8 * group + in % size) * 256);
+        } else {
+            j.k0 = __builtin_amdgcn_readfirstlane((r - w.nk * w.full) * 256);
+            j.n0 = w.full * 256;
+        }
         j.e = __builtin_amdgcn_readfirstlane(t.low[i]);
-        j.k0 = __builtin_amdgcn_readfirstlane(in / size * 256);
-        j.n0 = __builtin_amdgcn_readfirstlane(first_n + (8 * group + in % size) * 256);
         j.row0 = __builtin_amdgcn_readfirstlane(t.off[j.e]);
         j.cnt = __builtin_amdgcn_readfirstlane(table_count(t, j.e));
         return j;
     };
+    // The rows of `a` of a slab (0 past the expert's: nothing is loaded for those).
     auto toks_of = [&](const Job &j, const TL &tl, int slab, int *ids) {
         if constexpr (GATHER) {
-            if (j.cnt == 0) return;   // (uniform)
+            const int rest = max(0, min(j.cnt - slab * 64, 64));
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.row_token + j.row0 + (size_t)slab * 64, (size_t)rest * 4);
 #pragma unroll
-            for (int i = 0; i < TL::SP::SLOTS; ++i) {
-                const int r = slab * 64 + tl.p.pos + kGroupedWaves * TL::SP::RPL * i;
-                const int v = a.row_token[j.row0 + min(r, j.cnt - 1)];
-                ids[i] = v < a.a_rows ? v : -1;
-            }
+            for (int i = 0; i < TL::SP::SLOTS; ++i)
+                ids[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(
+                    rs, (uint32_t)(tl.p.pos + kGroupedWaves * TL::SP::RPL * i) * 4u, 0, 0);
         }
     };
     auto begin = [&](const Job &j, TL &tl) {
@@ -236,27 +245,27 @@ __device__ __forceinline__ void wgrad_tiles(const GroupedArgs &a, const GroupedT
         tl.records_p =
             GATHER ? (a.a_rows > 0 ? (uint32_t)((size_t)a.a_rows * a.K * 2 - (size_t)j.k0 * 2) : 0u) : (uint32_t)kPlainRecords;
         tl.row_bytes = (uint32_t)ld;
+        tl.a_rows = a.a_rows;
         tl.load_slab(0);
         toks_of(j, tl, 1, tl.ids);
     };
-    if (place >= n) return;
-    Job job = job_of(place);
+    Job job = job_of(w.task(round));
     TL tl;
     tl.dst = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + (uint32_t)wave * 1024u);
     tl.p.pos = wave * TL::SP::RPL + lane / (TL::SP::RB / 16);   // (the same for every tile)
     int ids[GATHER ? TL::SP::SLOTS : 1];
     toks_of(job, tl, 0, tl.ids);
     begin(job, tl);
-    for (int round = 1;; ++round) {
-        const int nq = task_of(round);
-        const bool more = nq < n;
+    for (bool first = true;; first = false) {
+        const int nq = w.task(++round);
+        const bool more = nq < w.n && w.is_half(nq) == (BM == 128);
         Job next = job;
         if (more) {
             next = job_of(nq);
             toks_of(next, tl, 0, ids);
         }
         f32x16_t acc[T::NI][T::MI];
-        tile_sums<T, GATHER, STORES>(tl, !GATHER && round > 1, [&](int slab, int *to) { toks_of(job, tl, slab, to); }, lds, wave, lane, acc);
+        tile_sums<T, GATHER, STORES>(tl, !GATHER && !first, [&](int slab, int *to) { toks_of(job, tl, slab, to); }, lds, wave, lane, acc);
         __syncthreads();   // every wave is done with the stages
         lane = fresh_lane(lane0);
         if (more) {
@@ -277,10 +286,11 @@ __device__ __forceinline__ void wgrad_tiles(const GroupedArgs &a, const GroupedT
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
         __syncthreads();   // the outputs have left the stages
-        if (!more) break;   // (no later round has a task either)
+        if (!more) break;
         job = next;
     }
     wait_vmem_all();
+    return round;
 }
 
 }  // namespace
@@ -324,7 +334,7 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a
     }
 }
 
-// The weights' gradient: full tiles of 256 x 256 of all experts, then (N % 256 in 1 .. 128) tiles of 128 x 256.
+// The weights' gradient.
 template <bool GATHER, bool F32>
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_wgrad(GroupedArgs a)
 {
@@ -355,9 +365,18 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_wgrad(GroupedArg
     }
     __syncthreads();
     if (!a.accumulate) experts = a.E;   // (those without rows have nothing to add)
-    const int full = a.N / 256 + (a.N % 256 > 128), half = a.N % 256 > 0 && a.N % 256 <= 128;
-    if (full) wgrad_tiles<256, GATHER, F32>(a, t, experts, full, 0, lds, wave, lane);
-    if (half) wgrad_tiles<128, GATHER, F32>(a, t, experts, 1, full * 256, lds, wave, lane);
+    WgradTasks w;
+    w.nk = (a.K + 255) / 256;
+    w.full = a.N / 256 + (a.N % 256 > 128);
+    w.half = a.N % 256 > 0 && a.N % 256 <= 128;
+    w.per = w.nk * (w.full + w.half);
+    w.n = experts * w.per;
+    w.G = (int)gridDim.x;
+    w.place = xcd_place((int)blockIdx.x, w.G);
+    for (int round = 0; w.task(round) < w.n;) {   // (no task in a round: none in a later one)
+        if (w.is_half(w.task(round))) round = wgrad_tiles<128, GATHER, F32>(a, t, w, round, lds, wave, lane);
+        else round = wgrad_tiles<256, GATHER, F32>(a, t, w, round, lds, wave, lane);
+    }
 }
 
 namespace {

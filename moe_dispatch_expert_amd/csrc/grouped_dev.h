@@ -128,14 +128,16 @@ __device__ __forceinline__ rsrc4_t slab_rsrc(uint64_t base, uint32_t records)
 }
 
 // This lane's offset for load slot i of a slab; rest: what is left of the contraction from the slab's start (rows of KR, else
-// bytes; <= 0: nothing).  tok (GATHER): this lane's row of `a`.
+// bytes; <= 0: nothing).  tok (GATHER): this lane's row of `a`, which
+// has a_rows of them.
 template <bool GATHER, bool KR, int C>
-__device__ __forceinline__ uint32_t side_offset(const Side<KR, C> &s, int i, int rest, int tok, uint32_t row_bytes)
+__device__ __forceinline__ uint32_t side_offset(const Side<KR, C> &s, int i, int rest, int tok, int a_rows,
+                                                 uint32_t row_bytes)
 {
     uint32_t o = s.off[i];
     bool ok = s.pos + (KR ? kGroupedWaves * Side<KR, C>::RPL * i : 0) < rest;
     if constexpr (GATHER) {
-        ok = ok & (tok >= 0) & (o != kPastResource);
+        ok = ok & ((uint32_t)tok < (uint32_t)a_rows) & (o != kPastResource);
         o += (uint32_t)tok * row_bytes;
     }
     return ok ? o : kPastResource;
@@ -221,6 +223,7 @@ struct TileLoads {
     SQ q;
     int len;
     int ids[GATHER ? SP::SLOTS : 1];
+    int a_rows;
     uint32_t records_p, row_bytes;
     rsrc4_t rp, rq;
     uint32_t dst;   // LDS address of this wave's first block of stage 0
@@ -242,14 +245,18 @@ struct TileLoads {
         }
     }
     // This lane's offsets for a slab, then its load i; stage: LDS address of the wave's first block of the stage.
-    __device__ __forceinline__ void aim(int slab, uint32_t (&at)[NL]) const
+    __device__ __forceinline__ uint32_t offset(int i, int slab) const
     {
         const int rest = len - slab * T::L;
+        return i < SP::SLOTS
+                   ? side_offset<GATHER>(p, i, T::PKR ? rest : rest * T::ESZ, GATHER ? ids[GATHER ? i : 0] : 0, a_rows,
+                                          row_bytes)
+                   : side_offset<false>(q, i - SP::SLOTS, T::QKR ? rest : rest * T::ESZ, 0, 0, 0u);
+    }
+    __device__ __forceinline__ void aim(int slab, uint32_t (&at)[NL]) const
+    {
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
-            at[i] = i < SP::SLOTS
-                        ? side_offset<GATHER>(p, i, T::PKR ? rest : rest * T::ESZ, GATHER ? ids[GATHER ? i : 0] : 0, row_bytes)
-                        : side_offset<false>(q, i - SP::SLOTS, T::QKR ? rest : rest * T::ESZ, 0, 0u);
+        for (int i = 0; i < NL; ++i) at[i] = offset(i, slab);
     }
     __device__ __forceinline__ void load(int i, const uint32_t (&at)[NL], int slab, uint32_t stage) const
     {
@@ -347,7 +354,9 @@ __device__ __forceinline__ void tile_sums(TileLoads<T, GATHER> &tl, bool stored,
         step(fp0, fq0, [&](int r) { rd(r, 3, fp1, fq1); }, 0, none);
         uint32_t at[NL];
         tl.next_slab();
-        tl.aim(j + S, at);
+        // With a gather one by one among the products instead: the tokens were asked for after the loads that are waited for
+        // below, and all at once after that the offsets would hold up the products.
+        if constexpr (!GATHER) tl.aim(j + S, at);
         // vmcnt: slab j + 1 is here; lgkmcnt(0): so are the last step's fragments
         __builtin_amdgcn_s_waitcnt((((S - 2) * NL) & 15) | ((((S - 2) * NL) >> 4) << 14) | 0x0070);
         __syncthreads();
@@ -357,7 +366,10 @@ __device__ __forceinline__ void tile_sums(TileLoads<T, GATHER> &tl, bool stored,
             bp[n] += to;
             bq[n] += to;
         }
-        step(fp1, fq1, [&](int r) { rd(r, 0, fp0, fq0); }, NL, [&](int i) { tl.load(i, at, j + S, stage); });
+        step(fp1, fq1, [&](int r) { rd(r, 0, fp0, fq0); }, NL, [&](int i) {
+            if constexpr (GATHER) at[i] = tl.offset(i, j + S);
+            tl.load(i, at, j + S, stage);
+        });
         if constexpr (GATHER) toks(j + S + 1, tl.ids);
         stage = __builtin_amdgcn_readfirstlane(stage + (uint32_t)to);
         cur = cur == S - 1 ? 0 : cur + 1;
