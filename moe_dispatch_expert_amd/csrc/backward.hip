@@ -38,6 +38,7 @@ __device__ __forceinline__ void sigmoid_both(float g, float &s, float &t)
 template <int NP>
 __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
 {
+    constexpr int U = 4 / NP < 2 ? 2 : 4 / NP;
     __shared__ int32_t s_slot[kMaxK];
     __shared__ float s_w[kMaxK];
     __shared__ int32_t s_first[kMaxK];   // the token's first choice of the same slot
@@ -69,37 +70,46 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
 #pragma unroll
             for (int i = 0; i < NP; ++i)
                 d[i] = *(const u32x4_t *)(a.dout + (size_t)t * a.N + 8 * min(p0 + ti + 256 * i, pieces - 1));
-            for (int j = 0; j < a.k; ++j) {
-                const int slot = __builtin_amdgcn_readfirstlane(s_slot[j]);
-                if (slot < 0) continue;
-                const float w = s_w[j];
-                float dot = 0.0f;
-                u32x4_t v[NP];
-                if (a.dgate) {
+            // U choices at a time: their rows are all asked for before the first is used
+            for (int j0 = 0; j0 < a.k; j0 += U) {
+                u32x4_t v[U][NP];
+                int slot[U];
 #pragma unroll
-                    for (int i = 0; i < NP; ++i)
-                        v[i] = *(const u32x4_t *)(a.y + (size_t)slot * a.N + 8 * min(p0 + ti + 256 * i, pieces - 1));
-                }
+                for (int u = 0; u < U; ++u) {
+                    slot[u] = j0 + u < a.k ? __builtin_amdgcn_readfirstlane(s_slot[min(j0 + u, kMaxK - 1)]) : -1;
+                    if (a.dgate && slot[u] >= 0) {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int p = p0 + ti + 256 * i;
-                    const bool in = p < pieces;
-                    float f[8], o[8];
-                    unpack8(d[i], f);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) o[q] = w * f[q];
-                    if (in) *(u32x4_t *)(a.dy + (size_t)slot * a.N + 8 * p) = pack8(o);
-                    if (a.dgate) {
-                        float y[8], part = 0.0f;
-                        unpack8(v[i], y);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) part = __builtin_fmaf(f[q], y[q], part);
-                        dot += in ? part : 0.0f;
+                        for (int i = 0; i < NP; ++i)
+                            v[u][i] =
+                                *(const u32x4_t *)(a.y + (size_t)slot[u] * a.N + 8 * min(p0 + ti + 256 * i, pieces - 1));
                     }
                 }
-                if (a.dgate) {
-                    dot = wave_sum_f32(dot);
-                    if (lane == 0) s_dot[j][wave] += dot;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (slot[u] < 0) continue;   // uniform
+                    const float w = s_w[j0 + u];
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const int p = p0 + ti + 256 * i;
+                        const bool in = p < pieces;
+                        float f[8], o[8];
+                        unpack8(d[i], f);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) o[q] = w * f[q];
+                        if (in) *(u32x4_t *)(a.dy + (size_t)slot[u] * a.N + 8 * p) = pack8(o);
+                        if (a.dgate) {
+                            float y[8], part = 0.0f;
+                            unpack8(v[u][i], y);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) part = __builtin_fmaf(f[q], y[q], part);
+                            dot += in ? part : 0.0f;
+                        }
+                    }
+                    if (a.dgate) {
+                        dot = wave_sum_f32(dot);
+                        if (lane == 0) s_dot[j0 + u][wave] += dot;
+                    }
                 }
             }
         }

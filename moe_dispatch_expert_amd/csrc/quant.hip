@@ -3,10 +3,14 @@
 //
 //   m = max |v|,   scale = m / 127,   q = round(127 v / m)   (ties to even; scale 0 and codes 0 in a row of zeros)
 //
-// v = x (bf16), or v = silu(g) u in fp32, not rounded in between.  127 x of a bf16 x is exact in fp32 and the quotient
-// 127 x / m of two bf16 values is a tie only where it is one exactly (otherwise it is at least 2^-16 away from it,
-// relative), so one correctly rounded division gives the codes of the real numbers.  A row stays in registers between its
-// maximum and its codes: one pass, bound by memory.
+// v = x (bf16), or v = silu(g) u in fp32, not rounded in between.  A row stays in registers between its maximum and its
+// codes: one pass, bound by memory, as long as the arithmetic stays short:
+//   - No division per element: r = v (127 / m) is within 2^-22 of 127 v / m, relative.  For bf16 rows the codes are still those of
+//     the real numbers: 127 x / m of two bf16 values (significands below 2^8) is a tie only where it is one exactly, and
+//     otherwise at least 2^-16 away from one, relative; so r is first rounded to 20 bits, which makes every tie a tie again and
+//     carries nothing else across one.
+//   - silu(g) = g / (1 + e^-g) with e^-g = 2^(-g c) e^(-g c'), c = log2(e) to 15 bits: g has 8 bits, so the product g c is exact, and
+//     the second factor is 1 - g c' to within 2^-23 (|g| < 88; beyond, the result is 0 or g).
 #include <hip/hip_runtime.h>
 
 #include "grouped_args.h"
@@ -16,18 +20,35 @@
 
 namespace mk {
 
-template <int THREADS, int NP, bool SWIGLU>
-__global__ __launch_bounds__(THREADS) void k_quant_i8(QuantArgs a, int row0)
+namespace {
+
+constexpr float kLog2eHi = 1.44268798828125f;                   // log2(e) to 15 bits
+constexpr float kExpLo = 4.8884952e-06f;                        // 1 - kLog2eHi ln(2): what is left of the exponent
+
+// silu(g) u.
+__device__ __forceinline__ float swiglu(float g, float u)
 {
-    const int ti = (int)threadIdx.x, r = row0 + (int)blockIdx.x;
-    if (a.rows_valid && r >= *a.rows_valid) return;   // uniform
+    const float e = __builtin_amdgcn_exp2f(-g * kLog2eHi) * __builtin_fmaf(-g, kExpLo, 1.0f);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+
+}  // namespace
+
+// LANES threads a row (64: a wave, four rows a workgroup; else a workgroup), NP pieces of 8 columns a thread.
+template <int LANES, int NP, bool SWIGLU>
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_quant_i8(QuantArgs a, int row0)
+{
+    constexpr int ROWS = LANES < 256 ? 256 / LANES : 1;
+    const int ti = (int)threadIdx.x % LANES;
+    const int r = row0 + (int)blockIdx.x * ROWS + (ROWS > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / LANES) : 0);
+    if (r >= (a.rows_valid ? min(a.rows, *a.rows_valid) : a.rows)) return;   // the same for all threads of a row
     const int pieces = a.d / 8;
     const uint16_t *x = a.x + (size_t)r * a.d * (SWIGLU ? 2 : 1);
     float v[NP][8];
     u32x4_t vx[NP], vu[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const int p = min(ti + i * THREADS, pieces - 1);
+        const int p = min(ti + i * LANES, pieces - 1);
         vx[i] = *(const u32x4_t *)(x + 8 * p);
         if (SWIGLU) vu[i] = *(const u32x4_t *)(x + a.d + 8 * p);
     }
@@ -40,62 +61,72 @@ __global__ __launch_bounds__(THREADS) void k_quant_i8(QuantArgs a, int row0)
             float u[8];
             unpack8(vu[i], u);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] / (1.0f + expf(-v[i][j])) * u[j];
+            for (int j = 0; j < 8; ++j) v[i][j] = swiglu(v[i][j], u[j]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
     }
     m = wave_max_u32(m);
-    __shared__ uint32_t red[THREADS / kWave];
-    if (ti % kWave == 0) red[ti / kWave] = m;
-    __syncthreads();
-    m = 0;
+    if constexpr (LANES > kWave) {
+        __shared__ uint32_t red[LANES / kWave];
+        if (ti % kWave == 0) red[ti / kWave] = m;
+        __syncthreads();
+        m = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / kWave; ++w) m = max(m, red[w]);
+        for (int w = 0; w < LANES / kWave; ++w) m = max(m, red[w]);
+    }
     const float big = __uint_as_float(m);
-    const bool finite = m < 0x7F800000u;
+    const bool finite = m < 0x7F800000u, live = finite && m != 0;
     if (ti == 0) a.scale[r] = finite ? big / 127.0f : __uint_as_float(0x7FC00000u);
-    // 127 v stays finite: rows of large values are taken 2^-8 times as large, which changes no quotient
-    const float down = big > 1.0f ? 0x1p-8f : 1.0f;
-    const bool live = finite && m != 0;
-    const float den = live ? big * down : 1.0f;
-    const float num = live ? 127.0f * down : 0.0f;
+    // 127 / m stays finite: rows of tiny values are taken 2^100 times as large, which changes no quotient
+    const float up = big < 0x1p-100f ? 0x1p100f : 1.0f;
+    const float k = 127.0f / (live ? big * up : 1.0f);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const int p = ti + i * THREADS;
+        const int p = ti + i * LANES;
         uint32_t w[2] = {0u, 0u};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float t = live ? v[i][j] * num / den : 0.0f;
+            float t = v[i][j] * up * k;
+            if (!SWIGLU) t = __uint_as_float((__float_as_uint(t) + 8u) & ~15u);   // 20 bits
             w[j / 4] |= ((uint32_t)(int32_t)__builtin_rintf(t) & 0xFFu) << (8 * (j % 4));
         }
-        if (p < pieces) *(uint2 *)(a.q + (size_t)r * a.d + 8 * p) = make_uint2(w[0], w[1]);
+        if (p < pieces) *(uint2 *)(a.q + (size_t)r * a.d + 8 * p) = live ? make_uint2(w[0], w[1]) : make_uint2(0u, 0u);
     }
 }
 
 namespace {
 
 // A launch takes fewer than 2^32 work items, so more rows than that go to several.
-template <int THREADS, int NP>
+template <int LANES, int NP>
 hipError_t launch_quant_as(const QuantArgs &a, bool swiglu, hipStream_t s)
 {
-    constexpr int kRows = 0x7FFFFFFF / THREADS;
-    for (int r0 = 0; r0 < a.rows;) {
-        const int n = a.rows - r0 < kRows ? a.rows - r0 : kRows;
-        if (swiglu) hipLaunchKernelGGL((k_quant_i8<THREADS, NP, true>), dim3(n), dim3(THREADS), 0, s, a, r0);
-        else hipLaunchKernelGGL((k_quant_i8<THREADS, NP, false>), dim3(n), dim3(THREADS), 0, s, a, r0);
+    constexpr int THREADS = LANES < 256 ? 256 : LANES, ROWS = THREADS / LANES;
+    constexpr int64_t kRows = (int64_t)(0x7FFFFFFF / THREADS) * ROWS;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += kRows) {
+        const int64_t n = a.rows - r0 < kRows ? a.rows - r0 : kRows;
+        const dim3 grid((uint32_t)((n + ROWS - 1) / ROWS));
+        if (swiglu) hipLaunchKernelGGL((k_quant_i8<LANES, NP, true>), grid, dim3(THREADS), 0, s, a, (int)r0);
+        else hipLaunchKernelGGL((k_quant_i8<LANES, NP, false>), grid, dim3(THREADS), 0, s, a, (int)r0);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        r0 += n;
     }
     return hipSuccess;
 }
 
 }  // namespace
 
+// A wave holds a row of up to 2048 columns.  A few such rows are spread over workgroups of their own instead, where all
+// their loads are on their way at once.
 hipError_t launch_quant_i8(const QuantArgs &a, bool swiglu, hipStream_t s)
 {
     const int pieces = a.d / 8;
+    if (pieces <= 256 && (pieces <= 64 || a.rows > 1024)) {
+        if (pieces <= 64) return launch_quant_as<64, 1>(a, swiglu, s);
+        if (pieces <= 128) return launch_quant_as<64, 2>(a, swiglu, s);
+        if (pieces <= 192) return launch_quant_as<64, 3>(a, swiglu, s);
+        return launch_quant_as<64, 4>(a, swiglu, s);
+    }
     if (pieces <= 256) return launch_quant_as<256, 1>(a, swiglu, s);
     if (pieces <= 512) return launch_quant_as<512, 1>(a, swiglu, s);
     if (pieces <= 1024) return launch_quant_as<1024, 1>(a, swiglu, s);
