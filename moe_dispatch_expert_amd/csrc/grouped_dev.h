@@ -381,7 +381,7 @@ __device__ __forceinline__ void tile_sums(TileLoads<T, GATHER> &tl, bool stored,
 #pragma unroll
     for (int i = 0; i < T::NI; ++i)
 #pragma unroll
-        for (int k = 0; k < T::MI; ++k) asm volatile("" : "+a"(acc[i][k]));
+        for (int k = 0; k < T::MI; ++k) asm volatile("" : "+v"(acc[i][k]));
     __builtin_amdgcn_sched_barrier(0);
     wait_vmem_all();
 }
