@@ -87,7 +87,8 @@ __device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t
                       o);
         }
         tl.records_p = kPlainRecords;
-        tl.load_slab(0);
+#pragma unroll
+        for (int i = 0; i < T::PRE; ++i) tl.load_slab(i);
     };
     GroupedJob job = job_of(q);
     tokens(job);
@@ -201,7 +202,7 @@ template <int BM, bool GATHER, bool F32>
 __device__ __forceinline__ int wgrad_tiles(const GroupedArgs &a, const GroupedTables &t, const WgradTasks &w, int round,
                                            lds_char_t *lds, int wave, int lane0)
 {
-    typedef GTile<kWgrad, BM, 256> T;
+    typedef GTile<kWgrad, BM, 256, BM == 256 && !GATHER ? 64 : 128> T;
     typedef TileLoads<T, GATHER> TL;
     constexpr int STORES = (F32 ? 4 : 2) * T::NI * T::MI;
     const int64_t ld = (int64_t)a.K * 2;
@@ -228,8 +229,8 @@ __device__ __forceinline__ int wgrad_tiles(const GroupedArgs &a, const GroupedTa
     // The rows of `a` of a slab (0 past the expert's: nothing is loaded for those).
     auto toks_of = [&](const Job &j, const TL &tl, int slab, int *ids) {
         if constexpr (GATHER) {
-            const int rest = max(0, min(j.cnt - slab * 64, 64));
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.row_token + j.row0 + (size_t)slab * 64, (size_t)rest * 4);
+            const int rest = max(0, min(j.cnt - slab * T::L, T::L));
+            const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.row_token + j.row0 + (size_t)slab * T::L, (size_t)rest * 4);
 #pragma unroll
             for (int i = 0; i < TL::SP::SLOTS; ++i)
                 ids[i] = (int)__builtin_amdgcn_raw_buffer_load_b32(
@@ -246,7 +247,9 @@ __device__ __forceinline__ int wgrad_tiles(const GroupedArgs &a, const GroupedTa
             GATHER ? (a.a_rows > 0 ? (uint32_t)((size_t)a.a_rows * a.K * 2 - (size_t)j.k0 * 2) : 0u) : (uint32_t)kPlainRecords;
         tl.row_bytes = (uint32_t)ld;
         tl.a_rows = a.a_rows;
-        tl.load_slab(0);
+        static_assert(!GATHER || T::PRE == 1, "the rows of slab 0 alone are known before");
+#pragma unroll
+        for (int i = 0; i < T::PRE; ++i) tl.load_slab(i);
         toks_of(j, tl, 1, tl.ids);
     };
     Job job = job_of(w.task(round));

@@ -18,8 +18,8 @@
 // Every load is checked lane by lane against the tile's rows or columns and the slab's rest of the contraction: a lane
 // outside gets an offset past the resource, which reads zeros without a memory access, so ragged ends add exact zeros
 // whatever lies behind them.
-// A tile's first slab is loaded before the outputs of the tile before it are stored (they go through the upper half of the
-// stages' LDS).
+// A tile's first slabs are loaded before the outputs of the tile before it are stored (these go through the upper half of
+// the stages' LDS).
 #pragma once
 
 #include "gemm_dev.h"
@@ -41,17 +41,20 @@ constexpr int kPlainRecords = (int)0x80000000u;     // of resources whose offset
 
 // A tile of BM rows by BN columns, the waves WN along the columns and WM along the rows (of small tiles several waves
 // compute the same: they are bound by memory).
-template <int KIND_, int BM_, int BN_>
+template <int KIND_, int BM_, int BN_, int KB_ = 128>
 struct GTile {
     static constexpr int KIND = KIND_, BM = BM_, BN = BN_;
+    static constexpr int KB = KB_, STEPS = KB / 32;                  // bytes of an operand's row in a slab, instruction steps
     static constexpr int WN = BM == 256 ? 2 : (BM == 128 ? (BN == 64 ? 2 : 4) : BN / 32);
     static constexpr int WM = BM == 32 ? 1 : kGroupedWaves / WN;
     static constexpr int NI = BN / WN / 32, MI = BM / WM / 32;
     static constexpr bool PKR = KIND != kI8, QKR = KIND == kWgrad;   // rows along the contraction
     static constexpr int ESZ = KIND == kI8 ? 1 : 2;                  // bytes of an element
-    static constexpr int L = 128 / ESZ;                              // contraction per slab
-    static constexpr int PB = BN * 128, QB = (BM > 64 ? BM : 64) * 128, SB = PB + QB;   // bytes of a stage
+    static constexpr int L = KB / ESZ;                               // contraction per slab
+    static constexpr int PB = BN * KB, QB = (BM > 64 ? BM : 64) * KB, SB = PB + QB;     // bytes of a stage
     static constexpr int S = kGroupedStages / SB < 8 ? kGroupedStages / SB : 8;         // stages
+    static constexpr int PRE0 = kGroupedStages / 2 / SB;                                // of them in the lower half of the LDS,
+    static constexpr int PRE = PRE0 < S ? PRE0 : S;                                     // loaded before outputs are stored
     static_assert(NI >= 1 && MI >= 1 && WN * WM <= kGroupedWaves && S >= 2 && SB <= kGroupedStages / 2, "tile shape");
 };
 
@@ -73,12 +76,12 @@ __device__ __forceinline__ void wave_sync()
 }
 
 // One operand of a tile: C rows (or columns) of it, and this lane's part of its loads.
-template <bool KR, int C>
+template <bool KR, int C, int KB>
 struct Side {
     static constexpr int RB = 2 * C;                         // KR: bytes of an LDS row
     static constexpr int RPL = 1024 / RB;                    // KR: rows a load
-    static constexpr int SLOTS = KR ? 64 / RPL / kGroupedWaves : (C / 8 + kGroupedWaves - 1) / kGroupedWaves;
-    static_assert(C >= 64 || !KR, "row swizzle");
+    static constexpr int SLOTS = KR ? KB / 2 / RPL / kGroupedWaves : (C / 8 + kGroupedWaves - 1) / kGroupedWaves;
+    static_assert(KR ? C >= 64 && SLOTS >= 1 : KB == 128, "row swizzle");
     uint32_t off[SLOTS];   // byte offsets in the resource (kPastResource: nothing to read)
     int pos;               // place in the slab: KR the row of slot 0, else the byte
     uint64_t base;         // KR: of the next slab to load
@@ -118,7 +121,7 @@ __device__ __forceinline__ void side_columns(S &s, const void *base, uint64_t ld
     }
     s.pos = wave * S::RPL + r0;
     s.base = (uint64_t)base;
-    s.step = 64 * ld;
+    s.step = (uint64_t)(kGroupedWaves * S::RPL * S::SLOTS) * ld;
 }
 
 __device__ __forceinline__ rsrc4_t slab_rsrc(uint64_t base, uint32_t records)
@@ -130,12 +133,12 @@ __device__ __forceinline__ rsrc4_t slab_rsrc(uint64_t base, uint32_t records)
 // This lane's offset for load slot i of a slab; rest: what is left of the contraction from the slab's start (rows of KR, else
 // bytes; <= 0: nothing).  tok (GATHER): this lane's row of `a`, which
 // has a_rows of them.
-template <bool GATHER, bool KR, int C>
-__device__ __forceinline__ uint32_t side_offset(const Side<KR, C> &s, int i, int rest, int tok, int a_rows,
+template <bool GATHER, bool KR, int C, int KB>
+__device__ __forceinline__ uint32_t side_offset(const Side<KR, C, KB> &s, int i, int rest, int tok, int a_rows,
                                                  uint32_t row_bytes)
 {
     uint32_t o = s.off[i];
-    bool ok = s.pos + (KR ? kGroupedWaves * Side<KR, C>::RPL * i : 0) < rest;
+    bool ok = s.pos + (KR ? kGroupedWaves * Side<KR, C, KB>::RPL * i : 0) < rest;
     if constexpr (GATHER) {
         ok = ok & ((uint32_t)tok < (uint32_t)a_rows) & (o != kPastResource);
         o += (uint32_t)tok * row_bytes;
@@ -151,7 +154,7 @@ __device__ __forceinline__ void lds_load4(rsrc4_t rsrc, uint32_t lds_addr, uint3
 
 // Where this lane's fragments start in a stage.  Contraction contiguous: by step of the slab; rows along it: by block of
 // 32 columns (block q of the operand: q0 + index).
-template <bool KR, int C, int NB>
+template <bool KR, int C, int KB, int NB>
 __device__ __forceinline__ void frag_bases(lds_char_t *stage, int q0, int lane, lds_char_t *(&b)[4])
 {
     b[0] = b[1] = b[2] = b[3] = stage;
@@ -179,7 +182,7 @@ __device__ __forceinline__ void frag_bases(lds_char_t *stage, int q0, int lane, 
 }
 
 // Half t of fragment n of step kk from the stage that b points into (t = 0 alone with the contraction contiguous).
-template <bool KR, int C>
+template <bool KR, int C, int KB>
 __device__ __forceinline__ void read_half(lds_char_t *const (&b)[4], int n, int t, int kk, i32x4_t &f)
 {
     if constexpr (KR) {
@@ -216,8 +219,8 @@ __device__ __forceinline__ void product(i32x4_t p, i32x4_t q, i32x16_t &acc)
 // the next slab to load (ids), P's resource size and its rows' bytes.
 template <class T, bool GATHER>
 struct TileLoads {
-    typedef Side<T::PKR, T::BN> SP;
-    typedef Side<T::QKR, T::BM> SQ;
+    typedef Side<T::PKR, T::BN, T::KB> SP;
+    typedef Side<T::QKR, T::BM, T::KB> SQ;
     static constexpr int NL = SP::SLOTS + SQ::SLOTS;   // loads a slab
     SP p;
     SQ q;
@@ -263,7 +266,7 @@ struct TileLoads {
         const bool isp = i < SP::SLOTS;
         const uint32_t to = __builtin_amdgcn_readfirstlane(
             stage + (isp ? 0u : (uint32_t)T::PB) + (uint32_t)(kGroupedWaves * 1024 * (isp ? i : i - SP::SLOTS)));
-        const uint32_t k0 = (isp ? T::PKR : T::QKR) ? 0u : __builtin_amdgcn_readfirstlane((uint32_t)slab * 128u);
+        const uint32_t k0 = (isp ? T::PKR : T::QKR) ? 0u : __builtin_amdgcn_readfirstlane((uint32_t)(slab * T::KB));
         lds_load16(isp ? rp : rq, to, at[i], k0);
     }
     __device__ __forceinline__ void load_slab(int slab)
@@ -279,10 +282,10 @@ struct TileLoads {
     }
 };
 
-// The sums of a tile whose slab 0 is on its way into stage 0, with STORES memory operations or more after it (stored: else
-// none): acc[i][j], lane: column 32 i + 8 (v / 4) + 4 (lane / 32) + v % 4 of the wave's columns, row 32 j + lane % 32 of
-// its rows.  toks(slab, ids): the rows of `a` that this lane loads of a slab (with a gather; those of slab 1 have been
-// asked for).  On return every load is done, but waves may still read the stages.
+// The sums of a tile whose first PRE slabs are on their way into the stages, with STORES memory operations or more after them
+// (stored: else none): acc[i][j], lane: column 32 i + 8 (v / 4) + 4 (lane / 32) + v % 4 of the wave's columns, row
+// 32 j + lane % 32 of its rows.  toks(slab, ids): the rows of `a` that this lane loads of a slab (with a gather; those of
+// slab PRE have been asked for).  On return every load is done, but waves may still read the stages.
 template <class T, bool GATHER, int STORES, class TOK>
 __device__ __forceinline__ void tile_sums(TileLoads<T, GATHER> &tl, bool stored, TOK &&toks, lds_char_t *lds, int wave,
                                           int lane, typename Acc<T::KIND>::type (&acc)[T::NI][T::MI])
@@ -300,13 +303,13 @@ __device__ __forceinline__ void tile_sums(TileLoads<T, GATHER> &tl, bool stored,
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
     const int KK = __builtin_amdgcn_readfirstlane((tl.len + T::L - 1) / T::L);
     lds_char_t *bp[4], *bq[4];
-    frag_bases<T::PKR, T::BN, T::NI>(lds, wn * T::NI, lane, bp);
-    frag_bases<T::QKR, T::BM, T::MI>(lds + T::PB, wm * T::MI, lane, bq);
+    frag_bases<T::PKR, T::BN, T::KB, T::NI>(lds, wn * T::NI, lane, bp);
+    frag_bases<T::QKR, T::BM, T::KB, T::MI>(lds + T::PB, wm * T::MI, lane, bq);
     // (the places of memory operations matter to the counts below)
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int s = 1; s < S; ++s) {
+    for (int s = T::PRE; s < S; ++s) {
         tl.load_slab(s);
         if constexpr (GATHER) toks(s + 1, tl.ids);
     }
@@ -321,11 +324,11 @@ __device__ __forceinline__ void tile_sums(TileLoads<T, GATHER> &tl, bool stored,
     i32x4_t fp0[T::NI], fq0[T::MI], fp1[T::NI], fq1[T::MI];
     // read r of a step, in the order in which the products need them: P 0, the Q, the other P
     auto rd = [&](int r, int kk, i32x4_t (&fp)[T::NI], i32x4_t (&fq)[T::MI]) {
-        if (r < NH) read_half<T::PKR, T::BN>(bp, 0, r, kk, fp[0]);
-        else if (r < NH + T::MI * MH) read_half<T::QKR, T::BM>(bq, (r - NH) / MH, (r - NH) % MH, kk, fq[(r - NH) / MH]);
+        if (r < NH) read_half<T::PKR, T::BN, T::KB>(bp, 0, r, kk, fp[0]);
+        else if (r < NH + T::MI * MH) read_half<T::QKR, T::BM, T::KB>(bq, (r - NH) / MH, (r - NH) % MH, kk, fq[(r - NH) / MH]);
         else {
             const int n = (r - T::MI * MH) / NH;
-            read_half<T::PKR, T::BN>(bp, n, (r - T::MI * MH) % NH, kk, fp[n]);
+            read_half<T::PKR, T::BN, T::KB>(bp, n, (r - T::MI * MH) % NH, kk, fp[n]);
         }
     };
     // the products of a step on (fp, fq), with the reads of the next one and a slab's loads spread over them
@@ -350,8 +353,10 @@ __device__ __forceinline__ void tile_sums(TileLoads<T, GATHER> &tl, bool stored,
     uint32_t stage = tl.dst;
     for (int j = 0; j < KK; ++j) {
         step(fp0, fq0, [&](int r) { rd(r, 1, fp1, fq1); }, 0, none);
-        step(fp1, fq1, [&](int r) { rd(r, 2, fp0, fq0); }, 0, none);
-        step(fp0, fq0, [&](int r) { rd(r, 3, fp1, fq1); }, 0, none);
+        if constexpr (T::STEPS == 4) {
+            step(fp1, fq1, [&](int r) { rd(r, 2, fp0, fq0); }, 0, none);
+            step(fp0, fq0, [&](int r) { rd(r, 3, fp1, fq1); }, 0, none);
+        }
         uint32_t at[NL];
         tl.next_slab();
         // With a gather one by one among the products instead: the tokens were asked for after the loads that are waited for
