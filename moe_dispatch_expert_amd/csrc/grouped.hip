@@ -192,8 +192,11 @@ __device__ __forceinline__ void rows_all(const GroupedArgs &a, GroupedTables &t,
 struct WgradTasks {
     int nk, full, half, per, n;   // tiles along K; tasks an expert, and all of them
     int G, place;
+    int rounds;                   // in which this workgroup has a task
+    bool backwards;
 
-    __device__ __forceinline__ int task(int round) const { return round * G + ((round & 1) ? G - 1 - place : place); }
+    __device__ __forceinline__ int dealt(int round) const { return round * G + ((round & 1) ? G - 1 - place : place); }
+    __device__ __forceinline__ int task(int round) const { return dealt(backwards ? rounds - 1 - round : round); }
     __device__ __forceinline__ bool is_half(int q) const { return q % per >= nk * full; }
 };
 
@@ -261,7 +264,7 @@ __device__ __forceinline__ int wgrad_tiles(const GroupedArgs &a, const GroupedTa
     begin(job, tl);
     for (bool first = true;; first = false) {
         const int nq = w.task(++round);
-        const bool more = nq < w.n && w.is_half(nq) == (BM == 128);
+        const bool more = round < w.rounds && w.is_half(nq) == (BM == 128);
         Job next = job;
         if (more) {
             next = job_of(nq);
@@ -376,7 +379,10 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_wgrad(GroupedArg
     w.n = experts * w.per;
     w.G = (int)gridDim.x;
     w.place = xcd_place((int)blockIdx.x, w.G);
-    for (int round = 0; w.task(round) < w.n;) {   // (no task in a round: none in a later one)
+    w.rounds = w.n / w.G;
+    if (w.dealt(w.rounds) < w.n) ++w.rounds;
+    w.backwards = blockIdx.x & 1;
+    for (int round = 0; round < w.rounds;) {
         if (w.is_half(w.task(round))) round = wgrad_tiles<128, GATHER, F32>(a, t, w, round, lds, wave, lane);
         else round = wgrad_tiles<256, GATHER, F32>(a, t, w, round, lds, wave, lane);
     }
