@@ -483,7 +483,7 @@ mk_status mk_swiglu_backward(const void *gate_up, const void *dh, int32_t rows, 
  * for every row r of expert e, offsets[e] <= r < offsets[e + 1].  The sum's order
  * does not depend on other rows.
  *   dy [rows, N] bf16     expert_offsets [E_local + 1] int32 (non-decreasing, offsets[0] = 0; read on the device,
- *                         values past `rows` are taken as `rows`)
+ *                         values past `rows` are taken as `rows`, past the last one as the last one)
  *   w [E_local, N, K] bf16 (as for mk_grouped_gemm)
  *   da [rows, K] bf16 (out; rows >= offsets[E_local] untouched)
  * Requires rows >= 0, 1 <= E_local <= 1024, N > 0, K > 0, N % 8 == 0, K % 8 == 0;

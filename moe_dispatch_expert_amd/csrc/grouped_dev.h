@@ -494,7 +494,9 @@ static_assert(kGroupedStages + sizeof(GroupedTables) <= 160 * 1024, "LDS");
 
 __device__ __forceinline__ void tables_offsets(const GroupedArgs &a, GroupedTables &t)
 {
-    for (int e = (int)threadIdx.x; e <= a.E; e += kGroupedThreads) t.off[e] = min(max(a.offsets[e], 0), a.rows);
+    // (no offset past the last one: the few rows' tables have as many places)
+    const int end = min(max(a.offsets[a.E], 0), a.rows);
+    for (int e = (int)threadIdx.x; e <= a.E; e += kGroupedThreads) t.off[e] = min(max(a.offsets[e], 0), end);
     __syncthreads();
 }
 

@@ -105,6 +105,34 @@ def test_wgrad(counts, K, N, what, form):
     assert torch.equal(got.cpu(), want.to(dtype))
 
 
+def test_offsets_past_the_last_one_are_cut_to_it():
+    """Offsets that go back at the end: what lies past the last one belongs to nobody, however few rows are left."""
+    g = torch.Generator().manual_seed(1)
+    given, cut = torch.tensor([0, 2000, 900, 10], dtype=torch.int32), torch.tensor([0, 10, 10, 10], dtype=torch.int32)
+    dy, a, w = ref.whole(g, 2000, 72), ref.whole(g, 2000, 48), ref.whole(g, 3, 72, 48)
+    out = torch.full((2000, 48), 7.0, dtype=BF, device="cuda")
+    mk.mk_grouped_gemm_dgrad(dy.cuda(), given.cuda(), w.cuda(), out=out)
+    assert torch.equal(out[:10].cpu(), ref.dgrad(dy, cut, w)[:10].to(BF)) and (out[10:] == 7.0).all()
+    got = mk.mk_grouped_gemm_wgrad(dy.cuda(), a.cuda(), given.cuda())
+    assert torch.equal(got.cpu(), ref.wgrad(dy, a, cut).float())
+    codes, s = torch.randint(-128, 128, (2000, 48), generator=g).to(torch.int8), torch.rand(2000, generator=g)
+    w, ws = torch.randint(-128, 128, (3, 40, 48), generator=g).to(torch.int8), torch.rand(3, 40, generator=g)
+    for rt in (None, torch.randint(0, 2000, (2000,), generator=g, dtype=torch.int32)):
+        out = torch.full((2000, 40), 7.0, dtype=BF, device="cuda")
+        mk.mk_grouped_gemm_i8(codes.cuda(), s.cuda(), given.cuda(), w.cuda(), ws.cuda(),
+                              row_token=None if rt is None else rt.cuda(), out=out)
+        assert torch.equal(out[:10].cpu(), ref.i8(codes, s, cut, w, ws, rt)[:10]) and (out[10:] == 7.0).all()
+
+
+def test_a_row_of_dgrad_has_the_same_bits_in_any_batch():
+    g = torch.Generator().manual_seed(2)
+    dy, w = torch.randn(1600, 520, generator=g).to(BF).cuda(), torch.randn(2, 520, 264, generator=g).to(BF).cuda()
+    whole = mk.mk_grouped_gemm_dgrad(dy, torch.tensor([0, 800, 1600], dtype=torch.int32, device="cuda"), w)
+    for r0, r1 in ((0, 1), (10, 50), (790, 800), (800, 940), (1000, 1600)):
+        off = torch.tensor([0, r1 - r0, r1 - r0] if r0 < 800 else [0, 0, r1 - r0], dtype=torch.int32, device="cuda")
+        assert torch.equal(mk.mk_grouped_gemm_dgrad(dy[r0:r1], off, w), whole[r0:r1])
+
+
 def _i8_ffn(x, ids, gates, w1, s1, w2, s2, **kw):
     E, F = w1.shape[0], w2.shape[2]
     lay = mk.mk_expert_layout(ids, E, **kw)
