@@ -147,8 +147,12 @@ __device__ __forceinline__ int rounds(int rows, int columns, int width, int G)
 // Row products (dgrad, 8-bit): tall tiles (more than 128 rows), then the experts' last rows.
 //   - Tall tiles are 256 columns wide (the last 128 or fewer: 128), or all 128 (which takes 0.56 of the time) where that
 //     leaves fewer rounds' time.
-//   - The short ones read the weights for few rows: their time goes with the width, so the width is the one of 256, 128
-//     and 64 with the least rounds x width: half as wide a tile is half as long a task for twice as many CUs.
+//     Measured (us, 256 / 128 wide): 8 experts x 1024 rows, 4096 x 14336: 806 / 1047, 8-bit 457 / 555; 8 x 256 rows,
+//     4096 x 4096: 115 / 87, 8-bit 66 / 40.
+//   - The short ones read the weights for few rows.  A round of tiles 64, 128 and 256 wide takes about 5 : 8 : 15 (narrow
+//     ones read the weights in shorter segments and the rows more often); the width is the one with the least.  Measured
+//     (us, 64 / 128 / 256 wide): 64 experts x 20 rows, 2048 x 2816: 164 / 137 / 128, 8-bit 100 / 74 / 71; 64 x 100 rows,
+//     2048 x 1408: 100 / 82 / 100, 8-bit 51 / 43 / 44; 8 x 30 rows, 2048 x 2048: 16 / 23 / 31, 8-bit 10 / 14 / 19.
 template <int KIND>
 __device__ __forceinline__ void rows_all(const GroupedArgs &a, GroupedTables &t, bool long_tails, lds_char_t *lds, int wave,
                                          int lane)
@@ -172,7 +176,7 @@ __device__ __forceinline__ void rows_all(const GroupedArgs &a, GroupedTables &t,
         }
     }
     if (low == 0) return;
-    const int c256 = rounds(low, C, 256, G) * 4, c128 = rounds(low, C, 128, G) * 2, c64 = rounds(low, C, 64, G);
+    const int c256 = rounds(low, C, 256, G) * 15, c128 = rounds(low, C, 128, G) * 8, c64 = rounds(low, C, 64, G) * 5;
     const int width = c256 <= c128 && c256 <= c64 ? 256 : (c128 <= c64 ? 128 : 64);
     n = low * ((C + width - 1) / width);
     if (long_tails) {
