@@ -20,21 +20,38 @@ struct NoTokens {
     __device__ __forceinline__ void operator()(int, int *) const {}
 };
 
-// The row products' tiles q, q + G, ... < n of one shape (BM = 256: of the tall tiles, else of the short ones), cols columns
-// of tiles from column first_col; returns the first q past n.
+// A run of the row products' tiles of one shape, n of them: short ones, or tall ones from the from-th on; tiles of `width`
+// columns, cols of them from column first_col.  A tall one may be cut into 2^cut tiles of BM x BN.
+struct Tiles {
+    int n, cols, first_col, width;
+    bool low;
+    int from, cut;
+};
+
+// Tiles q, q + G, ... of a run; returns the first q past it.
 template <int KIND, int BM, int BN>
-__device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t, int q, int n, int cols, int first_col,
-                                          lds_char_t *lds, int wave, int lane0)
+__device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t, int q, const Tiles &of, lds_char_t *lds,
+                                          int wave, int lane0)
 {
     typedef GTile<KIND, BM, BN> T;
     typedef TileLoads<T, false> TL;
     constexpr int STORES = 2 * T::NI * T::MI;
+    const int n = of.n;
     if (q >= n) return q;
     const int G = (int)gridDim.x;
     int lane = fresh_lane(lane0);
     auto job_of = [&](int i) {
-        GroupedJob j = BM == 256 ? tall_job(a, t, cols, BN, i) : low_job(a, t, cols, BN, i);
-        j.col0 += first_col;
+        GroupedJob j;
+        if (BM <= 128 && of.low) {
+            j = low_job(a, t, of.cols, BN, i);
+        } else {
+            constexpr int kAcross = BN == 256 ? 0 : (BN == 128 ? 1 : 2);   // of 2^kAcross parts
+            j = tall_job(a, t, of.cols, of.width, of.from + (i >> of.cut));
+            const int part = i & ((1 << of.cut) - 1), down = part >> kAcross;
+            j.row0 += down * BM;
+            j.rows = min(j.rows - down * BM, BM);
+            j.col0 += of.first_col + (part & ((1 << kAcross) - 1)) * BN;
+        }
         return j;
     };
     // 8-bit with a gather: the tokens of a tile's rows, into LDS (waves 0 to 3, 64 each), and token m of them, or -1.
@@ -138,17 +155,21 @@ __device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t
     return q;
 }
 
-// How many workgroups' worth of time n tiles of each of `rows` row tiles take, in rounds.
+// The rounds that tiles take, of each of `rows` row tiles as many as cover the columns.
 __device__ __forceinline__ int rounds(int rows, int columns, int width, int G)
 {
     return (rows * ((columns + width - 1) / width) + G - 1) / G;
 }
 
+// What a round of tall tiles 256 x 256 takes, and of their halves, quarters and eighths, in 1 / 97 of it.
+constexpr int kTallCost = 97, kTallCost2 = 56, kTallCost4 = 37, kTallCost8 = 25;
+
 // Row products (dgrad, 8-bit): tall tiles (more than 128 rows), then the experts' last rows.
-//   - Tall tiles are 256 columns wide (the last 128 or fewer: 128), or all 128 (which takes 0.56 of the time) where that
-//     leaves fewer rounds' time.
-//     Measured (us, 256 / 128 wide): 8 experts x 1024 rows, 4096 x 14336: 806 / 1047, 8-bit 457 / 555; 8 x 256 rows,
-//     4096 x 4096: 115 / 87, 8-bit 66 / 40.
+//   - Tall tiles are 256 columns wide (the last 128 or fewer: 128), but those of the last round are cut into 256 x 128,
+//     128 x 128 or 128 x 64 where the workgroups suffice for all of the parts: a round of parts is shorter.  Or all are 128
+//     wide, where that takes less.  Measured (us, the last round whole / halves / quarters / eighths): 528 tiles, 14336
+//     deep: 985 / 945 / 855 / 843, 8-bit 542 / 503 / 458 / 452; 32 tiles, 4096 deep: 85 / 63 / 39 / 27, 8-bit 49 / 37 /
+//     24 / 17.  (All of 8 x 1024 rows, 4096 x 14336, 256 / 128 wide: 806 / 1047, 8-bit 457 / 555.)
 //   - The short ones read the weights for few rows.  A round of tiles 64, 128 and 256 wide takes about 5 : 8 : 15 (narrow
 //     ones read the weights in shorter segments and the rows more often); the width is the one with the least.  Measured
 //     (us, 64 / 128 / 256 wide): 64 experts x 20 rows, 2048 x 2816: 164 / 137 / 128, 8-bit 100 / 74 / 71; 64 x 100 rows,
@@ -159,42 +180,65 @@ __device__ __forceinline__ void rows_all(const GroupedArgs &a, GroupedTables &t,
 {
     const int G = (int)gridDim.x, C = KIND == kI8 ? a.N : a.K;
     const int tall = __builtin_amdgcn_readfirstlane(t.tall[a.E]), low = __builtin_amdgcn_readfirstlane(t.low[a.E]);
-    // The phases' tiles are numbered on, so that workgroups without a tile in one's last round come first in the next.
+    const int full = C / 256, rest = C - full * 256, wide = full + (rest > 128);
     // (Outputs that fit the device have fewer than 2^31 tiles.)
-    int q = xcd_place((int)blockIdx.x, G), n;
-    if (tall > 0) {
-        const int full = C / 256, rest = C - full * 256;
-        if (rounds(tall, C, 128, G) * 56 < rounds(tall, C, 256, G) * 97) {
-            n = tall * ((C + 127) / 128);
-            q = rows_tiles<KIND, 256, 128>(a, t, q, n, (C + 127) / 128, 0, lds, wave, lane) - n;
-        } else {
-            const int wide = full + (rest > 128);
-            n = tall * wide;
-            q = rows_tiles<KIND, 256, 256>(a, t, q, n, wide, 0, lds, wave, lane) - n;
-            if (rest > 0 && rest <= 128)
-                q = rows_tiles<KIND, 256, 128>(a, t, q, tall, 1, full * 256, lds, wave, lane) - tall;
-        }
-    }
-    if (low == 0) return;
+    const int n = tall * wide, last = n % G;   // of the last round
+    int cut = 0, cost = last > 0 ? kTallCost : 0;
+    if (last * 8 <= G) cut = 3, cost = last > 0 ? kTallCost8 : 0;
+    else if (last * 4 <= G) cut = 2, cost = kTallCost4;
+    else if (last * 2 <= G) cut = 1, cost = kTallCost2;
+    const int whole = n / G * kTallCost + cost + (rest > 0 && rest <= 128 ? rounds(tall, 128, 128, G) * kTallCost2 : 0);
+    const bool halves = rounds(tall, C, 128, G) * kTallCost2 < whole;
     const int c256 = rounds(low, C, 256, G) * 15, c128 = rounds(low, C, 128, G) * 8, c64 = rounds(low, C, 64, G) * 5;
     const int width = c256 <= c128 && c256 <= c64 ? 256 : (c128 <= c64 ? 128 : 64);
-    n = low * ((C + width - 1) / width);
-    if (long_tails) {
-        if (width == 256) rows_tiles<KIND, 128, 256>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
-        else if (width == 128) rows_tiles<KIND, 128, 128>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
-        else rows_tiles<KIND, 128, 64>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
-    } else {
-        if (width == 256) rows_tiles<KIND, 32, 256>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
-        else if (width == 128) rows_tiles<KIND, 32, 128>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
-        else rows_tiles<KIND, 32, 64>(a, t, q, n, (C + width - 1) / width, 0, lds, wave, lane);
+    // The tiles of a phase are numbered on from the one before, so that workgroups without a tile in one's last round come
+    // first in the next.
+    int q = xcd_place((int)blockIdx.x, G);
+    for (int phase = 0; phase < 4; ++phase) {
+        Tiles of{0, wide, 0, 256, false, 0, 0};
+        int bm = 256, bn = 256;
+        if (phase == 0) {
+            if (halves) of.cols = (C + 127) / 128, of.width = bn = 128, of.n = tall * of.cols;
+            else of.n = n - last;
+        } else if (phase == 1) {
+            if (!halves) {
+                of.from = n - last, of.cut = cut, of.n = last << cut;
+                bm = cut >= 2 ? 128 : 256;
+                bn = cut == 0 ? 256 : (cut == 3 ? 64 : 128);
+            }
+        } else if (phase == 2) {
+            if (!halves && rest > 0 && rest <= 128) of = Tiles{tall, 1, full * 256, 128, false, 0, 0}, bn = 128;
+        } else {
+            of.cols = (C + width - 1) / width;
+            of.n = low * of.cols;
+            of.low = true;
+            bm = long_tails ? 128 : 32;
+            bn = width;
+        }
+        if (of.n == 0) continue;
+        if (bm == 256) {
+            if (bn == 256) q = rows_tiles<KIND, 256, 256>(a, t, q, of, lds, wave, lane);
+            else q = rows_tiles<KIND, 256, 128>(a, t, q, of, lds, wave, lane);
+        } else if (bm == 128) {
+            if (bn == 256) q = rows_tiles<KIND, 128, 256>(a, t, q, of, lds, wave, lane);
+            else if (bn == 128) q = rows_tiles<KIND, 128, 128>(a, t, q, of, lds, wave, lane);
+            else q = rows_tiles<KIND, 128, 64>(a, t, q, of, lds, wave, lane);
+        } else {
+            if (bn == 256) q = rows_tiles<KIND, 32, 256>(a, t, q, of, lds, wave, lane);
+            else if (bn == 128) q = rows_tiles<KIND, 32, 128>(a, t, q, of, lds, wave, lane);
+            else q = rows_tiles<KIND, 32, 64>(a, t, q, of, lds, wave, lane);
+        }
+        q -= of.n;
     }
 }
 
-// The tasks of the weights' gradient: every expert's full tiles (256 x 256; full of them along N), then its tiles of the last
-// 128 or fewer of N (128 x 256; half: 1 if there are any).  Experts with the most rows first; every other round goes through
-// the workgroups backwards, so that those with a long task get a short one next.
+// The tasks of the weights' gradient: every expert's full tiles (256 x 256), then its half ones (128 x 256): of the last 128
+// or fewer of N, or of all of N where one round holds all of them (8 experts x 512 rows, 1024 x 1024: 12.7 us against 19.8).  Experts with
+// the most rows first; every other round goes through the workgroups backwards, so that those with a long task get a short
+// one next.  The odd XCDs take their tasks from the last to the first: two places of the matrices are then under way
+// (8 x 1024 rows, 4096 x 14336: 853 us against 901 with one; 64 x 768 rows, 2048 x 1408, accumulating: 417 against 437).
 struct WgradTasks {
-    int nk, full, half, per, n;   // tiles along K; tasks an expert, and all of them
+    int nk, full, half, per, n;   // tiles along K; full and half ones along N; tasks an expert, and all of them
     int G, place;
     int rounds;                   // in which this workgroup has a task
     bool backwards;
@@ -225,8 +269,9 @@ __device__ __forceinline__ int wgrad_tiles(const GroupedArgs &a, const GroupedTa
             j.k0 = __builtin_amdgcn_readfirstlane(in / size * 256);
             j.n0 = __builtin_amdgcn_readfirstlane((8 * group + in % size) * 256);
         } else {
-            j.k0 = __builtin_amdgcn_readfirstlane((r - w.nk * w.full) * 256);
-            j.n0 = w.full * 256;
+            const int in = r - w.nk * w.full, row = in / w.nk;
+            j.k0 = __builtin_amdgcn_readfirstlane((in - row * w.nk) * 256);
+            j.n0 = __builtin_amdgcn_readfirstlane(w.full * 256 + row * 128);
         }
         j.e = __builtin_amdgcn_readfirstlane(t.low[i]);
         j.row0 = __builtin_amdgcn_readfirstlane(t.off[j.e]);
@@ -379,9 +424,13 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_wgrad(GroupedArg
     w.nk = (a.K + 255) / 256;
     w.full = a.N / 256 + (a.N % 256 > 128);
     w.half = a.N % 256 > 0 && a.N % 256 <= 128;
+    w.G = (int)gridDim.x;
+    if (experts * w.nk * ((a.N + 127) / 128) <= w.G) {
+        w.full = 0;
+        w.half = (a.N + 127) / 128;
+    }
     w.per = w.nk * (w.full + w.half);
     w.n = experts * w.per;
-    w.G = (int)gridDim.x;
     w.place = xcd_place((int)blockIdx.x, w.G);
     w.rounds = w.n / w.G;
     if (w.dealt(w.rounds) < w.n) ++w.rounds;

@@ -13,10 +13,15 @@ BF = torch.bfloat16
 
 # rows of each expert, contraction, columns of the output
 ROWS = [
-    ([700, 836] * 8, 136, 2120, "48 tall tiles, 256 wide, the last 72 columns 128 wide; short ones 128 wide"),
-    ([700, 836] * 8, 200, 2296, "48 tall tiles of 9 x 256 columns, the last of them ragged"),
-    ([256] * 70, 64, 1288, "70 tall tiles of 5 x 256 columns and 8 columns, no short ones"),
-    ([300, 20] * 4, 520, 136, "few tall tiles: 128 wide; short ones 64 wide"),
+    ([700, 836] * 8, 136, 2120, "48 tall tiles: 256 wide, half a round of halves, the last 72 columns; short ones 128 wide"),
+    ([700, 836] * 8, 200, 2296, "48 tall tiles of 9 x 256 columns, the last of them ragged, all whole"),
+    ([256] * 70, 64, 1288, "70 tall tiles of 5 x 256 columns, the last 94 as halves, and 8 columns, no short ones"),
+    ([256] * 40, 64, 1144, "40 tall tiles, all 128 wide"),
+    ([300, 200] * 11, 264, 2760, "22 tall tiles of 11 x 256 columns, whole"),
+    ([300, 200] * 12, 264, 2760, "24 tall tiles of 11 x 256 columns, the last 8 in eighths"),
+    ([300, 200] * 12, 72, 2696, "24 tall tiles of 11 x 256 columns, the last 8 in eighths, of which some have no columns"),
+    ([250] * 8, 328, 1240, "40 tall tiles in quarters"),
+    ([300, 20] * 4, 520, 136, "4 tall tiles in eighths, a quarter of which have no columns; short ones 64 wide"),
     ([20] * 64, 80, 2040, "64 short tiles of at most 32 rows, 256 wide"),
     ([33, 20] * 32, 80, 2040, "64 short tiles of at most 128 rows, 256 wide"),
     ([25] * 44, 144, 2048, "44 short tiles of at most 32 rows, 128 wide"),
@@ -82,6 +87,8 @@ def test_i8_of_few_rows(counts, K, N, what, gather):
 # rows of each expert, K, N: tasks of full and half tiles in several rounds, from both ends
 GRADIENTS = [
     ([3, 90, 0, 131] * 10, 520, 1400, "720 tasks of 40 experts, a sixth of them half tiles"),
+    ([64, 33, 65, 0, 1], 520, 1000, "120 tasks, all of half tiles"),
+    ([300, 70, 5], 264, 2600, "126 tasks, all of half tiles"),
     ([64, 33, 65, 1] * 16, 264, 1280, "640 tasks, full tiles only"),
     ([40, 0, 7] * 100, 776, 128, "1200 tasks of half tiles only"),
     ([2000, 5, 700, 1] * 4, 1032, 1160, "400 tasks of very different lengths"),
