@@ -34,7 +34,8 @@ __device__ __forceinline__ void sigmoid_both(float g, float &s, float &t)
 //   dy[slot(t, j)] = w[t, j] dout[t],   dw[t, j] = sum_n dout[t, n] y[slot(t, j), n]
 // A workgroup per token keeps the token's dout in registers (pieces of 8 columns, 2048 NP at a time) and goes through its
 // choices, so dout is read once and y and dy once per choice.  A slot that a token names more than once is visited once,
-// with the sum of its gates.  The dot products' partial sums (thread, wave, workgroup) are fp32 in a fixed order.  Bound by memory.
+// with the sum of its gates.  The dot products' partial sums (thread, wave, workgroup) are fp32 in a fixed order.  Bound by memory:
+// 16384 tokens of 7168, one local choice each on the mean (0.7 GB): 136 us, 5.2 TB/s.
 template <int NP>
 __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
 {
@@ -125,7 +126,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
 // Gradient of  h = silu(g) u,  silu(g) = g s,  s = 1 / (1 + e^-g):
 //   dg = dh u s (1 + g (1 - s)),   du = dh g s
 // in fp32, rounded once; h (if asked for) with the expression of the forward kernel, bit for bit.  Item i = 8 columns of a
-// row.  Bound by memory: 6 bytes in, 4 (6 with h) out per feature.
+// row.  Bound by memory: 6 bytes in, 4 (6 with h) out per feature: 8192 rows of 14336 features with h 254 us, 5.5 TB/s.
 __global__ __launch_bounds__(256) void k_swiglu_backward(SwigluBackwardArgs a)
 {
     const int rows = a.rows_valid ? min(a.rows, max(0, *a.rows_valid)) : a.rows;

@@ -6,6 +6,7 @@
 // chunk's choices by expert; in the second every workgroup sums the counts up (totals for the offsets, earlier chunks for
 // its base) and ranks its own choices, 64 at a time per wave: the lanes of a wave that hold the same expert find one
 // another by one ballot per bit of the expert's number.  Bound by latency: a few thousand choices are a few KB.
+// 1024 choices, 32 local experts of 256: 5.2 us in one launch; 49152 choices of 64 experts: 4.9 + 7.3 us.
 #include <hip/hip_runtime.h>
 
 #include "grouped_args.h"

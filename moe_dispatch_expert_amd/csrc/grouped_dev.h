@@ -1,15 +1,15 @@
 // grouped_dev.h -- the tile of the grouped product's gradients (bf16) and of its 8-bit form, on gfx950 matrix cores.
 //
-// A workgroup of eight waves computes BM rows x 256 columns of
+// A workgroup of eight waves computes BM rows x BN columns of
 //   out[m, n] = sum_l Q[m, l] P[n, l]
 // P is the matrix instructions' A operand, so a lane ends with four neighbouring columns of a row.  The three products
 // differ in which index of an operand is contiguous in memory:
 //   dgrad  out = da,    P[i, n] = W[e, n, i] (rows along the contraction),  Q[r, n] = dy[r, n] (contraction contiguous)
 //   wgrad  out = dW[e], P[i, r] = a[r, i] and Q[n, r] = dy[r, n] (rows along the contraction both)
 //   8-bit  out = y,     P[n, i] = w[e, n, i] and Q[r, i] = a[r, i] (contraction contiguous both)
-// The contraction runs in slabs of 128 bytes of an operand's row (64 bf16, 128 int8), straight from memory into LDS
-// (buffer_load ... lds, 1 KiB a load), into a ring of two to eight stages; four matrix instruction steps a slab, the
-// fragments of step s + 1 read during the products of step s, one barrier a slab, before its last step.
+// The contraction runs in slabs of 64 bf16 or 128 int8 (wgrad's full tile with rows in place: 32), straight from memory into
+// LDS (buffer_load ... lds, 1 KiB a load), into a ring of two to eight stages; four matrix instruction steps a slab (32 rows:
+// two), the fragments of step s + 1 read during the products of step s, one barrier a slab, before its last step.
 //   - Contraction contiguous: LDS rows of 128 bytes, 16-byte chunk c of row r at c ^ ((r >> 1) & 7); a fragment is one
 //     16-byte read.
 //   - Rows along the contraction: 64 LDS rows of 2 C bytes; a fragment is two transposing reads (ds_read_b64_tr_b16: 16
@@ -20,6 +20,12 @@
 // whatever lies behind them.
 // A tile's first slabs are loaded before the outputs of the tile before it are stored (these go through the upper half of
 // the stages' LDS).
+// Bound by the matrix cores: 256 x 256 with 8 waves is the largest tile whose sums (128 registers a lane) and fragments stay in
+// registers; a slab of it takes 1.6 us (bf16), and beginning and ending a tile 5.3 us, of which the stores are 2.7.  8192^3, one
+// matrix (us and rate): dgrad 808 (1360 TFLOP/s), wgrad 812 (1354), 8-bit 432 (2550 TOP/s); large library products reach 1377
+// and 2083 on such a card.  Measured and not taken (the same, or 8 x 1024 rows of 4096 x 14336): four waves of 128 x 128 (no
+// gain), sums in accumulation registers (8-bit 4% slower: moves and spills), 64-byte slabs for dgrad and 8-bit (3% slower),
+// lines asked for 3 to 6 slabs ahead by 4-byte loads (7% slower: the address unit is what is scarce).
 #pragma once
 
 #include "gemm_dev.h"
@@ -427,6 +433,8 @@ __device__ __forceinline__ void store_bf16(F &&value, uint16_t *out, int ldc, in
     }
 }
 
+// (Through LDS because the width of a store matters: wgrad of 8 x 1024 rows, 4096 x 14336, in fp32 took 1194 us with 32 bytes a
+// row from the registers, 1177 with 64, 1108 with 256 and 1035 with 512.)
 // The same in fp32, 16 rows at a time (4 NI MI stores a wave), added to what is there where add is set.
 template <class T, class F>
 __device__ __forceinline__ void store_f32(F &&value, float *out, int ldc, int rows, int cols, bool add, lds_char_t *lds,
