@@ -487,7 +487,8 @@ mk_status mk_swiglu_backward(const void *gate_up, const void *dh, int32_t rows, 
  *   w [E_local, N, K] bf16 (as for mk_grouped_gemm)
  *   da [rows, K] bf16 (out; rows >= offsets[E_local] untouched)
  * Requires rows >= 0, 1 <= E_local <= 1024, N > 0, K > 0, N % 8 == 0, K % 8 == 0;
- * N, K <= 2^20 (else MK_EUNSUPPORTED).  rows == 0 is a no-op.  No workspace. */
+ * N, K <= 2^20 and rows <= 2^31 - 4096 (else MK_EUNSUPPORTED).  rows == 0 is a
+ * no-op.  No workspace. */
 mk_status mk_grouped_gemm_dgrad(const void *dy, int32_t rows, const int32_t *expert_offsets, int32_t E_local,
                                 const void *w, int32_t K, int32_t N, void *da, void *stream);
 
@@ -541,7 +542,7 @@ mk_status mk_swiglu_i8(const void *gate_up, int32_t rows, int32_t F, const int32
  *   w [E_local, N, K] int8 (K contiguous)     w_scale [E_local, N] fp32
  *   y [rows, N] bf16 (out; rows >= offsets[E_local] untouched)
  * Requires rows >= 0, 1 <= E_local <= 1024, N > 0, K > 0, N % 8 == 0, K % 16 == 0;
- * K < 2^17 (int32 sums), N <= 2^20 and, with row_token, a_rows >= 0,
+ * K < 2^17 (int32 sums), N <= 2^20, rows <= 2^31 - 4096 and, with row_token, a_rows >= 0,
  * a_rows * K <= 2^32 - 512 (else MK_EUNSUPPORTED).  rows == 0 is a no-op.  No
  * workspace. */
 mk_status mk_grouped_gemm_i8(const void *a, const float *a_scale, int32_t rows, const int32_t *expert_offsets,

@@ -646,7 +646,8 @@ mk_status check_layout_shape(int32_t T, int32_t k, int32_t e_begin, int32_t E_lo
 mk_status check_grouped_shape(int32_t rows, int32_t E_local, int32_t K, int32_t N, int32_t step)
 {
     if (rows < 0 || E_local < 1 || K <= 0 || N <= 0 || K % step != 0 || N % 8 != 0) return MK_EINVAL;
-    if (E_local > kGroupedMaxE || K > kGroupedMaxDim || N > kGroupedMaxDim) return MK_EUNSUPPORTED;
+    if (rows > kGroupedMaxRows || E_local > kGroupedMaxE || K > kGroupedMaxDim || N > kGroupedMaxDim)
+        return MK_EUNSUPPORTED;
     return MK_OK;
 }
 

@@ -46,10 +46,10 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
     __shared__ float s_dot[kMaxK][4];
     const int ti = (int)threadIdx.x, wave = ti / kWave, lane = ti % kWave;
     const int pieces = a.N / 8;
-    for (int t = (int)blockIdx.x; t < a.T; t += (int)gridDim.x) {
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         if (wave == 0) {
-            const int slot = lane < a.k ? a.slot_of[(size_t)t * a.k + lane] : -1;
-            const float w = lane < a.k ? a.gate[(size_t)t * a.k + lane] : 0.0f;
+            const int slot = lane < a.k ? a.slot_of[t * a.k + lane] : -1;
+            const float w = lane < a.k ? a.gate[t * a.k + lane] : 0.0f;
             float sum = 0.0f;
             int first = lane;
             for (int j = a.k - 1; j >= 0; --j) {
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
             u32x4_t d[NP];
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                d[i] = *(const u32x4_t *)(a.dout + (size_t)t * a.N + 8 * min(p0 + ti + 256 * i, pieces - 1));
+                d[i] = *(const u32x4_t *)(a.dout + t * a.N + 8 * min(p0 + ti + 256 * i, pieces - 1));
             // U choices at a time: their rows are all asked for before the first is used
             for (int j0 = 0; j0 < a.k; j0 += U) {
                 u32x4_t v[U][NP];
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
         __syncthreads();
         if (a.dgate && ti < a.k) {
             const float *d = s_dot[s_first[ti]];
-            a.dgate[(size_t)t * a.k + ti] = (d[0] + d[1]) + (d[2] + d[3]);
+            a.dgate[t * a.k + ti] = (d[0] + d[1]) + (d[2] + d[3]);
         }
         __syncthreads();   // the tables are free for the next token
     }

@@ -7,6 +7,7 @@ namespace mk {
 
 constexpr int kGroupedMaxE = 1024;          // experts: their offsets are scanned in LDS
 constexpr int kGroupedMaxDim = 1 << 20;     // N and K: a tile's 256 rows then stay inside 32-bit offsets
+constexpr int kGroupedMaxRows = 0x7FFFFFFF - 4095;   // the ends of an expert's last tile and slabs then have 32 bits too
 constexpr int kI8MaxK = 131072;             // 131072 products of -128 * -128 would pass int32
 constexpr int kQuantMaxD = 32768;           // a workgroup of 1024 threads holds the row: 4 pieces of 8 columns each
 

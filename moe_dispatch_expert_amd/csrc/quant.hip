@@ -41,8 +41,10 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES) void k_quant_i8(QuantArg
 {
     constexpr int ROWS = LANES < 256 ? 256 / LANES : 1;
     const int ti = (int)threadIdx.x % LANES;
-    const int r = row0 + (int)blockIdx.x * ROWS + (ROWS > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / LANES) : 0);
-    if (r >= (a.rows_valid ? min(a.rows, *a.rows_valid) : a.rows)) return;   // the same for all threads of a row
+    const uint32_t r =   // (the last workgroup's may pass 2^31)
+        (uint32_t)row0 + blockIdx.x * ROWS + (ROWS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / LANES) : 0u);
+    const int rows = a.rows_valid ? min(a.rows, max(0, *a.rows_valid)) : a.rows;
+    if (r >= (uint32_t)rows) return;   // the same for all threads of a row
     const int pieces = a.d / 8;
     const uint16_t *x = a.x + (size_t)r * a.d * (SWIGLU ? 2 : 1);
     float v[NP][8];

@@ -189,3 +189,15 @@ def test_binding_names_the_wrong_tensor():
                      (lambda: mk.mk_grouped_gemm_i8(Q, S, OFF, Q.view(2, 2, 64), S), "w_scale")):
         with pytest.raises(ValueError, match=word):
             fn()
+
+
+def test_rows_whose_tiles_would_pass_32_bits_are_refused():
+    for rows, st in ((2 ** 31 - 4096, mk.MK_EINVAL), (2 ** 31 - 4095, mk.MK_EUNSUPPORTED), (2 ** 31 - 1, mk.MK_EUNSUPPORTED)):
+        for name, names, args in (
+                ("mk_grouped_gemm_dgrad", ("dy", "rows", "off", "E", "w", "K", "N", "da"),
+                 dict(dy=None, off=C, E=8, w=D, K=64, N=64, da=F)),
+                ("mk_grouped_gemm_wgrad", ("dy", "a", "rows", "off", "E", "rt", "ar", "K", "N", "dw", "fp32", "acc"),
+                 dict(dy=None, a=B, off=C, E=8, rt=None, ar=0, K=64, N=64, dw=D, fp32=1, acc=0)),
+                ("mk_grouped_gemm_i8", ("a", "s", "rows", "off", "E", "rt", "ar", "w", "ws", "K", "N", "y"),
+                 dict(a=None, s=B, off=C, E=8, rt=None, ar=0, w=D, ws=F, K=64, N=64, y=G))):
+            assert _caller(name, names, dict(rows=rows, **args))() == st, (name, rows)
