@@ -131,6 +131,16 @@ def test_offsets_past_the_last_one_are_cut_to_it():
         assert torch.equal(out[:10].cpu(), ref.i8(codes, s, cut, w, ws, rt)[:10]) and (out[10:] == 7.0).all()
 
 
+def test_no_tokens_to_read():
+    """Rows that would read tokens, of which there are none: zeros, or nothing added."""
+    off, rt = torch.tensor([0, 40, 300], dtype=torch.int32).cuda(), torch.zeros(300, dtype=torch.int32).cuda()
+    dy, none = torch.ones(300, 136, dtype=BF, device="cuda"), torch.empty(0, 264, dtype=BF, device="cuda")
+    assert (mk.mk_grouped_gemm_wgrad(dy, none, off, row_token=rt) == 0).all()
+    out = torch.full((2, 136, 264), 3.0, device="cuda")
+    mk.mk_grouped_gemm_wgrad(dy, none, off, row_token=rt, out=out, accumulate=True)
+    assert (out == 3.0).all()
+
+
 def test_a_row_of_dgrad_has_the_same_bits_in_any_batch():
     g = torch.Generator().manual_seed(2)
     dy, w = torch.randn(1600, 520, generator=g).to(BF).cuda(), torch.randn(2, 520, 264, generator=g).to(BF).cuda()
