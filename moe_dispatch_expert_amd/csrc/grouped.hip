@@ -54,16 +54,17 @@ __device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t
         }
         return j;
     };
-    // 8-bit with a gather: the tokens of a tile's rows, into LDS (waves 0 to 3, 64 each), and token m of them, or -1.
+    // 8-bit with a gather: the tokens of a tile's rows, into LDS (waves 0 to 3, 64 each), and token m of them, or -1.  Waves
+    // that are through with a run's first begin() load the next tile's while others still read this one's: a place for each.
     const bool gather = KIND == kI8 && a.row_token;
-    auto tokens = [&](const GroupedJob &j) {
+    auto tokens = [&](const GroupedJob &j, int buf) {
         if (gather && wave < 4)
             lds_load4(make_rsrc4(a.row_token + j.row0, (size_t)j.rows * 4),
-                      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char_t *)&t.tok[64 * wave]),
+                      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_char_t *)&t.tok[tile_tokens_at(buf) + 64 * wave]),
                       (uint32_t)(64 * wave + lane) * 4u);
     };
-    auto token = [&](const GroupedJob &j, int m) {
-        const int v = t.tok[m & 255];
+    auto token = [&](const GroupedJob &j, int m, int buf) {
+        const int v = t.tok[tile_tokens_at(buf) + (m & (kTokenRows - 1))];
         return m < j.rows && v >= 0 && v < a.a_rows ? v : -1;
     };
     // The loads of a tile's scales (8-bit) and of its first slab.
@@ -81,7 +82,7 @@ __device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t
                       wave, lane, [&](int c, int) { return j.col0 + c < a.N ? (uint32_t)c * rb : kPastResource; });
             if (gather)
                 side_rows(tl.q, make_rsrc4(a.a, (size_t)a.a_rows * a.K), wave, lane, [&](int m, int) {
-                    const int v = token(j, m);
+                    const int v = token(j, m, buf);
                     return v >= 0 ? (uint32_t)v * rb : kPastResource;
                 });
             else
@@ -93,7 +94,7 @@ __device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t
             const bool rows = wave < 4;
             uint32_t o = kPastResource;
             if (rows) {
-                const int v = gather ? token(j, i) : (i < j.rows ? i : -1);
+                const int v = gather ? token(j, i, buf) : (i < j.rows ? i : -1);
                 if (v >= 0) o = (uint32_t)v * 4u;
             } else if (i < BN && j.col0 + i < a.N) {
                 o = (uint32_t)i * 4u;
@@ -107,20 +108,20 @@ __device__ __forceinline__ int rows_tiles(const GroupedArgs &a, GroupedTables &t
 #pragma unroll
         for (int i = 0; i < T::PRE; ++i) tl.load_slab(i);
     };
+    int buf = 0;
     GroupedJob job = job_of(q);
-    tokens(job);
+    tokens(job, buf);
     wait_vmem_all();
     __syncthreads();
     TL tl;
     tl.dst = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + (uint32_t)wave * 1024u);
-    int buf = 0;
     begin(job, tl, buf);
     for (bool first = true;; first = false) {
         const bool more = q + G < n;
         GroupedJob next = job;
         if (more) {
             next = job_of(q + G);
-            tokens(next);
+            tokens(next, buf ^ 1);
         }
         typename Acc<KIND>::type acc[T::NI][T::MI];
         tile_sums<T, false, STORES>(tl, !first, NoTokens{}, lds, wave, lane, acc);

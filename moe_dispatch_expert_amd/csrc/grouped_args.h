@@ -26,6 +26,13 @@ struct GroupedArgs {
     int32_t out_f32, accumulate;
 };
 
+// 8-bit product with a gather: where the tokens of a tile's rows lie in their table, by the tile's parity in a workgroup's run.
+// The next tile's tokens are loaded from the start of a tile's products on, without a barrier after the reads of the first
+// tile's own, so two tiles that follow one another have places of their own.
+constexpr int kTokenRows = 256;                      // rows of the tallest tile
+constexpr int kTokenTable = 2 * kTokenRows;
+__host__ __device__ constexpr int tile_tokens_at(int parity) { return (parity & 1) * kTokenRows; }
+
 struct CombineBackwardArgs {
     const uint16_t *dout, *y;   // [T, N], [rows, N] bf16
     const int32_t *slot_of;     // [T, k]

@@ -496,7 +496,7 @@ struct GroupedTables {
                                        // wgrad: low[i] = the expert with the i-th most rows
     uint64_t wave_sum[kGroupedWaves];
     float scale[2][2][256];            // 8-bit: scales of a tile's rows and columns, of two tiles in turn
-    int32_t tok[256];                  // 8-bit: the next tile's rows of `a`
+    int32_t tok[kTokenTable];          // 8-bit: rows of `a` of two tiles in turn (tile_tokens_at)
 };
 static_assert(kGroupedStages + sizeof(GroupedTables) <= 160 * 1024, "LDS");
 
