@@ -362,10 +362,9 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_dgrad(GroupedArg
     rows_all<kDgrad>(a, t, n.long_tails, (lds_char_t *)stages, wave, lane);
 }
 
-// The 8-bit product.  Few rows (at most 16 to an expert that has any, 512 together) are a stream of the weights, else tiles.
-// Measured (us, stream / tiles): 8 experts of 4096 x 14336 (470 MB): 1 row each 68 / 103, 16 rows 74 / 109, 24 rows (two
-// passes over the weights) 136 / 112; 32 of 2048 x 1408, 1 row 19 / 25, 16 rows 24 / 27.  68 us is 6.9 TB/s.  Tiles are bound by
-// the matrix cores: 8 x 1024 rows, K = 4096, N = 14336: 440 us (2190 TOP/s).
+// The 8-bit product.  Few rows (512 at most, and hardly more than 16 to an expert: few_width) are a stream of the weights,
+// else tiles.  Measured (us, stream / tiles): 8 experts of 4096 x 14336 (470 MB): 1 row each 68 / 103, 16 rows 74 / 109, 24 rows
+// (two passes over the weights) 136 / 112.  68 us is 6.9 TB/s.  Tiles are bound by the matrix cores: 8 x 1024 rows, K = 4096, N = 14336: 440 us (2190 TOP/s).
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(1024))) union {
@@ -384,12 +383,23 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
     const TableTotals n = tables_rows(a, m.tile.t);
     const int R = __builtin_amdgcn_readfirstlane(m.tile.t.off[a.E]), H = __builtin_amdgcn_readfirstlane(n.hits);
-    if (R <= kFewRows && R <= kFewGroup * H) {
+    int width = 0;
+    if (R <= kFewRows) {   // (every wave of the launch finds the same)
+        int passes = 0, most = 1;
+        if (R > kFewGroup) {
+            for (int e = lane; e < a.E; e += kWave) {
+                const int p = (table_count(m.tile.t, e) + kFewGroup - 1) / kFewGroup;
+                passes += p;
+                most = max(most, p);
+            }
+            most = (int)wave_max_u32((uint32_t)most);
+            if (most > 1) passes = (int)wave_sum_f32((float)passes);   // (whole numbers below 2^24)
+        }
+        width = few_width(H, passes, most, a.N, (int)gridDim.x, a.per_grid);
+    }
+    if (width) {
         few_tables(a, m.tile.t, m.few.t, n.before);
-        // The width of a weight tile: 32, or 16 where that leaves the workgroup with the most tasks less to read.
-        const int G = (int)gridDim.x;
-        const int w32 = (H * ((a.N + 31) / 32) + G - 1) / G * 32, w16 = (H * ((a.N + 15) / 16) + G - 1) / G * 16;
-        if (w16 < w32) few_rows<16>(a, m.few.t, H, (lds_char_t *)m.few.ring, wave, lane);
+        if (width == 16) few_rows<16>(a, m.few.t, H, (lds_char_t *)m.few.ring, wave, lane);
         else few_rows<32>(a, m.few.t, H, (lds_char_t *)m.few.ring, wave, lane);
     } else {
         rows_all<kI8>(a, m.tile.t, n.long_tails, (lds_char_t *)m.tile.stages, wave, lane);
@@ -493,7 +503,9 @@ hipError_t launch_grouped_i8(const GroupedArgs &a, hipStream_t s)
 {
     const int grid = persistent_grid();
     if (grid <= 0) return hipErrorInvalidDevice;
-    hipLaunchKernelGGL(k_grouped_i8, dim3(grid), dim3(kGroupedThreads), 0, s, a);
+    GroupedArgs b = a;
+    b.per_grid = inverse_of(grid);
+    hipLaunchKernelGGL(k_grouped_i8, dim3(grid), dim3(kGroupedThreads), 0, s, b);
     return hipGetLastError();
 }
 

@@ -24,6 +24,7 @@ struct GroupedArgs {
     const float *w_scale;       // 8-bit: [E, N]
     void *out;                  // dgrad [rows, K] bf16;  wgrad [E, N, K] fp32 or bf16;  8-bit [rows, N] bf16
     int32_t out_f32, accumulate;
+    uint32_t per_grid;          // 8-bit: inverse_of the workgroups
 };
 
 // 8-bit product with a gather: where the tokens of a tile's rows lie in their table, by the tile's parity in a workgroup's run.
@@ -32,6 +33,41 @@ struct GroupedArgs {
 constexpr int kTokenRows = 256;                      // rows of the tallest tile
 constexpr int kTokenTable = 2 * kTokenRows;
 __host__ __device__ constexpr int tile_tokens_at(int parity) { return (parity & 1) * kTokenRows; }
+
+// 8-bit product: the stream of the weights for few rows (grouped_few.h) against the tiles.
+constexpr int kFewRows = 512;   // rows the stream takes (its tables)
+constexpr int kFewGroup = 16;   // rows a pass over a weight tile
+
+// ceil(n / G) as a product with inv = inverse_of(G): shorter than the divisions that the compiler makes, of code that runs once
+// a launch.  Exact below 2^32 / G, and for every G that is a power of two; above, it may be one more.
+__host__ __device__ constexpr uint32_t inverse_of(int G) { return (uint32_t)((((uint64_t)1 << 32) + G - 1) / G); }
+__host__ __device__ inline int rounds_of(int n, int G, uint32_t inv)
+{
+    return (int)(((uint64_t)(uint32_t)(n + G - 1) * inv) >> 32);
+}
+
+// Rows of a weight tile (32, or 16 where that leaves the workgroup with the most tasks less to read) with which G workgroups
+// stream the weights of H experts with rows, or 0 for the tiles.  passes: the experts' passes of kFewGroup rows together; most: of
+// the expert with the most.  A workgroup goes through the passes of its weight tiles one after another, so what counts is the
+// busiest one's: its share of all tiles, and beyond that the longest expert's other passes or the mean of all others, whichever is
+// more.  The stream is taken for at most 10 / 7 of the passes that one a tile would be (3 for 2), or if no more weight rows are
+// read one after another than the tiles' narrowest form has.  Measured (us, stream / tiles):
+//   32 experts of 2816 x 2048, a row each but for one of 17: 33 / 41, of 64: 37 / 44, of 128: 45 / 44, of 256: 64 / 47, of 480:
+//   98 / 48; 16 of 17 rows and 16 of 2: 45 / 41;  32 of 2048 x 1408, 16 rows each: 26 / 23 (the one case of a pass each that loses);
+//   8 of 14336 x 4096, a row each but for one of 17: 82 / 110, of 64: 100 / 117, of 96: 118 / 118, of 128: 136 / 118;
+//   8 of 2048 x 2048, of 17: 13 / 15, of 48: 17 / 14;  one of 4096 x 14336, 17 rows: 23 / 38, 48: 35 / 42, 64: 45 / 44, 128: 85 / 56;
+//   one of 14336 x 4096, 16 rows: 17 / 20, 17: 25 / 20.
+__host__ __device__ inline int few_width(int H, int passes, int most, int N, int G, uint32_t inv)
+{
+    const int t32 = (N + 31) / 32, t16 = (N + 15) / 16;
+    const int once32 = rounds_of(H * t32, G, inv), once16 = rounds_of(H * t16, G, inv);
+    const bool narrow = once16 < 2 * once32;
+    const int width = narrow ? 16 : 32, tiles = narrow ? t16 : t32, once = narrow ? once16 : once32;
+    if (most <= 1) return width;
+    const int longest = (most - 1) * rounds_of(tiles, G, inv), mean = rounds_of((passes - H) * tiles, G, inv);
+    const int busiest = once + (longest > mean ? longest : mean);
+    return 7 * busiest <= 10 * once + 1 || busiest * width <= 64 ? width : 0;
+}
 
 struct CombineBackwardArgs {
     const uint16_t *dout, *y;   // [T, N], [rows, N] bf16

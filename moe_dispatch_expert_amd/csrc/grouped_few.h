@@ -15,8 +15,6 @@
 
 namespace mk {
 
-constexpr int kFewRows = 512;       // rows this form takes (its tables)
-constexpr int kFewGroup = 16;       // rows a pass over a weight tile
 constexpr int kFewStages = 3;
 constexpr int kFewStageBytes = (32 + kFewGroup) * 128;
 constexpr int kFewRing = kFewStages * kFewStageBytes;       // one wave's

@@ -32,3 +32,26 @@ def test_rows_read_in_place_are_those_of_their_tile(counts, K, N):
     t = rt[R - last:]
     part = ref.i8(a[t.long()], s[t.long()], torch.tensor([0, last], dtype=torch.int32), w[E - 1:], ws[E - 1:])
     assert torch.equal(want[R - last:].cpu(), part)
+
+
+# rows of the experts, K, N: where the stream of the weights for few rows ends, at uneven counts
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,K,N", [
+    ([1, 0, 481] + [1] * 30, 272, 1408),        # the most rows of one expert: tiles
+    ([1, 0, 100] + [1] * 30, 272, 2816),        # seven passes of one expert: the stream
+    ([17] * 16 + [2] * 16, 144, 2816),          # two passes of many: tiles
+    ([17] * 4 + [2] * 28, 144, 2816),           # of few: the stream
+    ([64], 1040, 4088),                         # four passes of one expert's narrow tiles
+    ([65], 1040, 4088),
+    ([33, 1], 400, 4096),
+    ([40] * 8, 400, 504),
+], ids=lambda v: None if not isinstance(v, list) else f"{len(v)}x{max(v)}")
+def test_uneven_counts_of_few_rows(counts, K, N, gather):
+    g = torch.Generator().manual_seed(K + N + len(counts))
+    R, E, off = sum(counts), len(counts), ref.offsets_of(counts)
+    T = 77 if gather else R
+    a, s = torch.randint(-128, 128, (T, K), generator=g).to(torch.int8), torch.rand(T, generator=g) + 0.1
+    w, ws = torch.randint(-128, 128, (E, N, K), generator=g).to(torch.int8), torch.rand(E, N, generator=g) + 0.1
+    rt = torch.randint(-4, T + 4, (R,), generator=g, dtype=torch.int32) if gather else None
+    got = mk.mk_grouped_gemm_i8(*(t.cuda() for t in (a, s, off, w, ws)), row_token=None if rt is None else rt.cuda())
+    assert torch.equal(got.cpu(), ref.i8(a, s, off, w, ws, rt))
