@@ -4,6 +4,7 @@
 
 #include <algorithm>
 
+#include "far_gate.h"
 #include "gemm_dev.h"
 #include "grouped_args.h"
 #include "mk_device.h"
@@ -125,8 +126,8 @@ __global__ __launch_bounds__(256) void k_combine_backward(CombineBackwardArgs a)
 
 // Gradient of  h = silu(g) u,  silu(g) = g s,  s = 1 / (1 + e^-g):
 //   dg = dh u s (1 + g (1 - s)),   du = dh g s
-// in fp32, rounded once; h (if asked for) with the expression of the forward kernel, bit for bit.  Item i = 8 columns of a
-// row.  Bound by memory: 6 bytes in, 4 (6 with h) out per feature: 8192 rows of 14336 features with h 254 us, 5.5 TB/s.
+// in fp32, rounded once; h (if asked for) with the expression of the forward kernel, bit for bit.  Gates below -80, where s = e^g to
+// within fp32, keep its exponent apart, so that dh and u may make up for it.  Item i = 8 columns of a row.  Bound by memory: 6 bytes in, 4 (6 with h) out per feature: 8192 rows of 14336 features with h 254 us, 5.5 TB/s.
 __global__ __launch_bounds__(256) void k_swiglu_backward(SwigluBackwardArgs a)
 {
     const int rows = a.rows_valid ? min(a.rows, max(0, *a.rows_valid)) : a.rows;
@@ -136,7 +137,8 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(SwigluBackwardArgs a)
         const int64_t r = i / P;
         const int c = (int)(i - r * P) * 8;
         float g[8], u[8], d[8], dg[8], du[8];
-        unpack8(*(const u32x4_t *)(a.gu + r * 2 * a.F + c), g);
+        const u32x4_t gates = *(const u32x4_t *)(a.gu + r * 2 * a.F + c);
+        unpack8(gates, g);
         unpack8(*(const u32x4_t *)(a.gu + r * 2 * a.F + a.F + c), u);
         unpack8(*(const u32x4_t *)(a.dh + r * a.F + c), d);
 #pragma unroll
@@ -145,6 +147,17 @@ __global__ __launch_bounds__(256) void k_swiglu_backward(SwigluBackwardArgs a)
             sigmoid_both(g[q], s, s1);
             dg[q] = d[q] * (s * __builtin_fmaf(g[q], s1, 1.0f)) * u[q];
             du[q] = d[q] * (g[q] * s);
+        }
+        if (__builtin_expect(any_far(gates), 0)) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (!is_far(bf16_of(gates, q))) continue;
+                int n;
+                const float e = far_exp(g[q], n), f = fmaxf(g[q], -400.0f), de = apart(d[q], n) * e;
+                du[q] = ldexpf(de * f, n);
+                const float due = de * apart(u[q], n);
+                dg[q] = ldexpf(due * (1.0f + f), n);
+            }
         }
         *(u32x4_t *)(a.dgu + r * 2 * a.F + c) = pack8(dg);
         *(u32x4_t *)(a.dgu + r * 2 * a.F + a.F + c) = pack8(du);

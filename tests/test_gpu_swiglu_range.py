@@ -98,3 +98,28 @@ def test_rows_of_zeros_and_what_is_not_finite():
     for r in (4, 5, 6, 7, 8, 9, 10):
         assert (q[r] == 0).all() and s[r].isnan(), r
     _check(gu[[0, 11]])
+
+
+@pytest.mark.parametrize("F", [8, 704])
+def test_gradient_of_gates_far_below_zero(F):
+    """mk_swiglu_backward where s = 1 / (1 + e^-g) is below fp32's range and the gradients are not: dg = dh u s (1 + g (1 - s)), du =
+    dh g s within 2^-20 for the operations (see test_gpu_ffn_backward.py) and a bf16 rounding; what is below 2^-126 may be flushed."""
+    g = torch.Generator().manual_seed(F)
+    rows = 160
+    gate = (-75.0 - torch.arange(rows) * 0.9)[:, None] + 0.5 * torch.rand(rows, F, generator=g)
+    lift = ((-gate[:, :1]).double() * 1.4427 / 2).floor()   # dh and u each make up for half of e^g
+    u = (torch.randn(rows, F, generator=g).double() * 2.0 ** lift.clamp(max=120)).to(BF)
+    dh = (torch.randn(rows, F, generator=g).double() * 2.0 ** lift.clamp(max=120)).to(BF)
+    gate = gate.to(BF)
+    gate[0, :4] = torch.tensor([-80.0, -80.5, -1e30, torch.finfo(BF).min]).to(BF)
+    got = mk.mk_swiglu_backward(torch.cat([gate, u], 1).cuda(), dh.cuda())["dgate_up"].cpu().double()
+    a, U, d = gate.double(), u.double(), dh.double()
+    e = torch.exp(a)
+    s, s1 = e / (1 + e), 1 / (1 + e)
+    dg, du = d * U * s * (1 + a * s1), d * a * s
+    assert (dg[1:].abs() > 2.0 ** -100).all() and (dg.abs() < 2.0 ** 127).all()
+    assert ((got[:, :F] - dg).abs() <= (2.0 ** -8 + 2.0 ** -19) * dg.abs() + 2.0 ** -126).all()
+    assert ((got[:, F:] - du).abs() <= (2.0 ** -8 + 2.0 ** -20) * du.abs() + 2.0 ** -126).all()
+    h = mk.mk_swiglu(torch.cat([gate, u], 1).cuda())
+    both = mk.mk_swiglu_backward(torch.cat([gate, u], 1).cuda(), dh.cuda(), h=True)
+    assert torch.equal(both["h"], h) and torch.equal(both["dgate_up"].cpu().double(), got)
