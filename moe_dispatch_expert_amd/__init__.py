@@ -625,6 +625,12 @@ def mk_moe_layer_q8(x_q8: torch.Tensor, x_scale: torch.Tensor, w_gate_up: torch.
 _I8 = torch.int8
 
 
+def _counted(what: str, *counts: int) -> None:
+    """The C ABI's counts have 32 bits, and ctypes would cut larger ones down to them."""
+    if max(counts) > 0x7FFFFFFF:
+        raise ValueError(f"{what}: sizes of at most 2^31 - 1 are supported, got {counts}")
+
+
 def _outputs(what, given, dev, stream, wanted):
     """The output tensors of a call by name, those of `given` checked, the others allocated: (dict, made).  wanted: name ->
     (dtype, shape)."""
@@ -653,6 +659,7 @@ def mk_expert_layout(topk_ids: torch.Tensor, E_local: int, e_begin: int = 0, *, 
     first expert_offsets[E_local] are written, workspace); tensors given in `out` under these names receive them."""
     what = "mk_expert_layout"
     T, k = topk_ids.shape
+    _counted(what, T, k, E_local, e_begin)
     dev = topk_ids.device
     lib = _lib or load()
     pi = _need(what, "topk_ids", topk_ids, dev, _I32, (T, k))
@@ -680,6 +687,7 @@ def mk_combine_backward(dout: torch.Tensor, y_perm: torch.Tensor, slot_of: torch
     T, N = dout.shape
     k = slot_of.shape[1]
     rows = y_perm.shape[0]
+    _counted(what, T, k, N, rows)
     dev = dout.device
     pd = _need(what, "dout", dout, dev, _BF16, (T, N))
     py = _need(what, "y_perm", y_perm, dev, _BF16, (rows, N))
@@ -704,6 +712,7 @@ def mk_swiglu_backward(gate_up: torch.Tensor, dh: torch.Tensor, *, h: bool = Fal
     they are).  Tensors given in `out` receive the outputs (dgate_up may be gate_up, h may be dh)."""
     what = "mk_swiglu_backward"
     rows, F = dh.shape
+    _counted(what, rows, F)
     dev = dh.device
     pg = _need(what, "gate_up", gate_up, dev, _BF16, (rows, 2 * F))
     pd = _need(what, "dh", dh, dev, _BF16, (rows, F))
@@ -725,6 +734,7 @@ def mk_grouped_gemm_dgrad(dy: torch.Tensor, expert_offsets: torch.Tensor, w: tor
     what = "mk_grouped_gemm_dgrad"
     E_local, N, K = w.shape
     rows = dy.shape[0]
+    _counted(what, rows, E_local, N, K)
     dev = dy.device
     pd = _need(what, "dy", dy, dev, _BF16, (rows, N))
     po = _need(what, "expert_offsets", expert_offsets, dev, _I32, (E_local + 1,))
@@ -747,6 +757,7 @@ def mk_grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, expert_offsets: tor
     a_rows, K = a.shape
     dev = dy.device
     E_local = expert_offsets.shape[0] - 1
+    _counted(what, rows, N, a_rows, K, E_local)
     if dtype is not _F32 and dtype is not _BF16:
         raise ValueError(f"{what}: dtype must be torch.float32 or torch.bfloat16, got {dtype}")
     if accumulate and out is None:
@@ -763,6 +774,7 @@ def mk_grouped_gemm_wgrad(dy: torch.Tensor, a: torch.Tensor, expert_offsets: tor
 
 
 def _quant_i8(what, x, rows, d, rows_valid, out, stream) -> dict:
+    _counted(what, rows, d)
     dev = x.device
     px = _need(what, "x" if what == "mk_quant_i8" else "gate_up", x, dev, _BF16, x.shape)
     pv = _may(what, "rows_valid", rows_valid, dev, _I32, (1,))
@@ -803,6 +815,7 @@ def mk_grouped_gemm_i8(a: torch.Tensor, a_scale: torch.Tensor, expert_offsets: t
     E_local, N, K = w.shape
     a_rows = a.shape[0]
     rows = a_rows if row_token is None else row_token.shape[0]
+    _counted(what, rows, a_rows, E_local, N, K)
     dev = a.device
     pa = _need(what, "a", a, dev, _I8, (a_rows, K))
     ps = _need(what, "a_scale", a_scale, dev, _F32, (a_rows,))
