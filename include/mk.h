@@ -495,7 +495,8 @@ mk_status mk_grouped_gemm_dgrad(const void *dy, int32_t rows, const int32_t *exp
 /* Gradient of mk_grouped_gemm for the experts' weights:
  *   dw[e, n, i] (+)= sum over e's rows r of dy[r, n] * a[t(r), i],  fp32 accumulation,
  * t(r) = r, or row_token[r] where the product read its rows in place
- * (mk_dispatch_gemm: a is then the token matrix).  An expert without rows gets
+ * (mk_dispatch_gemm of one source: a is then its token matrix; sources in buffers
+ * of their own have to be put into one first).  An expert without rows gets
  * zeros.  The sum's order is fixed.
  *   dy [rows, N] bf16     expert_offsets as for mk_grouped_gemm_dgrad
  *   row_token NULL, or [rows] int32; a is then [a_rows, K], and a value outside
@@ -537,7 +538,7 @@ mk_status mk_swiglu_i8(const void *gate_up, int32_t rows, int32_t F, const int32
  * scaled by w_scale, then by a_scale.  A plain product is E_local = 1.
  *   a [rows, K] int8 and a_scale [rows] fp32 (row_token NULL; a_rows is ignored),
  *     or [a_rows, K] and [a_rows] with row_token [rows] (a value outside
- *     [0, a_rows) gives a row of zeros)
+ *     [0, a_rows) reads a row of zeros with a scale of 0)
  *   expert_offsets as for mk_grouped_gemm_dgrad
  *   w [E_local, N, K] int8 (K contiguous)     w_scale [E_local, N] fp32
  *   y [rows, N] bf16 (out; rows >= offsets[E_local] untouched)

@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kLayoutThreads) void k_layout_slots(LayoutArgs a)
     __shared__ int32_t next[kGroupedMaxE];                        // next slot of every expert
     __shared__ int32_t scan[kGroupedMaxE];
     __shared__ uint8_t wcnt[kLayoutWaves][kGroupedMaxE];          // choices of each wave's 64 by expert (at most 64)
-    const int ti = (int)threadIdx.x, lane = ti % kWave, wave = ti / kWave;
+    const int ti = (int)threadIdx.x, wave = ti / kWave;
     const int chunk = (int)blockIdx.x;
     const int64_t i0 = (int64_t)chunk * a.chunk, end = min(i0 + a.chunk, (int64_t)a.n);
     // totals and what earlier chunks hold of expert ti

@@ -170,7 +170,7 @@ constexpr int kTallCost = 97, kTallCost2 = 56, kTallCost4 = 37, kTallCost8 = 25;
 //     128 x 128 or 128 x 64 where the workgroups suffice for all of the parts: a round of parts is shorter.  Or all are 128
 //     wide, where that takes less.  Measured (us, the last round whole / halves / quarters / eighths): 528 tiles, 14336
 //     deep: 985 / 945 / 855 / 843, 8-bit 542 / 503 / 458 / 452; 32 tiles, 4096 deep: 85 / 63 / 39 / 27, 8-bit 49 / 37 /
-//     24 / 17.  (All of 8 x 1024 rows, 4096 x 14336, 256 / 128 wide: 806 / 1047, 8-bit 457 / 555.)
+//     24 / 17.  (All of 8 x 1024 rows, 4096 x 14336, 256 / 128 wide: 752 / 1038, 8-bit 449 / 547.)
 //   - The short ones read the weights for few rows.  A round of tiles 64, 128 and 256 wide takes about 5 : 8 : 15 (narrow
 //     ones read the weights in shorter segments and the rows more often); the width is the one with the least.  Measured
 //     (us, 64 / 128 / 256 wide): 64 experts x 20 rows, 2048 x 2816: 164 / 137 / 128, 8-bit 100 / 74 / 71; 64 x 100 rows,
@@ -352,7 +352,7 @@ __device__ __forceinline__ int wgrad_tiles(const GroupedArgs &a, const GroupedTa
 }  // namespace
 
 // da = dy W.  Bound by the matrix cores once an expert has some 200 rows, below by reading the weights.  8 x 1024 rows, N =
-// 14336, K = 4096: 751 us (1281 TFLOP/s); 64 x 20 rows, N = 2048, K = 2816 (738 MB of weights): 129 us (5.7 TB/s).
+// 14336, K = 4096: 752 us (1279 TFLOP/s); 64 x 20 rows, N = 2048, K = 2816 (738 MB of weights): 129 us (5.7 TB/s).
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_dgrad(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(1024))) char stages[kGroupedStages];
@@ -363,8 +363,8 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_dgrad(GroupedArg
 }
 
 // The 8-bit product.  Few rows (512 at most, and hardly more than 16 to an expert: few_width) are a stream of the weights,
-// else tiles.  Measured (us, stream / tiles): 8 experts of 4096 x 14336 (470 MB): 1 row each 68 / 103, 16 rows 74 / 109, 24 rows
-// (two passes over the weights) 136 / 112.  68 us is 6.9 TB/s.  Tiles are bound by the matrix cores: 8 x 1024 rows, K = 4096, N = 14336: 440 us (2190 TOP/s).
+// else tiles.  Measured (us, stream / tiles): 8 experts of 4096 x 14336 (470 MB): 1 row each 73 / 110, 16 rows 77 / 111, 24 rows
+// (two passes over the weights) 140 / 111.  73 us is 6.4 TB/s (68, 6.9 TB/s, on another card).  Tiles are bound by the matrix cores: 8 x 1024 rows, K = 4096, N = 14336: 449 us (2140 TOP/s).
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(1024))) union {
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a
 }
 
 // The weights' gradient.  Bound by the matrix cores and, with few rows an expert, by writing dW: 8 x 1024 rows, K = 4096, N =
-// 14336: bf16 853 us (1128 TFLOP/s), fp32 977, accumulating 1132, with a gather too 1220; 64 x 768 rows, K = 2048, N = 1408, fp32
+// 14336: bf16 848 us (1134 TFLOP/s), fp32 986, accumulating 1143, with a gather too 1244; 64 x 768 rows, K = 2048, N = 1408, fp32
 // accumulating (738 MB read and written): 411 us.
 // Measured and not taken: every task to the workgroup with the least work so far (64 experts by Zipf's law: the longest share is
 // 4% over the mean instead of 25%, but the call takes as long, and 5% longer with equal experts: it parts the tasks

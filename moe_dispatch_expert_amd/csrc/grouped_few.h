@@ -7,7 +7,7 @@
 // whole numbers, so the waves add theirs up in LDS with atomics, in any order, to the same result; one barrier a task, two
 // buffers in turn.  What a task needs besides the stream lies in LDS: rows' tokens and scales from the start, its
 // columns' scales loaded with its first slab.
-// Bound by memory: 8 experts of 4096 x 14336 (470 MB), 1 row each: 68 us, 6.9 TB/s; one such matrix and one
+// Bound by memory: 8 experts of 4096 x 14336 (470 MB), 1 row each: 68 to 73 us, 6.4 to 6.9 TB/s; one such matrix and one
 // row: 13 us, of which the launch, the tables and the first loads' way are 5.
 #pragma once
 

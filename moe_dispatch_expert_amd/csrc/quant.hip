@@ -12,7 +12,7 @@
 //   - silu(g) = g / (1 + e^-g) with e^-g = 2^(-g c) e^(-g c'), c = log2(e) to 15 bits: g has 8 bits, so the product g c is exact, and
 //     the second factor is 1 - g c' to within 2^-23 (|g| < 88; above, the result is g u).  Gates below -80 take a longer way that
 //     keeps e^g's exponent apart (a wave without one skips it): h = g e^g u may be an ordinary number there.
-// 49152 rows of 1408 from gate|up: 59 us, 5.9 TB/s (128 with expf, divisions and a workgroup a row); 8192 rows of 2048: 11 us.
+// 49152 rows of 1408 from gate|up: 60 us, 5.8 TB/s (128 with expf, divisions and a workgroup a row); 8192 rows of 2048: 11 us.
 #include <hip/hip_runtime.h>
 
 #include "far_gate.h"
