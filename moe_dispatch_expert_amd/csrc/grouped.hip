@@ -364,7 +364,8 @@ __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_dgrad(GroupedArg
 
 // The 8-bit product.  Few rows (512 at most, and hardly more than 16 to an expert: few_width) are a stream of the weights,
 // else tiles.  Measured (us, stream / tiles): 8 experts of 4096 x 14336 (470 MB): 1 row each 73 / 110, 16 rows 77 / 111, 24 rows
-// (two passes over the weights) 140 / 111.  73 us is 6.4 TB/s (68, 6.9 TB/s, on another card).  Tiles are bound by the matrix cores: 8 x 1024 rows, K = 4096, N = 14336: 449 us (2140 TOP/s).
+// (two passes over the weights) 140 / 111.  73 us is 6.4 TB/s (68, 6.9 TB/s, on another card).
+// Tiles are bound by the matrix cores: 8 x 1024 rows, K = 4096, N = 14336: 449 us (2140 TOP/s).
 __global__ __launch_bounds__(kGroupedThreads, 1) void k_grouped_i8(GroupedArgs a)
 {
     __shared__ __attribute__((aligned(1024))) union {
